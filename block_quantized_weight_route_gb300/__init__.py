@@ -93,6 +93,16 @@ def lib() -> ctypes.CDLL:
         L.qmm_q8_0_q8_1_workspace_size.argtypes = [i32, i32, i32]
         L.qmm_q8_0_q8_1.restype = i32
         L.qmm_q8_0_q8_1.argtypes = [P, P, i32, i32, i32, P, P, P, P, P, P, P, sz, P]
+        f32, i64 = ctypes.c_float, ctypes.c_int64
+        norm = [P, i32, i64, P, i64, P, i64, i32, P, i32, f32, i32, i32]
+        L.qmm_add_rmsnorm_fp8.restype = i32
+        L.qmm_add_rmsnorm_fp8.argtypes = norm + [P, P, P, P]
+        L.qmm_add_rmsnorm_q8_1.restype = i32
+        L.qmm_add_rmsnorm_q8_1.argtypes = norm + [P, P, P, P, P]
+        L.qmm_fp8a8_blk128.restype = i32
+        L.qmm_fp8a8_blk128.argtypes = [P, P, i32, i32, i32, P, P, P, i32, P]
+        L.qmm_fp8a8_swiglu_blk128.restype = i32
+        L.qmm_fp8a8_swiglu_blk128.argtypes = [P, P, i32, i32, i32, P, P, P, P, P]
         L.qmm_dbg_wait_timeout.restype = i32
         L.qmm_dbg_wait_timeout.argtypes = [ctypes.c_uint, P]
         _lib = L
@@ -215,6 +225,126 @@ def qmm_q8_0_q8_1(Xq, Xd, Wq, Wd, ws=None, fp32_out: bool = False) -> dict:
     _check("qmm_q8_0_q8_1", lib().qmm_q8_0_q8_1(_ptr(Xq), _ptr(Xd), M, K, N, _ptr(Wq), _ptr(Wd), _ptr(Yq), _ptr(Yd),
                                                 _ptr(Ys), _ptr(Y), _ptr(ws), ws.numel(), _stream(dev)))
     return dict(Yq=Yq, Yd=Yd, Ys=Ys, Y=Y)
+
+
+_DTYPE = {torch.float32: 0, torch.bfloat16: 1}
+_F8 = (torch.float8_e4m3fn, torch.uint8, torch.int8)
+
+
+def _need_rows(t: torch.Tensor, name: str, shape=None) -> torch.Tensor:
+    """A CUDA matrix in fp32 or bf16 whose rows are contiguous (any row pitch)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DTYPE:
+        raise TypeError(f"{name} must have dtype in {tuple(_DTYPE)}, got {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a matrix with contiguous rows")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t
+
+
+def _pitch(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _norm_args(X, G, R, eps, Rout, Y, bf16_out):
+    """Checked arguments that the two norms share: (T, D, Rout, Y, the call's first 13 arguments)."""
+    _need_rows(X, "X")
+    T, D = X.shape
+    _need(G, "G", tuple(_DTYPE), (D,))
+    if R is None:
+        if Rout is not None:
+            raise ValueError("Rout without R")
+        res = (None, 0, None, 0, 0)
+    else:
+        _need_rows(R, "R", (T, D))
+        if Rout is None:
+            Rout = torch.empty((T, D), dtype=R.dtype, device=X.device)
+        _need_rows(Rout, "Rout", (T, D))
+        if Rout.dtype != R.dtype:
+            raise TypeError("Rout must have R's dtype")
+        res = (R.data_ptr(), _pitch(R), Rout.data_ptr(), _pitch(Rout), _DTYPE[R.dtype])
+    if Y is None and bf16_out:
+        Y = torch.empty((T, D), dtype=torch.bfloat16, device=X.device)
+    if Y is not None:
+        _need(Y, "Y", _BF16, (T, D))
+    args = (X.data_ptr(), _DTYPE[X.dtype], _pitch(X), *res, G.data_ptr(), _DTYPE[G.dtype], float(eps), T, D)
+    return T, D, Rout, Y, args
+
+
+def qmm_add_rmsnorm_fp8(X, G, R=None, eps: float = 1e-6, Rout=None, Q=None, S=None, Y=None,
+                        bf16_out: bool = False) -> dict:
+    """RMS norm of X [T, D], or of the stored sum Rout = X + R, times G [D], as E4M3
+    codes Q [T, D] with one fp32 scale per 128 columns S [T, ceil(D/128)].  X, R and
+    G are fp32 or bf16; X, R and Rout may be row slices.  Rout=R adds in place.
+    bf16_out (or Y given): the normalised rows in bf16 too.  Returns Q, S, R
+    (Rout, or None) and Y (or None)."""
+    T, D, Rout, Y, args = _norm_args(X, G, R, eps, Rout, Y, bf16_out)
+    if Q is None:
+        Q = torch.empty((T, D), dtype=torch.float8_e4m3fn, device=X.device)
+    _need(Q, "Q", _F8, (T, D))
+    if S is None:
+        S = torch.empty((T, (D + 127) // 128), dtype=torch.float32, device=X.device)
+    _need(S, "S", (torch.float32,), (T, (D + 127) // 128))
+    _check("qmm_add_rmsnorm_fp8", lib().qmm_add_rmsnorm_fp8(*args, Q.data_ptr(), S.data_ptr(),
+                                                            None if Y is None else Y.data_ptr(), _stream(X.device)))
+    return dict(Q=Q, S=S, R=Rout, Y=Y)
+
+
+def qmm_add_rmsnorm_q8_1(X, G, R=None, eps: float = 1e-6, Rout=None, Y=None, bf16_out: bool = False) -> dict:
+    """qmm_add_rmsnorm_fp8 with the rows as q8_1 blocks of 32 (what qmm_q8_0_q8_1
+    takes): Yq int8 [T, D], Yd / Ys fp16 bits [T, D/32], R and Y as there."""
+    T, D, Rout, Y, args = _norm_args(X, G, R, eps, Rout, Y, bf16_out)
+    Yq = torch.empty((T, D), dtype=torch.int8, device=X.device)
+    Yd = torch.empty((T, D // 32), dtype=torch.int16, device=X.device)
+    Ys = torch.empty((T, D // 32), dtype=torch.int16, device=X.device)
+    _check("qmm_add_rmsnorm_q8_1", lib().qmm_add_rmsnorm_q8_1(*args, Yq.data_ptr(), Yd.data_ptr(), Ys.data_ptr(),
+                                                              None if Y is None else Y.data_ptr(), _stream(X.device)))
+    return dict(Yq=Yq, Yd=Yd, Ys=Ys, R=Rout, Y=Y)
+
+
+def qmm_fp8a8_blk128(Xq, Xs, W, S, out_dtype=torch.bfloat16, Y=None):
+    """Y[M,N] = sum over 128-K blocks of Xs[m, kb] * S[n/128, kb] * e4m3(Xq) . e4m3(W)^T.
+    Xq [M, K] and W [N, K] E4M3, Xs [M, ceil(K/128)] and S [ceil(N/128), ceil(K/128)] fp32."""
+    M, K = Xq.shape
+    N = W.shape[0]
+    kb = (K + 127) // 128
+    _need(Xq, "Xq", _F8, (M, K))
+    _need(Xs, "Xs", (torch.float32,), (M, kb))
+    _need(W, "W", _F8, (N, K))
+    _need(S, "S", (torch.float32,), ((N + 127) // 128, kb))
+    if out_dtype not in _DTYPE:
+        raise TypeError("out_dtype must be float32 or bfloat16")
+    if Y is None:
+        Y = torch.empty((M, N), dtype=out_dtype, device=Xq.device)
+    _need(Y, "Y", (out_dtype,), (M, N))
+    _check("qmm_fp8a8_blk128", lib().qmm_fp8a8_blk128(Xq.data_ptr(), Xs.data_ptr(), M, K, N, W.data_ptr(), S.data_ptr(),
+                                                      Y.data_ptr(), _DTYPE[out_dtype], _stream(Xq.device)))
+    return Y
+
+
+def qmm_fp8a8_swiglu_blk128(Xq, Xs, Wgu, Sgu, Hq=None, Hs=None):
+    """H = silu(X . Wg^T) * (X . Wu^T) as E4M3 codes Hq [M, F] with one fp32 scale per
+    128 columns Hs [M, F/128].  Xq, Xs as in qmm_fp8a8_blk128; Wgu [2F, K] E4M3 (gate
+    rows first), Sgu [2F/128, ceil(K/128)] fp32."""
+    M, K = Xq.shape
+    F = Wgu.shape[0] // 2
+    kb = (K + 127) // 128
+    _need(Xq, "Xq", _F8, (M, K))
+    _need(Xs, "Xs", (torch.float32,), (M, kb))
+    _need(Wgu, "Wgu", _F8, (2 * F, K))
+    _need(Sgu, "Sgu", (torch.float32,), (2 * F // 128, kb))
+    if Hq is None:
+        Hq = torch.empty((M, F), dtype=torch.float8_e4m3fn, device=Xq.device)
+    _need(Hq, "Hq", _F8, (M, F))
+    if Hs is None:
+        Hs = torch.empty((M, F // 128), dtype=torch.float32, device=Xq.device)
+    _need(Hs, "Hs", (torch.float32,), (M, F // 128))
+    _check("qmm_fp8a8_swiglu_blk128", lib().qmm_fp8a8_swiglu_blk128(Xq.data_ptr(), Xs.data_ptr(), M, K, F,
+                                                                    Wgu.data_ptr(), Sgu.data_ptr(), Hq.data_ptr(),
+                                                                    Hs.data_ptr(), _stream(Xq.device)))
+    return Hq, Hs
 
 
 def moe_route_workspace_size(T: int, E: int, k: int) -> int:

@@ -851,6 +851,122 @@ qmm_status qmm_dbg_wait_timeout(unsigned timeout_us, cudaStream_t stream) {
     return e == cudaSuccess ? QMM_OK : cuda_fail(e, "qmm_dbg_wait_timeout launch");
 }
 
+// ---------------------------------------------------------------- norm with an 8-bit output
+
+static bool is_dtype(qmm_dtype t) { return t == QMM_F32 || t == QMM_BF16; }
+
+static qmm_status add_rmsnorm(const char* who, bool q81, const void* X, qmm_dtype xdt, int64_t ldx, const void* R,
+                              int64_t ldr, void* Rout, int64_t ldro, qmm_dtype rdt, const void* G, qmm_dtype gdt,
+                              float eps, int T, int D, void* Q, float* S, uint16_t* Yd, uint16_t* Ys, uint16_t* Y,
+                              cudaStream_t stream) {
+    const int unit = q81 ? 32 : 16;
+    if (T < 0 || D < unit || D % unit || D > rmsnorm8_max_width())
+        return fail(QMM_ERR_UNSUPPORTED_SHAPE, "%s: need T >= 0, D %% %d == 0, D <= %d (T=%d D=%d)", who, unit,
+                    rmsnorm8_max_width(), T, D);
+    if (!is_dtype(xdt) || !is_dtype(gdt) || (R && !is_dtype(rdt))) return fail(QMM_ERR_INVALID_ARG, "%s: bad type", who);
+    if (!(eps >= 0.0f)) return fail(QMM_ERR_INVALID_ARG, "%s: eps must not be negative", who);
+    if ((R == nullptr) != (Rout == nullptr))
+        return fail(QMM_ERR_INVALID_ARG, "%s: R and Rout come together", who);
+    if (!G || (T > 0 && (!X || !Q || (q81 ? (!Yd || !Ys) : !S)))) return fail(QMM_ERR_INVALID_ARG, "%s: null pointer", who);
+    if (ldx < D || ldx % 8 || (R && (ldr < D || ldr % 8 || ldro < D || ldro % 8)))
+        return fail(QMM_ERR_INVALID_ARG, "%s: row pitches must be at least D and multiples of 8", who);
+    if (!aligned16(X) || !aligned16(R) || !aligned16(Rout) || !aligned16(G) || !aligned16(Q) || !aligned16(S) ||
+        !aligned16(Yd) || !aligned16(Ys) || !aligned16(Y))
+        return fail(QMM_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned", who);
+    DeviceState* d = nullptr;
+    qmm_status st = device_state(&d);
+    if (st != QMM_OK || T == 0) return st;
+    NormParams p{};
+    p.X = X;
+    p.R = R;
+    p.Rout = Rout;
+    p.G = G;
+    p.ldx = (long)ldx;
+    p.ldr = (long)ldr;
+    p.ldro = (long)ldro;
+    p.x_bf16 = xdt == QMM_BF16;
+    p.r_bf16 = rdt == QMM_BF16;
+    p.g_bf16 = gdt == QMM_BF16;
+    p.eps = eps;
+    p.T = T;
+    p.D = D;
+    p.Q = static_cast<uint8_t*>(Q);
+    p.S = S;
+    p.Yd = reinterpret_cast<__half*>(Yd);
+    p.Ys = reinterpret_cast<__half*>(Ys);
+    p.Y = Y;
+    cudaError_t e = launch_rmsnorm8(p, q81, stream);
+    return e == cudaSuccess ? QMM_OK : cuda_fail(e, who);
+}
+
+qmm_status qmm_add_rmsnorm_fp8(const void* X, qmm_dtype xdt, int64_t ldx, const void* R, int64_t ldr, void* Rout,
+                               int64_t ldro, qmm_dtype rdt, const void* G, qmm_dtype gdt, float eps, int T, int D,
+                               uint8_t* Q, float* S, uint16_t* Y, cudaStream_t stream) {
+    return add_rmsnorm("qmm_add_rmsnorm_fp8", false, X, xdt, ldx, R, ldr, Rout, ldro, rdt, G, gdt, eps, T, D, Q, S,
+                       nullptr, nullptr, Y, stream);
+}
+
+qmm_status qmm_add_rmsnorm_q8_1(const void* X, qmm_dtype xdt, int64_t ldx, const void* R, int64_t ldr, void* Rout,
+                                int64_t ldro, qmm_dtype rdt, const void* G, qmm_dtype gdt, float eps, int T, int D,
+                                int8_t* Yq, uint16_t* Yd, uint16_t* Ys, uint16_t* Y, cudaStream_t stream) {
+    return add_rmsnorm("qmm_add_rmsnorm_q8_1", true, X, xdt, ldx, R, ldr, Rout, ldro, rdt, G, gdt, eps, T, D, Yq,
+                       nullptr, Yd, Ys, Y, stream);
+}
+
+// ---------------------------------------------------------------- FP8 x FP8 products
+
+qmm_status qmm_fp8a8_blk128(const uint8_t* Xq, const float* Xs, int M, int K, int N, const uint8_t* W, const float* S,
+                            void* Y, qmm_dtype ydt, cudaStream_t stream) {
+    if (M < 0 || K < 16 || K % 16 || N < 1)
+        return fail(QMM_ERR_UNSUPPORTED_SHAPE, "qmm_fp8a8_blk128: need M >= 0, K %% 16 == 0, N >= 1 (M=%d K=%d N=%d)", M,
+                    K, N);
+    if (!is_dtype(ydt)) return fail(QMM_ERR_INVALID_ARG, "qmm_fp8a8_blk128: bad output type");
+    if (!W || !S || (M > 0 && (!Xq || !Xs || !Y))) return fail(QMM_ERR_INVALID_ARG, "qmm_fp8a8_blk128: null pointer");
+    if (!aligned16(Xq) || !aligned16(Xs) || !aligned16(W) || !aligned16(S) || !aligned16(Y))
+        return fail(QMM_ERR_INVALID_ARG, "qmm_fp8a8_blk128: buffers must be 16-byte aligned");
+    DeviceState* d = nullptr;
+    qmm_status st = device_state(&d);
+    if (st != QMM_OK || M == 0) return st;
+    Fp8a8Params p{};
+    p.Xq = Xq;
+    p.Xs = Xs;
+    p.W = W;
+    p.S = S;
+    p.M = M;
+    p.K = K;
+    p.N = N;
+    p.Y = Y;
+    p.y_bf16 = ydt == QMM_BF16;
+    cudaError_t e = launch_fp8a8(p, false, stream);
+    return e == cudaSuccess ? QMM_OK : cuda_fail(e, "qmm_fp8a8_blk128 launch");
+}
+
+qmm_status qmm_fp8a8_swiglu_blk128(const uint8_t* Xq, const float* Xs, int M, int K, int F, const uint8_t* Wgu,
+                                   const float* Sgu, uint8_t* Hq, float* Hs, cudaStream_t stream) {
+    if (M < 0 || K < 16 || K % 16 || F < 128 || F % 128)
+        return fail(QMM_ERR_UNSUPPORTED_SHAPE,
+                    "qmm_fp8a8_swiglu_blk128: need M >= 0, K %% 16 == 0, F %% 128 == 0 (M=%d K=%d F=%d)", M, K, F);
+    if (!Wgu || !Sgu || (M > 0 && (!Xq || !Xs || !Hq || !Hs)))
+        return fail(QMM_ERR_INVALID_ARG, "qmm_fp8a8_swiglu_blk128: null pointer");
+    if (!aligned16(Xq) || !aligned16(Xs) || !aligned16(Wgu) || !aligned16(Sgu) || !aligned16(Hq) || !aligned16(Hs))
+        return fail(QMM_ERR_INVALID_ARG, "qmm_fp8a8_swiglu_blk128: buffers must be 16-byte aligned");
+    DeviceState* d = nullptr;
+    qmm_status st = device_state(&d);
+    if (st != QMM_OK || M == 0) return st;
+    Fp8a8Params p{};
+    p.Xq = Xq;
+    p.Xs = Xs;
+    p.W = Wgu;
+    p.S = Sgu;
+    p.M = M;
+    p.K = K;
+    p.N = F;
+    p.Hq = Hq;
+    p.Hs = Hs;
+    cudaError_t e = launch_fp8a8(p, true, stream);
+    return e == cudaSuccess ? QMM_OK : cuda_fail(e, "qmm_fp8a8_swiglu_blk128 launch");
+}
+
 qmm_status qmm_profile_enable(int on) {
     DeviceState* d = nullptr;
     qmm_status st = device_state(&d);

@@ -118,6 +118,38 @@ cudaError_t launch_wait_timeout_probe(uint32_t* err, uint64_t limit_ns, cudaStre
 cudaError_t launch_combine(const float* Yslot, int P, const int32_t* row, const float* w, int T, int k, int D,
                            float* Y, uint32_t* err, cudaStream_t s);
 
+// Residual addition + RMS norm + 8-bit output (rmsnorm8.cu).
+struct NormParams {
+    const void* X;       // [T][ldx] f32 or bf16
+    const void* R;       // [T][ldr] residual, or null
+    void* Rout;          // [T][ldro] the sum in the residual's type
+    const void* G;       // [D]
+    long ldx, ldr, ldro; // row pitches in elements
+    int x_bf16, r_bf16, g_bf16;
+    float eps;
+    int T, D;
+    uint8_t* Q;          // [T][D] codes: E4M3, or q8_1's int8
+    float* S;            // [T][ceil(D/128)] E4M3 scales
+    __half *Yd, *Ys;     // [T][D/32] q8_1's d and d * sum
+    uint16_t* Y;         // [T][D] bf16 rows, or null
+};
+int rmsnorm8_max_width();
+cudaError_t launch_rmsnorm8(const NormParams& p, bool q81, cudaStream_t s);
+
+// FP8 x FP8 products with block scales (gemm_fp8a8.cu).
+struct Fp8a8Params {
+    const uint8_t* Xq;   // [M][K] E4M3
+    const float* Xs;     // [M][ceil(K/128)]
+    const uint8_t* W;    // [N][K] E4M3; gated: [2N][K], gate rows first
+    const float* S;      // [ceil(rows/128)][ceil(K/128)]
+    int M, K, N;         // gated: N = F
+    void* Y;             // [M][N]
+    int y_bf16;
+    uint8_t* Hq;         // gated: [M][F] E4M3
+    float* Hs;           // gated: [M][F/128]
+};
+cudaError_t launch_fp8a8(const Fp8a8Params& p, bool gated, cudaStream_t s);
+
 // Set the calling thread's message returned by qmm_last_error().
 void set_last_error(const char* msg);
 }  // namespace qmm

@@ -132,6 +132,56 @@ qmm_status qmm_q8_0_q8_1(const int8_t *Xq, const uint16_t *Xd, int M, int K, int
                          size_t ws_bytes, cudaStream_t stream);
 
 /*
+ * qmm_add_rmsnorm_fp8 / qmm_add_rmsnorm_q8_1 -- the residual's addition, an RMS
+ * norm, and the normalised rows in 8 bits, the activation operand of the
+ * products that follow (qmm_fp8a8_blk128, qmm_fp8a8_swiglu_blk128; qmm_q8_0_q8_1):
+ *   v = X[t], or (R given) Rout[t] = X[t] + R[t] rounded to R's type, and v that
+ *   stored sum;   y = v / sqrt(mean(v^2) + eps) * G;   then per row
+ *   _fp8:  per 128 columns (the last group D % 128 wide): S = max|y| / 448,
+ *          Q = E4M3(y / S), to nearest even;  Q [T][D], S [T][ceil(D/128)] fp32;
+ *   _q8_1: per 32 columns: d = max|y| / 127, Yq = round-half-away(y / d) in
+ *          [-127, 127], Yd = fp16(d), Ys = fp16(d * sum Yq);  Yq [T][D], Yd / Ys [T][D/32].
+ *   A group of zeros has scale 0 and codes 0; a NaN in a row makes its Q NaN.
+ *   Y (or NULL): the rows y as well, bf16 (RNE) [T][D], for a product that takes bf16.
+ *   X [T] rows of ldx elements, R / Rout (both NULL: no residual) of ldr / ldro,
+ *   G [D]; each fp32 or bf16 (rdt is the type of R and Rout).  Rout may be R (or
+ *   X, where type and pitch are equal): the sum in place.  fp32 arithmetic.
+ * Shapes: T >= 0, D % 16 == 0 (_q8_1: D % 32 == 0), D <= 16384; pitches at least D
+ * and multiples of 8.
+ */
+qmm_status qmm_add_rmsnorm_fp8(const void *X, qmm_dtype xdt, int64_t ldx, const void *R, int64_t ldr, void *Rout,
+                               int64_t ldro, qmm_dtype rdt, const void *G, qmm_dtype gdt, float eps, int T, int D,
+                               uint8_t *Q, float *S, uint16_t *Y, cudaStream_t stream);
+qmm_status qmm_add_rmsnorm_q8_1(const void *X, qmm_dtype xdt, int64_t ldx, const void *R, int64_t ldr, void *Rout,
+                                int64_t ldro, qmm_dtype rdt, const void *G, qmm_dtype gdt, float eps, int T, int D,
+                                int8_t *Yq, uint16_t *Yd, uint16_t *Ys, uint16_t *Y, cudaStream_t stream);
+
+/*
+ * qmm_fp8a8_blk128 -- product of FP8 activations and FP8 weights, for prompts and
+ * for single tokens:
+ *   Y[m,n] = sum_kb Xs[m][kb] * S[n/128][kb] * sum_{k in block kb} e4m3(Xq[m,k]) * e4m3(W[n,k])
+ *   Xq [M][K] OCP E4M3 bytes, Xs [M][ceil(K/128)] fp32 (as qmm_add_rmsnorm_fp8 writes them);
+ *   W [N][K] E4M3 bytes, S [ceil(N/128)][ceil(K/128)] fp32 (the weight format of
+ *   qmm_fp8_blk128; the last block of either dimension may be partly filled);
+ *   Y [M][N] fp32 (QMM_F32) or bf16 rounded to nearest even (QMM_BF16).
+ * Products exact, block sums and their scaled sum in fp32.
+ * Shapes: M >= 0, K % 16 == 0, N >= 1.
+ *
+ * qmm_fp8a8_swiglu_blk128 -- the first half of a gated feed-forward: gate and up
+ * products, SwiGLU and the rounding of H to FP8 in one kernel:
+ *   g[n], u[n] = rows n and F + n of Wgu as above;  h = g / (1 + exp(-g)) * u;
+ *   per token and 128 columns: Hs = max|h| / 448, Hq = E4M3(h / Hs)  (0 for a group of zeros)
+ *   Wgu [2F][K] E4M3 (gate rows first), Sgu [2F/128][ceil(K/128)] fp32;
+ *   Hq [M][F] E4M3 bytes, Hs [M][F/128] fp32: the activation operand of the down
+ *   product (qmm_fp8a8_blk128 with K = F).
+ * Shapes: M >= 0, K % 16 == 0, F % 128 == 0.
+ */
+qmm_status qmm_fp8a8_blk128(const uint8_t *Xq, const float *Xs, int M, int K, int N, const uint8_t *W, const float *S,
+                            void *Y, qmm_dtype ydt, cudaStream_t stream);
+qmm_status qmm_fp8a8_swiglu_blk128(const uint8_t *Xq, const float *Xs, int M, int K, int F, const uint8_t *Wgu,
+                                   const float *Sgu, uint8_t *Hq, float *Hs, cudaStream_t stream);
+
+/*
  * moe_route_permute -- top-k routing and per-expert grouping of T tokens.
  * For each token t: ids[t][0..k) are the k largest logits (descending; a tie
  * goes to the lower expert index) and w[t][j] = exp(l_j - l_max) / sum over the
