@@ -915,6 +915,26 @@ qmm_status qmm_add_rmsnorm_q8_1(const void* X, qmm_dtype xdt, int64_t ldx, const
 
 // ---------------------------------------------------------------- FP8 x FP8 products
 
+static qmm_status run_fp8a8(const char* who, DeviceState* d, Fp8a8Params& p, bool gated, cudaStream_t stream) {
+    const Fp8a8Plan pl = fp8a8_plan(p.M, p.K, p.N, gated, d->sms);
+    p.err = d->err;
+    cudaError_t e;
+    if (pl.x_rows) {
+        qmm_status st;
+        CUtensorMap tx, tw;
+        if ((st = make_tmap(&tx, p.Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, p.M, p.K, 128, pl.x_rows,
+                            CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK)
+            return st;
+        if ((st = make_tmap(&tw, p.W, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, (uint64_t)p.N * (gated ? 2 : 1), p.K, 128,
+                            pl.w_rows, CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK)
+            return st;
+        e = launch_fp8a8_pair(tx, tw, p, gated, pl.bn, d->sms, stream);
+    } else {
+        e = launch_fp8a8(p, gated, stream);
+    }
+    return e == cudaSuccess ? QMM_OK : cuda_fail(e, who);
+}
+
 qmm_status qmm_fp8a8_blk128(const uint8_t* Xq, const float* Xs, int M, int K, int N, const uint8_t* W, const float* S,
                             void* Y, qmm_dtype ydt, cudaStream_t stream) {
     if (M < 0 || K < 16 || K % 16 || N < 1)
@@ -937,8 +957,7 @@ qmm_status qmm_fp8a8_blk128(const uint8_t* Xq, const float* Xs, int M, int K, in
     p.N = N;
     p.Y = Y;
     p.y_bf16 = ydt == QMM_BF16;
-    cudaError_t e = launch_fp8a8(p, false, stream);
-    return e == cudaSuccess ? QMM_OK : cuda_fail(e, "qmm_fp8a8_blk128 launch");
+    return run_fp8a8("qmm_fp8a8_blk128 launch", d, p, false, stream);
 }
 
 qmm_status qmm_fp8a8_swiglu_blk128(const uint8_t* Xq, const float* Xs, int M, int K, int F, const uint8_t* Wgu,
@@ -963,8 +982,7 @@ qmm_status qmm_fp8a8_swiglu_blk128(const uint8_t* Xq, const float* Xs, int M, in
     p.N = F;
     p.Hq = Hq;
     p.Hs = Hs;
-    cudaError_t e = launch_fp8a8(p, true, stream);
-    return e == cudaSuccess ? QMM_OK : cuda_fail(e, "qmm_fp8a8_swiglu_blk128 launch");
+    return run_fp8a8("qmm_fp8a8_swiglu_blk128 launch", d, p, true, stream);
 }
 
 qmm_status qmm_profile_enable(int on) {

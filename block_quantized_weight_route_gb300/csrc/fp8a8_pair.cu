@@ -1,0 +1,421 @@
+// FP8 x FP8 products with block scales, prompt form (many tokens).
+//
+//   y[m][n] = sum_kb Xs[m][kb] S[n/128][kb] P_kb[m][n],   P_kb = sum_{k in kb} Xq[m][k] W[n][k]
+//   GATED: h = silu(y gate) * y up, rounded to E4M3 per 128 columns of a token
+//
+// Persistent CTA pairs (cta_group::2), each on one 256 x BN tile: the even CTA
+// issues M = 256, N = BN, K = 32 MMAs over both CTAs' shared memory, each CTA's
+// TMEM holds its 128 rows x BN columns of P_kb.  A block's sum cannot stay in the
+// tensor core (its scale differs by row and by block), so eight warps fold each
+// P_kb into fp32 running sums in registers, two TMEM buffers apart from the MMA.
+//   warp 0: TMA producer   warp 1: MMA issuer (even CTA)
+//   warps 2, 3: products of the two scales, four K blocks at a time, into a ring
+//   warps 4..11: fold; warp w reads TMEM lanes 32 (w % 4) .. +31 (a row per lane),
+//                columns of half (w - 4) / 4 of the tile
+#include "fp8a8.cuh"
+
+namespace qmm {
+namespace {
+
+template <int BN_, bool GATED_>
+struct PairCfg {
+    static constexpr int BN = BN_;
+    static constexpr bool GATED = GATED_;
+    static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / 2 * 128, STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int STAGES = 196608 / STAGE_BYTES;           // 192 KB of operands
+    static constexpr int NBUF = BN <= 128 ? 4 : 2, BUF_COLS = 512 / NBUF;
+    static constexpr int SC_SLOTS = 4, SC_KB = 4;                 // ring of scale products: slots of 4 K blocks
+    static constexpr int SC_FLOATS = SC_SLOTS * SC_KB * 2 * 128;
+    static constexpr int CHUNKS = BN / 64;                        // 32-column chunks per fold thread
+    static constexpr int THREADS = 384, REGS = 168, REGS_FOLD = 224, REGS_OTHER = 56;
+    static_assert(REGS_FOLD * 256 + REGS_OTHER * 128 == REGS * THREADS, "register shares = launch registers");
+    static constexpr int BARS = 2 * STAGES + 2 * NBUF + 2 * SC_SLOTS + 3;
+    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + SC_FLOATS * 4 + (GATED ? 4 * 128 * 4 : 0) + BARS * 8 + 64;
+    static_assert(SMEM <= 232448, "shared memory");
+    static_assert(!GATED || BN == 256, "gate/up: 128 + 128 columns");
+};
+
+struct PairTile {
+    int m0, n0;   // first row of this CTA, first column (gated: first h column)
+};
+
+template <class C>
+__device__ __forceinline__ PairTile pair_tile(const Fp8a8Params& p, int t, int crank) {
+    const int mt = t % p.m_tiles, nt = t / p.m_tiles;
+    PairTile r;
+    r.m0 = mt * 256 + crank * 128;
+    r.n0 = nt * (C::GATED ? 128 : C::BN);
+    return r;
+}
+
+// E4M3 codes of four values scaled by gs
+__device__ __forceinline__ uint32_t codes4(const GroupScale& gs, const float* h) {
+    return e4m3x4(gs(h[0]), gs(h[1]), gs(h[2]), gs(h[3]));
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
+    fp8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, Fp8a8Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* stage = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* sc = reinterpret_cast<float*>(stage + C::STAGES * C::STAGE_BYTES);   // [slot][kb][2][128]
+    float* rowmax = sc + C::SC_FLOATS;                                           // gated: [tile parity][half][128]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(rowmax + (C::GATED ? 4 * 128 : 0));
+    uint64_t* full = bars;                    // even CTA's: both CTAs' operands have landed
+    uint64_t* empty = full + C::STAGES;
+    uint64_t* acc_full = empty + C::STAGES;
+    uint64_t* acc_empty = acc_full + C::NBUF; // even CTA's: both CTAs' fold warps have read the buffer
+    uint64_t* sc_full = acc_empty + C::NBUF;
+    uint64_t* sc_empty = sc_full + C::SC_SLOTS;
+    uint64_t* drain = sc_empty + C::SC_SLOTS;
+    uint64_t* rm_full = drain + 1;            // gated: every fold warp's row maxima are in shared memory
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rm_full + 2);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < C::NBUF; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 16);
+        }
+        for (int i = 0; i < C::SC_SLOTS; ++i) {
+            mbar_init(&sc_full[i], 2);
+            mbar_init(&sc_empty[i], 8);
+        }
+        mbar_init(drain, 1);
+        mbar_init(&rm_full[0], 8);
+        mbar_init(&rm_full[1], 8);
+        *abort_flag = 0;
+        fence_mbarrier_init();
+    }
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmW);
+    }
+    if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // the peer's barriers are initialised before any copy or commit signals them
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int crank = (int)cluster_ctarank(), cid = (int)cluster_id_x(), ncl = (int)cluster_count_x();
+    const int tiles = p.m_tiles * p.n_tiles, kbs = (p.K + 127) / 128;
+
+    if (warp >= 4) {
+        setmaxnreg_inc<C::REGS_FOLD>();
+        // ------------------------------------------------------------ fold
+        const int q = warp & 3, hf = (warp - 4) >> 2, row = q * 32 + lane;
+        const uint32_t lane_addr = tmem_base + ((uint32_t)(q * 32) << 16);
+        int buf = 0, slot = 0, parity = 0;
+        uint32_t bph = 0, sph = 0, rph = 0;
+        bool ok = true;
+        for (int t = cid; t < tiles && ok; t += ncl, parity ^= 1) {
+            const PairTile ti = pair_tile<C>(p, t, crank);
+            // columns below `bound` belong to the first of the tile's two scale blocks
+            const int bound = C::BN == 192 ? 128 - (ti.n0 & 127) : 128;
+            uint64_t acc[C::CHUNKS][16];
+#pragma unroll
+            for (int c = 0; c < C::CHUNKS; ++c)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) acc[c][j] = 0;
+            for (int kb = 0; kb < kbs; ++kb) {
+                const int k4 = kb & (C::SC_KB - 1);
+                if (k4 == 0 && !mbar_wait(&sc_full[slot], sph, abort_flag, p.err, DEV_TIMEOUT_CONV)) {
+                    ok = false;
+                    break;
+                }
+                const float* scr = sc + ((slot * C::SC_KB + k4) * 2) * 128 + row;
+                float s[2];
+                s[0] = scr[0];
+                s[1] = C::BN > 128 ? scr[128] : 0.f;
+                if (!mbar_wait(&acc_full[buf], bph, abort_flag, p.err, DEV_TIMEOUT_ACC)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t a0 = lane_addr + (uint32_t)(buf * C::BUF_COLS);
+                uint32_t r[2][32];
+                tmem_ld32(a0 + chunk_col<C>(hf, 0), r[0]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < C::CHUNKS; ++c) {
+                    if (c + 1 < C::CHUNKS) {
+                        tmem_ld32(a0 + chunk_col<C>(hf, c + 1), r[(c + 1) & 1]);
+                    } else {
+                        // every column is in registers: the MMA may write the buffer again
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(&acc_empty[buf], 0);
+                    }
+                    const float sf = chunk_col<C>(hf, c) < bound ? s[0] : s[1];
+                    const uint64_t s2 = pack2(sf, sf);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        acc[c][j] = fma2(pack2u(r[c & 1][2 * j], r[c & 1][2 * j + 1]), s2, acc[c][j]);
+                    if (c + 1 < C::CHUNKS) tmem_ld_wait();
+                }
+                if (k4 == C::SC_KB - 1 || kb == kbs - 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sc_empty[slot]);
+                    if (++slot == C::SC_SLOTS) {
+                        slot = 0;
+                        sph ^= 1u;
+                    }
+                }
+                if (++buf == C::NBUF) {
+                    buf = 0;
+                    bph ^= 1u;
+                }
+            }
+            if (!ok) break;
+            const long grow = (long)ti.m0 + row;
+            if constexpr (!C::GATED) {
+                if (grow < p.M) {
+#pragma unroll
+                    for (int c = 0; c < C::CHUNKS; ++c) store_chunk(p, grow, ti.n0 + chunk_col<C>(hf, c), acc[c]);
+                }
+            } else {
+                float h[64];
+                float a = 0.f;
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float2 g = unpack2(acc[c][j]), u = unpack2(acc[c + 2][j]);
+                        h[c * 32 + 2 * j] = swiglu(g.x, u.x);
+                        h[c * 32 + 2 * j + 1] = swiglu(g.y, u.y);
+                        a = max_nan(a, max_nan(fabsf(h[c * 32 + 2 * j]), fabsf(h[c * 32 + 2 * j + 1])));
+                    }
+                rowmax[(parity * 2 + hf) * 128 + row] = a;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&rm_full[parity]);
+                if (!mbar_wait(&rm_full[parity], rph, abort_flag, p.err, DEV_TIMEOUT_ACC)) break;
+                rph ^= (uint32_t)parity;
+                a = max_nan(a, rowmax[(parity * 2 + (hf ^ 1)) * 128 + row]);
+                const float s = a / 448.0f;
+                const GroupScale gs = group_scale(s);
+                if (grow < p.M) {
+                    uint4* dst = reinterpret_cast<uint4*>(p.Hq + grow * p.N + ti.n0 + hf * 64);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        dst[j] = make_uint4(codes4(gs, h + 16 * j), codes4(gs, h + 16 * j + 4), codes4(gs, h + 16 * j + 8),
+                                            codes4(gs, h + 16 * j + 12));
+                    if (hf == 0) p.Hs[grow * (p.N / 128) + ti.n0 / 128] = s;
+                }
+            }
+        }
+    } else {
+        setmaxnreg_dec<C::REGS_OTHER>();
+        if (warp == 0) {
+            // ------------------------------------------------------------ producer
+            // Both CTAs' copies complete on the even CTA's barrier, which expects all of
+            // them; a stage is free again when the pair's MMA commit arrives in both CTAs.
+            int s = 0;
+            uint32_t ph = 0;
+            long issued = 0;
+            bool ok = true;
+            for (int t = cid; t < tiles && ok; t += ncl) {
+                const PairTile ti = pair_tile<C>(p, t, crank);
+                // this CTA's BN/2 weight rows (gated: the even CTA gate, the odd CTA up rows)
+                const int w0 = C::GATED ? ti.n0 + crank * p.N : ti.n0 + crank * (C::BN / 2);
+                for (int kb = 0; kb < kbs; ++kb) {
+                    const bool got = mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_TMA_EMPTY);
+                    if (__any_sync(0xffffffffu, !got)) {
+                        ok = false;
+                        break;
+                    }
+                    // one copy at a time executes per thread: each copy of a stage on its own lane
+                    const int l0 = (s * 2) & 31;
+                    if (crank == 0 && lane == l0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE_BYTES);
+                    __syncwarp();
+                    uint8_t* st = stage + s * C::STAGE_BYTES;
+                    if (lane == l0) tma_load_2d_pair(st, &tmX, &full[s], kb * 128, ti.m0);
+                    else if (lane == l0 + 1) tma_load_2d_pair(st + C::A_BYTES, &tmW, &full[s], kb * 128, w0);
+                    __syncwarp();
+                    ++issued;
+                    if (++s == C::STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            // Every copy must have landed before the CTAs leave: the even CTA's barriers
+            // count both CTAs' bytes.  After a time-out the odd CTA may have copies in
+            // flight that the even CTA never expected: they land within microseconds.
+            if (lane == 0 && crank == 0) drain_ring(full, issued, C::STAGES, p.err);
+            if (!ok && crank != 0) {
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 5000000ull) {
+                }
+            }
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ MMA issuer
+            if (lane == 0 && crank == 0) {
+                int s = 0, buf = 0;
+                uint32_t ph = 0, bph = 0;
+                bool ok = true;
+                for (int t = cid; t < tiles && ok; t += ncl) {
+                    for (int kb = 0; kb < kbs; ++kb) {
+                        if (!mbar_wait_cl(&acc_empty[buf], bph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_ACC_EMPTY) ||
+                            !mbar_wait_cl(&full[s], ph, abort_flag, p.err, DEV_TIMEOUT_TMA_FULL)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sa = smem_u32(stage + s * C::STAGE_BYTES);
+                        const uint64_t ad = smem_desc_sw128(sa), bd = smem_desc_sw128(sa + C::A_BYTES);
+                        const uint32_t d = tmem_base + (uint32_t)(buf * C::BUF_COLS);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)   // 32 codes (32 bytes) per MMA
+                            tc_mma_f8_pair(d, ad + (uint64_t)(k * 2), bd + (uint64_t)(k * 2), idesc_e4m3(256, C::BN), k > 0);
+                        tc_commit_pair(&acc_full[buf], 3);
+                        tc_commit_pair(&empty[s], 3);
+                        if (++buf == C::NBUF) {
+                            buf = 0;
+                            bph ^= 1u;
+                        }
+                        if (++s == C::STAGES) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                }
+                tc_commit_pair(drain, 1);
+                drain_ring(drain, 1, 1, p.err);
+            }
+            __syncwarp();
+        } else {
+            // ------------------------------------------------------------ scale products
+            // lane: rows 64 (warp - 2) + lane and + 32; the loads of the next four K blocks
+            // are in flight while these are multiplied and stored
+            const int r0 = (warp - 2) * 64 + lane;
+            int slot = 0;
+            uint32_t sph = 0;
+            bool ok = true;
+            float x[2][4], w[2][4];
+            int pt = cid, pk = 0;
+            PairTile pi = pair_tile<C>(p, pt, crank);
+            auto fetch = [&]() {
+                if (pt >= tiles) return;
+                const int b0 = C::GATED ? pi.n0 / 128 : pi.n0 / 128;
+                const int b1 = C::GATED ? (p.N + pi.n0) / 128 : b0 + 1;
+                const int nblk = C::GATED ? p.N / 64 : (p.N + 127) / 128;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const bool in = pk + k < kbs;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const long m = (long)pi.m0 + r0 + 32 * i;
+                        x[i][k] = (in && m < p.M) ? __ldg(p.Xs + m * kbs + pk + k) : 0.f;
+                    }
+                    w[0][k] = in ? __ldg(p.S + (long)b0 * kbs + pk + k) : 0.f;
+                    w[1][k] = (in && C::BN > 128 && b1 < nblk) ? __ldg(p.S + (long)b1 * kbs + pk + k) : 0.f;
+                }
+                pk += 4;
+                if (pk >= kbs) {
+                    pk = 0;
+                    pt += ncl;
+                    pi = pair_tile<C>(p, pt, crank);
+                }
+            };
+            fetch();
+            for (int t = cid; t < tiles && ok; t += ncl) {
+                for (int kb = 0; kb < kbs; kb += 4) {
+                    float y[2][2][4];   // [block][row][k]
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            y[0][i][k] = x[i][k] * w[0][k];
+                            y[1][i][k] = x[i][k] * w[1][k];
+                        }
+                    fetch();
+                    if (!mbar_wait(&sc_empty[slot], sph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_CONV_EMPTY)) {
+                        ok = false;
+                        break;
+                    }
+                    float* dst = sc + slot * C::SC_KB * 2 * 128 + r0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            dst[(k * 2) * 128 + 32 * i] = y[0][i][k];
+                            if (C::BN > 128) dst[(k * 2 + 1) * 128 + 32 * i] = y[1][i][k];
+                        }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sc_full[slot]);
+                    if (++slot == C::SC_SLOTS) {
+                        slot = 0;
+                        sph ^= 1u;
+                    }
+                }
+            }
+        }
+    }
+
+    __syncthreads();
+    cluster_sync();   // neither CTA leaves while the other's MMAs, copies or arrivals may reach it
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+template <class C>
+cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, int sms, cudaStream_t s) {
+    static int most[64] = {};   // pairs that fit the device at once
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (most[dev] == 0) {
+        e = cudaFuncSetAttribute(fp8a8_pair_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return e;
+        // the warpgroups' register shares add up to the launch's: launch only if the
+        // kernel is allocated exactly that many (a setmaxnreg.inc past the pool waits)
+        cudaFuncAttributes fa{};
+        e = cudaFuncGetAttributes(&fa, fp8a8_pair_kernel<C>);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs != C::REGS) return cudaErrorInvalidConfiguration;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.blockDim = dim3(C::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (most[dev] == 0) {
+        cfg.gridDim = dim3(2 * (sms / 2), 1, 1);
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, fp8a8_pair_kernel<C>, &cfg);
+        if (e != cudaSuccess) return e;
+        if (n < 1) return cudaErrorInvalidConfiguration;
+        most[dev] = n;
+    }
+    const long tiles = (long)p.m_tiles * p.n_tiles;
+    cfg.gridDim = dim3(2 * (unsigned)(tiles < most[dev] ? tiles : most[dev]), 1, 1);
+    return cudaLaunchKernelEx(&cfg, fp8a8_pair_kernel<C>, tx, tw, p);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8a8_pair(const CUtensorMap& tx, const CUtensorMap& tw, Fp8a8Params p, bool gated, int bn, int sms,
+                              cudaStream_t s) {
+    p.m_tiles = (p.M + 255) / 256;
+    p.n_tiles = gated ? p.N / 128 : (p.N + bn - 1) / bn;
+    if (gated) return launch<PairCfg<256, true>>(tx, tw, p, sms, s);
+    if (bn == 256) return launch<PairCfg<256, false>>(tx, tw, p, sms, s);
+    if (bn == 192) return launch<PairCfg<192, false>>(tx, tw, p, sms, s);
+    return launch<PairCfg<128, false>>(tx, tw, p, sms, s);
+}
+
+}  // namespace qmm

@@ -118,6 +118,31 @@ __global__ void __launch_bounds__(GATED ? 256 : 128) fp8a8_simple_kernel(Fp8a8Pa
 
 }  // namespace
 
+// Columns of a prompt tile: the width whose waves of pairs take least, counting a
+// wave as its width plus a fixed part for filling and draining the pipeline.
+Fp8a8Plan fp8a8_plan(int M, int K, int N, bool gated, int sms) {
+    (void)K;
+    Fp8a8Plan pl{};
+    if (M <= 64) return pl;
+    pl.pair = true;
+    pl.x_rows = 128;
+    pl.bn = 256;
+    if (!gated) {
+        const long pairs = sms / 2, mt = (M + 255) / 256;
+        double best = 1e30;
+        for (int bn : {256, 192, 128}) {
+            const long tiles = mt * ((N + bn - 1) / bn);
+            const double cost = (double)((tiles + pairs - 1) / pairs) * (bn + 16);
+            if (cost < best) {
+                best = cost;
+                pl.bn = bn;
+            }
+        }
+    }
+    pl.w_rows = pl.bn / 2;
+    return pl;
+}
+
 cudaError_t launch_fp8a8(const Fp8a8Params& p, bool gated, cudaStream_t s) {
     const dim3 grid((p.N + 127) / 128, (p.M + kTok - 1) / kTok);
     if (gated) fp8a8_simple_kernel<true><<<grid, 256, 0, s>>>(p);

@@ -147,8 +147,20 @@ struct Fp8a8Params {
     int y_bf16;
     uint8_t* Hq;         // gated: [M][F] E4M3
     float* Hs;           // gated: [M][F/128]
+    uint32_t* err;       // device error word
+    int m_tiles, n_tiles;
 };
+// Which kernel takes a product, and the rows of the TMA boxes (128 codes wide) it
+// reads the activations and the weights in (0 rows: the kernel without TMA).
+struct Fp8a8Plan {
+    bool pair;
+    int bn;              // columns of a tile
+    int x_rows, w_rows;
+};
+Fp8a8Plan fp8a8_plan(int M, int K, int N, bool gated, int sms);
 cudaError_t launch_fp8a8(const Fp8a8Params& p, bool gated, cudaStream_t s);
+cudaError_t launch_fp8a8_pair(const CUtensorMap& tx, const CUtensorMap& tw, Fp8a8Params p, bool gated, int bn, int sms,
+                              cudaStream_t s);
 
 // Set the calling thread's message returned by qmm_last_error().
 void set_last_error(const char* msg);
