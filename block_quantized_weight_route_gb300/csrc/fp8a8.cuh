@@ -23,6 +23,19 @@ __device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t a_desc,
         : "memory");
 }
 
+// Arrive once on the mbarrier at `bar`'s offset in the even CTA of the pair, after
+// this thread's TMEM reads (complete at tcgen05.wait::ld, ordered by
+// tcgen05.fence::before_thread_sync).  No shared or global memory is handed over,
+// so the release is at CTA scope: a cluster-scope release took about 1200 cycles
+// per hand-over (2048 x 5120 x 5120: 128 us with it, 70 us without).
+__device__ __forceinline__ void mbar_arrive_even(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .b32 ra;\n\t"
+        "mapa.shared::cluster.u32 ra, %0, 0;\n\t"
+        "mbarrier.arrive.shared::cluster.b64 _, [ra];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+
 // As tma_load_2d into this CTA's shared memory, completing on the mbarrier at
 // `bar`'s offset in the even CTA of the pair.
 __device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
@@ -79,55 +92,93 @@ __device__ __forceinline__ float swiglu(float g, float u) {
     return __fdividef(g < 0.0f ? g * t : g, 1.0f + t) * u;
 }
 
-// First column, inside the tile, of 32-column chunk c of a fold thread of half hf:
-// consecutive columns, or (gated) chunks 0, 1 gate and 2, 3 the same columns of up.
+// First column, inside the tile, of chunk c of a fold thread of column quarter cq:
+// consecutive columns, or (gated) chunk 0 gate and chunk 1 the same columns of up.
 template <class C>
-__device__ __forceinline__ int chunk_col(int hf, int c) {
-    if constexpr (C::GATED) return (c < 2 ? 0 : 128) + hf * 64 + (c & 1) * 32;
-    else return hf * (C::BN / 2) + c * 32;
+__device__ __forceinline__ int chunk_col(int cq, int c) {
+    if constexpr (C::GATED) return c * 128 + cq * 32;
+    else return cq * C::CW + c * C::LDW;
 }
 
-// 32 consecutive outputs of one row, as 16-byte vectors where the row pitch
-// allows, masked at the last column.
-__device__ __forceinline__ void store_chunk(const Fp8a8Params& p, long grow, int col, const uint64_t (&v)[16]) {
-    const long o = grow * p.N + col;
-    const bool whole = col + 32 <= p.N;
-    if (p.y_bf16) {
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.Y) + o;
-        if (whole && (p.N & 7) == 0) {
+// 4-byte asynchronous copy to shared memory, or a zero.
+__device__ __forceinline__ void cp_async4(void* smem_dst, const void* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(smem_dst)), "l"(src), "r"(in ? 4 : 0)
+                 : "memory");
+}
+// One of the arrivals `bar` was initialised with, when this thread's copies so far are complete.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// A warp's staged 32 rows x NC 16-byte chunks (chunk c of row r at c ^ stage_swz<NC>(r),
+// which leaves bank conflicts of two ways at most on both sides) to Y at (row0, col):
+// consecutive lanes write consecutive chunks of a row.
+template <int NC>
+__device__ __forceinline__ int stage_swz(int r) {
+    return NC == 4 ? (r >> 1) & 3 : (r >> 2) & 1;
+}
+template <int NC>
+__device__ __forceinline__ void flush_stage(const Fp8a8Params& p, const uint8_t* stg, int lane, long row0, int col, int esz) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t w[4];
+    for (int i = 0; i < NC; ++i) {
+        const int r = (i * 32 + lane) / NC, c = (i * 32 + lane) % NC;
+        const uint4 d = *reinterpret_cast<const uint4*>(stg + (r * NC + (c ^ stage_swz<NC>(r))) * 16);
+        const int cc = col + c * (16 / esz);
+        if (row0 + r < p.M && cc < p.N)
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.Y) + ((row0 + r) * p.N + cc) * esz) = d;
+    }
+}
+
+// A warp's 32 rows x W columns (lane = row, `v` its W consecutive outputs) to Y at
+// (row0, col), through the warp's 2 KB of staging so that a store instruction writes
+// whole runs of a few rows rather than 16 bytes of 32 rows; element by element where
+// the row pitch is not a multiple of 16 bytes.
+template <int W>
+__device__ __forceinline__ void store_chunk(const Fp8a8Params& p, uint8_t* stg, int lane, long row0, int col,
+                                            const uint64_t (&v)[W / 2]) {
+    const bool rows16 = (((long)p.N * (p.y_bf16 ? 2 : 4)) & 15) == 0;
+    if (rows16 && p.y_bf16) {
+        constexpr int NC = W / 8;
+        __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = unpack2(v[4 * j + i]);
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
-                    w[i] = *reinterpret_cast<const uint32_t*>(&b);
-                }
-                reinterpret_cast<uint4*>(dst)[j] = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int c = 0; c < NC; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack2(v[4 * c + i]);
+                const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+                w[i] = *reinterpret_cast<const uint32_t*>(&b);
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const float2 f = unpack2(v[j]);
-                if (col + 2 * j < p.N) dst[2 * j] = __float2bfloat16_rn(f.x);
-                if (col + 2 * j + 1 < p.N) dst[2 * j + 1] = __float2bfloat16_rn(f.y);
-            }
+            *reinterpret_cast<uint4*>(stg + (lane * NC + (c ^ stage_swz<NC>(lane))) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-    } else {
-        float* dst = static_cast<float*>(p.Y) + o;
-        if (whole && (p.N & 3) == 0) {
+        __syncwarp();
+        flush_stage<NC>(p, stg, lane, row0, col, 2);
+    } else if (rows16) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 a = unpack2(v[2 * j]), b = unpack2(v[2 * j + 1]);
-                reinterpret_cast<float4*>(dst)[j] = make_float4(a.x, a.y, b.x, b.y);
+        for (int h = 0; h < W / 16; ++h) {
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float2 a = unpack2(v[8 * h + 2 * c]), b = unpack2(v[8 * h + 2 * c + 1]);
+                *reinterpret_cast<float4*>(stg + (lane * 4 + (c ^ stage_swz<4>(lane))) * 16) = make_float4(a.x, a.y, b.x, b.y);
             }
-        } else {
+            __syncwarp();
+            flush_stage<4>(p, stg, lane, row0, col + 16 * h, 4);
+        }
+    } else if (row0 + lane < p.M) {
+        const long o = (row0 + lane) * p.N + col;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const float2 f = unpack2(v[j]);
-                if (col + 2 * j < p.N) dst[2 * j] = f.x;
-                if (col + 2 * j + 1 < p.N) dst[2 * j + 1] = f.y;
+        for (int j = 0; j < W / 2; ++j) {
+            const float2 f = unpack2(v[j]);
+            if (p.y_bf16) {
+                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.Y) + o + 2 * j;
+                if (col + 2 * j < p.N) dst[0] = __float2bfloat16_rn(f.x);
+                if (col + 2 * j + 1 < p.N) dst[1] = __float2bfloat16_rn(f.y);
+            } else {
+                float* dst = static_cast<float*>(p.Y) + o + 2 * j;
+                if (col + 2 * j < p.N) dst[0] = f.x;
+                if (col + 2 * j + 1 < p.N) dst[1] = f.y;
             }
         }
     }

@@ -9,9 +9,10 @@
 // tensor core (its scale differs by row and by block), so eight warps fold each
 // P_kb into fp32 running sums in registers, two TMEM buffers apart from the MMA.
 //   warp 0: TMA producer   warp 1: MMA issuer (even CTA)
-//   warps 2, 3: products of the two scales, four K blocks at a time, into a ring
-//   warps 4..11: fold; warp w reads TMEM lanes 32 (w % 4) .. +31 (a row per lane),
-//                columns of half (w - 4) / 4 of the tile
+//   warps 2, 3: the scales of four K blocks at a time, by asynchronous copies into a ring
+//   warps 4..19: fold; warp w reads TMEM lanes 32 (w % 4) .. +31 (a row per lane) and
+//                quarter (w - 4) / 4 of the columns.  Sixteen warps rather than eight: a
+//                TMEM load cannot be waited for on its own, so other warps hide it.
 #include "fp8a8.cuh"
 
 namespace qmm {
@@ -22,17 +23,22 @@ struct PairCfg {
     static constexpr int BN = BN_;
     static constexpr bool GATED = GATED_;
     static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / 2 * 128, STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES = 196608 / STAGE_BYTES;           // 192 KB of operands
+    static constexpr int STAGES = 163840 / STAGE_BYTES;           // 160 KB of operands
     static constexpr int NBUF = BN <= 128 ? 4 : 2, BUF_COLS = 512 / NBUF;
-    static constexpr int SC_SLOTS = 4, SC_KB = 4;                 // ring of scale products: slots of 4 K blocks
-    static constexpr int SC_FLOATS = SC_SLOTS * SC_KB * 2 * 128;
-    static constexpr int CHUNKS = BN / 64;                        // 32-column chunks per fold thread
-    static constexpr int THREADS = 384, REGS = 168, REGS_FOLD = 224, REGS_OTHER = 56;
-    static_assert(REGS_FOLD * 256 + REGS_OTHER * 128 == REGS * THREADS, "register shares = launch registers");
-    static constexpr int BARS = 2 * STAGES + 2 * NBUF + 2 * SC_SLOTS + 3;
-    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + SC_FLOATS * 4 + (GATED ? 4 * 128 * 4 : 0) + BARS * 8 + 64;
+    static constexpr int SC_SLOTS = 4, SC_KB = 4;                 // ring of scales: slots of 4 K blocks
+    static constexpr int SC_PITCH = 128 + 4;                      // per K block: the rows' scales, the two blocks'
+    static constexpr int SC_FLOATS = SC_SLOTS * SC_KB * SC_PITCH;
+    static constexpr int FOLD_WARPS = 16, CW = BN / 4;            // columns of a fold thread
+    static constexpr int LDW = CW % 32 ? 16 : 32, CHUNKS = CW / LDW;
+    static constexpr int LW = 16;                                 // columns of a TMEM load
+    static constexpr int OUT_BYTES = GATED ? 2 * 4 * 128 * 4 : FOLD_WARPS * 2048;   // row maxima, or output staging
+    static constexpr int THREADS = 128 + 32 * FOLD_WARPS, REGS = 96, REGS_FOLD = 104, REGS_OTHER = 64;
+    static_assert(REGS_FOLD * 32 * FOLD_WARPS + REGS_OTHER * 128 == REGS * THREADS, "register shares = launch registers");
+    static constexpr int BARS = 2 * STAGES + NBUF + 2 * SC_SLOTS + 3;
+    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + OUT_BYTES + SC_FLOATS * 4 + BARS * 8 + 64;
     static_assert(SMEM <= 232448, "shared memory");
     static_assert(!GATED || BN == 256, "gate/up: 128 + 128 columns");
+    static_assert(NBUF <= STAGES, "a stage's MMA barrier completes again only after its accumulator was read");
 };
 
 struct PairTile {
@@ -58,13 +64,13 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
     fp8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, Fp8a8Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stage = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* sc = reinterpret_cast<float*>(stage + C::STAGES * C::STAGE_BYTES);   // [slot][kb][2][128]
-    float* rowmax = sc + C::SC_FLOATS;                                           // gated: [tile parity][half][128]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(rowmax + (C::GATED ? 4 * 128 : 0));
-    uint64_t* full = bars;                    // even CTA's: both CTAs' operands have landed
-    uint64_t* empty = full + C::STAGES;
-    uint64_t* acc_full = empty + C::STAGES;
-    uint64_t* acc_empty = acc_full + C::NBUF; // even CTA's: both CTAs' fold warps have read the buffer
+    uint8_t* outs = stage + C::STAGES * C::STAGE_BYTES;         // output staging, 2 KB per fold warp
+    float* rowmax = reinterpret_cast<float*>(outs);              // gated: [tile parity][quarter][128]
+    float* sc = reinterpret_cast<float*>(outs + C::OUT_BYTES);   // [slot][kb][128 rows, 2 weight blocks]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sc + C::SC_FLOATS);
+    uint64_t* full = bars;                    // even CTA's: both CTAs' operands of a stage have landed
+    uint64_t* done = full + C::STAGES;        // a stage's MMAs are complete: its operands are free, its P is in TMEM
+    uint64_t* acc_empty = done + C::STAGES;   // even CTA's: both CTAs' fold warps have read the buffer
     uint64_t* sc_full = acc_empty + C::NBUF;
     uint64_t* sc_empty = sc_full + C::SC_SLOTS;
     uint64_t* drain = sc_empty + C::SC_SLOTS;
@@ -76,19 +82,16 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&done[i], 1);
         }
-        for (int i = 0; i < C::NBUF; ++i) {
-            mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 16);
-        }
+        for (int i = 0; i < C::NBUF; ++i) mbar_init(&acc_empty[i], 2 * C::FOLD_WARPS);
         for (int i = 0; i < C::SC_SLOTS; ++i) {
-            mbar_init(&sc_full[i], 2);
-            mbar_init(&sc_empty[i], 8);
+            mbar_init(&sc_full[i], 64);
+            mbar_init(&sc_empty[i], C::FOLD_WARPS);
         }
         mbar_init(drain, 1);
-        mbar_init(&rm_full[0], 8);
-        mbar_init(&rm_full[1], 8);
+        mbar_init(&rm_full[0], C::FOLD_WARPS);
+        mbar_init(&rm_full[1], C::FOLD_WARPS);
         *abort_flag = 0;
         fence_mbarrier_init();
     }
@@ -108,55 +111,56 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
     if (warp >= 4) {
         setmaxnreg_inc<C::REGS_FOLD>();
         // ------------------------------------------------------------ fold
-        const int q = warp & 3, hf = (warp - 4) >> 2, row = q * 32 + lane;
+        const int q = warp & 3, cq = (warp - 4) >> 2, row = q * 32 + lane;
         const uint32_t lane_addr = tmem_base + ((uint32_t)(q * 32) << 16);
-        int buf = 0, slot = 0, parity = 0;
-        uint32_t bph = 0, sph = 0, rph = 0;
+        int st = 0, buf = 0, slot = 0, parity = 0;
+        uint32_t ph = 0, sph = 0, rph = 0;
         bool ok = true;
         for (int t = cid; t < tiles && ok; t += ncl, parity ^= 1) {
             const PairTile ti = pair_tile<C>(p, t, crank);
-            // columns below `bound` belong to the first of the tile's two scale blocks
+            // columns below `bound` belong to the first of the tile's two weight blocks
             const int bound = C::BN == 192 ? 128 - (ti.n0 & 127) : 128;
-            uint64_t acc[C::CHUNKS][16];
+            uint64_t acc[C::CHUNKS][C::LDW / 2];
 #pragma unroll
             for (int c = 0; c < C::CHUNKS; ++c)
 #pragma unroll
-                for (int j = 0; j < 16; ++j) acc[c][j] = 0;
+                for (int j = 0; j < C::LDW / 2; ++j) acc[c][j] = 0;
             for (int kb = 0; kb < kbs; ++kb) {
                 const int k4 = kb & (C::SC_KB - 1);
                 if (k4 == 0 && !mbar_wait(&sc_full[slot], sph, abort_flag, p.err, DEV_TIMEOUT_CONV)) {
                     ok = false;
                     break;
                 }
-                const float* scr = sc + ((slot * C::SC_KB + k4) * 2) * 128 + row;
-                float s[2];
-                s[0] = scr[0];
-                s[1] = C::BN > 128 ? scr[128] : 0.f;
-                if (!mbar_wait(&acc_full[buf], bph, abort_flag, p.err, DEV_TIMEOUT_ACC)) {
+                const float* scr = sc + (slot * C::SC_KB + k4) * C::SC_PITCH;
+                const float sx = scr[row], s0 = sx * scr[128], s1 = C::BN > 128 ? sx * scr[129] : 0.f;
+                if (!mbar_wait(&done[st], ph, abort_flag, p.err, DEV_TIMEOUT_ACC)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t a0 = lane_addr + (uint32_t)(buf * C::BUF_COLS);
-                uint32_t r[2][32];
-                tmem_ld32(a0 + chunk_col<C>(hf, 0), r[0]);
-                tmem_ld_wait();
 #pragma unroll
                 for (int c = 0; c < C::CHUNKS; ++c) {
-                    if (c + 1 < C::CHUNKS) {
-                        tmem_ld32(a0 + chunk_col<C>(hf, c + 1), r[(c + 1) & 1]);
-                    } else {
-                        // every column is in registers: the MMA may write the buffer again
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(&acc_empty[buf], 0);
-                    }
-                    const float sf = chunk_col<C>(hf, c) < bound ? s[0] : s[1];
+                    const float sf = chunk_col<C>(cq, c) < bound ? s0 : s1;
                     const uint64_t s2 = pack2(sf, sf);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        acc[c][j] = fma2(pack2u(r[c & 1][2 * j], r[c & 1][2 * j + 1]), s2, acc[c][j]);
-                    if (c + 1 < C::CHUNKS) tmem_ld_wait();
+                    for (int l = 0; l < C::LDW / C::LW; ++l) {
+                        uint32_t r[C::LW];
+                        if constexpr (C::LW == 32) tmem_ld32(a0 + chunk_col<C>(cq, c) + l * C::LW, r);
+                        else tmem_ld16(a0 + chunk_col<C>(cq, c) + l * C::LW, r);
+                        tmem_ld_wait();
+                        if (c == C::CHUNKS - 1 && l == C::LDW / C::LW - 1) {
+                            // every column is in registers: the MMA may write the buffer again
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_even(&acc_empty[buf]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < C::LW / 2; ++j) {
+                            uint64_t& y = acc[c][l * C::LW / 2 + j];
+                            y = fma2(pack2u(r[2 * j], r[2 * j + 1]), s2, y);
+                        }
+                    }
                 }
                 if (k4 == C::SC_KB - 1 || kb == kbs - 1) {
                     __syncwarp();
@@ -166,45 +170,46 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
                         sph ^= 1u;
                     }
                 }
-                if (++buf == C::NBUF) {
-                    buf = 0;
-                    bph ^= 1u;
+                if (++buf == C::NBUF) buf = 0;
+                if (++st == C::STAGES) {
+                    st = 0;
+                    ph ^= 1u;
                 }
             }
             if (!ok) break;
-            const long grow = (long)ti.m0 + row;
             if constexpr (!C::GATED) {
-                if (grow < p.M) {
+                uint8_t* stg = outs + (warp - 4) * 2048;
 #pragma unroll
-                    for (int c = 0; c < C::CHUNKS; ++c) store_chunk(p, grow, ti.n0 + chunk_col<C>(hf, c), acc[c]);
-                }
+                for (int c = 0; c < C::CHUNKS; ++c)
+                    store_chunk<C::LDW>(p, stg, lane, (long)ti.m0 + q * 32, ti.n0 + chunk_col<C>(cq, c), acc[c]);
             } else {
-                float h[64];
+                // acc[0]: 32 gate columns, acc[1]: the same columns of up
+                const long grow = (long)ti.m0 + row;
+                float h[32];
                 float a = 0.f;
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float2 g = unpack2(acc[c][j]), u = unpack2(acc[c + 2][j]);
-                        h[c * 32 + 2 * j] = swiglu(g.x, u.x);
-                        h[c * 32 + 2 * j + 1] = swiglu(g.y, u.y);
-                        a = max_nan(a, max_nan(fabsf(h[c * 32 + 2 * j]), fabsf(h[c * 32 + 2 * j + 1])));
-                    }
-                rowmax[(parity * 2 + hf) * 128 + row] = a;
+                for (int j = 0; j < 16; ++j) {
+                    const float2 g = unpack2(acc[0][j]), u = unpack2(acc[1][j]);
+                    h[2 * j] = swiglu(g.x, u.x);
+                    h[2 * j + 1] = swiglu(g.y, u.y);
+                    a = max_nan(a, max_nan(fabsf(h[2 * j]), fabsf(h[2 * j + 1])));
+                }
+                float* rm = rowmax + parity * 512 + row;
+                rm[cq * 128] = a;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&rm_full[parity]);
                 if (!mbar_wait(&rm_full[parity], rph, abort_flag, p.err, DEV_TIMEOUT_ACC)) break;
                 rph ^= (uint32_t)parity;
-                a = max_nan(a, rowmax[(parity * 2 + (hf ^ 1)) * 128 + row]);
+                a = max_nan(max_nan(rm[0], rm[128]), max_nan(rm[256], rm[384]));
                 const float s = a / 448.0f;
                 const GroupScale gs = group_scale(s);
                 if (grow < p.M) {
-                    uint4* dst = reinterpret_cast<uint4*>(p.Hq + grow * p.N + ti.n0 + hf * 64);
+                    uint4* dst = reinterpret_cast<uint4*>(p.Hq + grow * p.N + ti.n0 + cq * 32);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < 2; ++j)
                         dst[j] = make_uint4(codes4(gs, h + 16 * j), codes4(gs, h + 16 * j + 4), codes4(gs, h + 16 * j + 8),
                                             codes4(gs, h + 16 * j + 12));
-                    if (hf == 0) p.Hs[grow * (p.N / 128) + ti.n0 / 128] = s;
+                    if (cq == 0) p.Hs[grow * (p.N / 128) + ti.n0 / 128] = s;
                 }
             }
         }
@@ -213,7 +218,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
         if (warp == 0) {
             // ------------------------------------------------------------ producer
             // Both CTAs' copies complete on the even CTA's barrier, which expects all of
-            // them; a stage is free again when the pair's MMA commit arrives in both CTAs.
+            // them; a stage is free again when its MMAs' one commit arrives in both CTAs.
             int s = 0;
             uint32_t ph = 0;
             long issued = 0;
@@ -223,7 +228,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
                 // this CTA's BN/2 weight rows (gated: the even CTA gate, the odd CTA up rows)
                 const int w0 = C::GATED ? ti.n0 + crank * p.N : ti.n0 + crank * (C::BN / 2);
                 for (int kb = 0; kb < kbs; ++kb) {
-                    const bool got = mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_TMA_EMPTY);
+                    const bool got = mbar_wait(&done[s], ph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_TMA_EMPTY);
                     if (__any_sync(0xffffffffu, !got)) {
                         ok = false;
                         break;
@@ -254,26 +259,35 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
             }
         } else if (warp == 1) {
             // ------------------------------------------------------------ MMA issuer
-            if (lane == 0 && crank == 0) {
+            // The whole warp runs the loop, so that descriptors and addresses are
+            // warp-uniform, and one elected lane issues; from one lane's own branch each
+            // MMA took about 80 cycles to issue.  One commit per K block (65 cycles to
+            // issue) frees the stage and publishes the accumulator.
+            if (crank == 0) {
+                const uint32_t tb = __shfl_sync(0xffffffffu, tmem_base, 0);
+                const uint32_t st0 = smem_u32(stage);
                 int s = 0, buf = 0;
                 uint32_t ph = 0, bph = 0;
                 bool ok = true;
                 for (int t = cid; t < tiles && ok; t += ncl) {
                     for (int kb = 0; kb < kbs; ++kb) {
-                        if (!mbar_wait_cl(&acc_empty[buf], bph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_ACC_EMPTY) ||
-                            !mbar_wait_cl(&full[s], ph, abort_flag, p.err, DEV_TIMEOUT_TMA_FULL)) {
+                        const bool got = mbar_wait(&acc_empty[buf], bph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_ACC_EMPTY) &&
+                                         mbar_wait(&full[s], ph, abort_flag, p.err, DEV_TIMEOUT_TMA_FULL);
+                        if (__any_sync(0xffffffffu, !got)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t sa = smem_u32(stage + s * C::STAGE_BYTES);
+                        const uint32_t sa = st0 + (uint32_t)(s * C::STAGE_BYTES);
                         const uint64_t ad = smem_desc_sw128(sa), bd = smem_desc_sw128(sa + C::A_BYTES);
-                        const uint32_t d = tmem_base + (uint32_t)(buf * C::BUF_COLS);
+                        const uint32_t d = tb + (uint32_t)(buf * C::BUF_COLS);
+                        if (elect_one_sync()) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)   // 32 codes (32 bytes) per MMA
-                            tc_mma_f8_pair(d, ad + (uint64_t)(k * 2), bd + (uint64_t)(k * 2), idesc_e4m3(256, C::BN), k > 0);
-                        tc_commit_pair(&acc_full[buf], 3);
-                        tc_commit_pair(&empty[s], 3);
+                            for (int k = 0; k < 4; ++k)   // 32 codes (32 bytes) per MMA
+                                tc_mma_f8_pair(d, ad + (uint64_t)(k * 2), bd + (uint64_t)(k * 2), idesc_e4m3(256, C::BN), k > 0);
+                            tc_commit_pair(&done[s], 3);
+                        }
+                        __syncwarp();
                         if (++buf == C::NBUF) {
                             buf = 0;
                             bph ^= 1u;
@@ -284,76 +298,50 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
                         }
                     }
                 }
-                tc_commit_pair(drain, 1);
-                drain_ring(drain, 1, 1, p.err);
+                if (elect_one_sync()) tc_commit_pair(drain, 1);
+                __syncwarp();
+                if (lane == 0) drain_ring(drain, 1, 1, p.err);
             }
             __syncwarp();
         } else {
-            // ------------------------------------------------------------ scale products
-            // lane: rows 64 (warp - 2) + lane and + 32; the loads of the next four K blocks
-            // are in flight while these are multiplied and stored
-            const int r0 = (warp - 2) * 64 + lane;
+            // ------------------------------------------------------------ scales
+            // Copied 4 bytes at a time (any alignment and pitch; rows, K blocks and weight
+            // blocks past the end are filled with zeros); a slot's barrier counts the
+            // copies of all 64 lanes.
+            const int l = threadIdx.x - 64;
             int slot = 0;
             uint32_t sph = 0;
             bool ok = true;
-            float x[2][4], w[2][4];
-            int pt = cid, pk = 0;
-            PairTile pi = pair_tile<C>(p, pt, crank);
-            auto fetch = [&]() {
-                if (pt >= tiles) return;
-                const int b0 = C::GATED ? pi.n0 / 128 : pi.n0 / 128;
-                const int b1 = C::GATED ? (p.N + pi.n0) / 128 : b0 + 1;
-                const int nblk = C::GATED ? p.N / 64 : (p.N + 127) / 128;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const bool in = pk + k < kbs;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const long m = (long)pi.m0 + r0 + 32 * i;
-                        x[i][k] = (in && m < p.M) ? __ldg(p.Xs + m * kbs + pk + k) : 0.f;
-                    }
-                    w[0][k] = in ? __ldg(p.S + (long)b0 * kbs + pk + k) : 0.f;
-                    w[1][k] = (in && C::BN > 128 && b1 < nblk) ? __ldg(p.S + (long)b1 * kbs + pk + k) : 0.f;
-                }
-                pk += 4;
-                if (pk >= kbs) {
-                    pk = 0;
-                    pt += ncl;
-                    pi = pair_tile<C>(p, pt, crank);
-                }
-            };
-            fetch();
             for (int t = cid; t < tiles && ok; t += ncl) {
-                for (int kb = 0; kb < kbs; kb += 4) {
-                    float y[2][2][4];   // [block][row][k]
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            y[0][i][k] = x[i][k] * w[0][k];
-                            y[1][i][k] = x[i][k] * w[1][k];
-                        }
-                    fetch();
+                const PairTile ti = pair_tile<C>(p, t, crank);
+                const long b0 = ti.n0 / 128, b1 = C::GATED ? (p.N + ti.n0) / 128 : b0 + 1;
+                const long nblk = C::GATED ? p.N / 64 : (p.N + 127) / 128;
+                for (int kb = 0; kb < kbs; kb += C::SC_KB) {
                     if (!mbar_wait(&sc_empty[slot], sph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_CONV_EMPTY)) {
                         ok = false;
                         break;
                     }
-                    float* dst = sc + slot * C::SC_KB * 2 * 128 + r0;
+                    float* dst = sc + slot * C::SC_KB * C::SC_PITCH;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            dst[(k * 2) * 128 + 32 * i] = y[0][i][k];
-                            if (C::BN > 128) dst[(k * 2 + 1) * 128 + 32 * i] = y[1][i][k];
-                        }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sc_full[slot]);
+                    for (int i = 0; i < 2 * C::SC_KB; ++i) {
+                        const int k = i >> 1, r = (i & 1) * 64 + l;
+                        const bool in = kb + k < kbs && ti.m0 + r < p.M;
+                        cp_async4(dst + k * C::SC_PITCH + r, in ? p.Xs + ((long)ti.m0 + r) * kbs + kb + k : p.Xs, in);
+                    }
+                    if (l < 2 * C::SC_KB) {
+                        const int k = l >> 1;
+                        const long b = (l & 1) ? b1 : b0;
+                        const bool in = kb + k < kbs && b < nblk;
+                        cp_async4(dst + k * C::SC_PITCH + 128 + (l & 1), in ? p.S + b * kbs + kb + k : p.S, in);
+                    }
+                    cp_async_arrive(&sc_full[slot]);
                     if (++slot == C::SC_SLOTS) {
                         slot = 0;
                         sph ^= 1u;
                     }
                 }
             }
+            cp_async_wait_all();
         }
     }
 
