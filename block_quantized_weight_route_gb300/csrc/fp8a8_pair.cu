@@ -78,7 +78,9 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rm_full + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (read through a shuffle, so that the compiler knows it and the TMEM addresses made
+    // from it to be the same in the whole warp)
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(&full[i], 1);
@@ -104,8 +106,9 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
     __syncthreads();
     cluster_sync();   // the peer's barriers are initialised before any copy or commit signals them
     tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
-    const int crank = (int)cluster_ctarank(), cid = (int)cluster_id_x(), ncl = (int)cluster_count_x();
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    const int crank = __shfl_sync(0xffffffffu, (int)cluster_ctarank(), 0);
+    const int cid = __shfl_sync(0xffffffffu, (int)cluster_id_x(), 0), ncl = (int)(gridDim.x >> 1);
     const int tiles = p.m_tiles * p.n_tiles, kbs = (p.K + 127) / 128;
 
     if (warp >= 4) {
@@ -264,7 +267,6 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
             // MMA took about 80 cycles to issue.  One commit per K block (65 cycles to
             // issue) frees the stage and publishes the accumulator.
             if (crank == 0) {
-                const uint32_t tb = __shfl_sync(0xffffffffu, tmem_base, 0);
                 const uint32_t st0 = smem_u32(stage);
                 int s = 0, buf = 0;
                 uint32_t ph = 0, bph = 0;
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
                         tc_fence_after();
                         const uint32_t sa = st0 + (uint32_t)(s * C::STAGE_BYTES);
                         const uint64_t ad = smem_desc_sw128(sa), bd = smem_desc_sw128(sa + C::A_BYTES);
-                        const uint32_t d = tb + (uint32_t)(buf * C::BUF_COLS);
+                        const uint32_t d = tmem_base + (uint32_t)(buf * C::BUF_COLS);
                         if (elect_one_sync()) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k)   // 32 codes (32 bytes) per MMA
