@@ -28,11 +28,15 @@ __device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t a_desc,
 // tcgen05.fence::before_thread_sync).  No shared or global memory is handed over,
 // so the release is at CTA scope: a cluster-scope release took about 1200 cycles
 // per hand-over (2048 x 5120 x 5120: 128 us with it, 70 us without).
-__device__ __forceinline__ void mbar_arrive_even(uint64_t* bar) {
+// crank: this CTA's rank; the even CTA arrives without the detour over the cluster.
+__device__ __forceinline__ void mbar_arrive_even(uint64_t* bar, int crank) {
     asm volatile(
-        "{\n\t.reg .b32 ra;\n\t"
-        "mapa.shared::cluster.u32 ra, %0, 0;\n\t"
-        "mbarrier.arrive.shared::cluster.b64 _, [ra];\n\t}" ::"r"(smem_u32(bar))
+        "{\n\t.reg .b32 ra;\n\t.reg .pred p;\n\t"
+        "setp.eq.s32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t"
+        "@!p mapa.shared::cluster.u32 ra, %0, 0;\n\t"
+        "@!p mbarrier.arrive.shared::cluster.b64 _, [ra];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(crank)
         : "memory");
 }
 
@@ -46,6 +50,16 @@ __device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorM
         "\n\t}" ::"r"(smem_u32(smem_dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
         : "memory");
+}
+
+// 32 lanes x 32, 16 or 8 consecutive 32-bit TMEM columns.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
 }
 
 // Two fp32 values in one 64-bit register, and their packed multiply-add.
@@ -92,12 +106,12 @@ __device__ __forceinline__ float swiglu(float g, float u) {
     return __fdividef(g < 0.0f ? g * t : g, 1.0f + t) * u;
 }
 
-// First column, inside the tile, of chunk c of a fold thread of column quarter cq:
-// consecutive columns, or (gated) chunk 0 gate and chunk 1 the same columns of up.
+// The column, inside the tile, of a fold thread's column i, for column group cq:
+// consecutive columns, or (gated) half of them gate, then the same columns of up.
 template <class C>
-__device__ __forceinline__ int chunk_col(int cq, int c) {
-    if constexpr (C::GATED) return c * 128 + cq * 32;
-    else return cq * C::CW + c * C::LDW;
+__device__ __forceinline__ int fold_col(int cq, int i) {
+    if constexpr (C::GATED) return (i / (C::CW / 2)) * 128 + cq * (C::CW / 2) + i % (C::CW / 2);
+    else return cq * C::CW + i;
 }
 
 // 4-byte asynchronous copy to shared memory, or a zero.

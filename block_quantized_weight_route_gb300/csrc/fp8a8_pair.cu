@@ -11,8 +11,14 @@
 //   warp 0: TMA producer   warp 1: MMA issuer (even CTA)
 //   warps 2, 3: the scales of four K blocks at a time, by asynchronous copies into a ring
 //   warps 4..19: fold; warp w reads TMEM lanes 32 (w % 4) .. +31 (a row per lane) and
-//                quarter (w - 4) / 4 of the columns.  Sixteen warps rather than eight: a
-//                TMEM load cannot be waited for on its own, so other warps hide it.
+//                quarter (w - 4) / 4 of the columns
+// What bounds it: a TMEM buffer's way from the MMA's end through the fold and back to
+// the even CTA takes longer than the other buffer's MMA (512 cycles at BN = 256), so the
+// length of the fold's path counts, not its throughput: 16 warps rather than 8, TMEM loads
+// of 8 columns (5268 x 17408 x 5120: 388 us; of 16: 428, of 4: 578; BN = 192, whose path is
+// shorter: 16), four K blocks
+// unrolled and no spilled registers.  At 2.4 PFLOP/s the power limit is near: without any
+// fold the same loop reaches 3.0 PFLOP/s at clocks down to 1.6 GHz.
 #include "fp8a8.cuh"
 
 namespace qmm {
@@ -28,10 +34,9 @@ struct PairCfg {
     static constexpr int SC_SLOTS = 4, SC_KB = 4;                 // ring of scales: slots of 4 K blocks
     static constexpr int SC_PITCH = 128 + 4;                      // per K block: the rows' scales, the two blocks'
     static constexpr int SC_FLOATS = SC_SLOTS * SC_KB * SC_PITCH;
-    static constexpr int FOLD_WARPS = 16, CW = BN / 4;            // columns of a fold thread
-    static constexpr int LDW = CW % 32 ? 16 : 32, CHUNKS = CW / LDW;
-    static constexpr int LW = 16;                                 // columns of a TMEM load
-    static constexpr int OUT_BYTES = GATED ? 2 * 4 * 128 * 4 : FOLD_WARPS * 2048;   // row maxima, or output staging
+    static constexpr int FOLD_WARPS = 16, GROUPS = FOLD_WARPS / 4;                  // column groups
+    static constexpr int CW = BN / GROUPS, PARTS = CW / 16, LW = BN == 192 ? 16 : 8;// columns of a fold thread, of a load
+    static constexpr int OUT_BYTES = GATED ? 2 * GROUPS * 128 * 4 : FOLD_WARPS * 2048;   // row maxima, or output staging
     static constexpr int THREADS = 128 + 32 * FOLD_WARPS, REGS = 96, REGS_FOLD = 104, REGS_OTHER = 64;
     static_assert(REGS_FOLD * 32 * FOLD_WARPS + REGS_OTHER * 128 == REGS * THREADS, "register shares = launch registers");
     static constexpr int BARS = 2 * STAGES + NBUF + 2 * SC_SLOTS + 3;
@@ -55,8 +60,9 @@ __device__ __forceinline__ PairTile pair_tile(const Fp8a8Params& p, int t, int c
 }
 
 // E4M3 codes of four values scaled by gs
-__device__ __forceinline__ uint32_t codes4(const GroupScale& gs, const float* h) {
-    return e4m3x4(gs(h[0]), gs(h[1]), gs(h[2]), gs(h[3]));
+__device__ __forceinline__ uint32_t codes4(const GroupScale& gs, uint64_t a, uint64_t b) {
+    const float2 x = unpack2(a), y = unpack2(b);
+    return e4m3x4(gs(x.x), gs(x.y), gs(y.x), gs(y.y));
 }
 
 template <class C>
@@ -116,86 +122,88 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
         // ------------------------------------------------------------ fold
         const int q = warp & 3, cq = (warp - 4) >> 2, row = q * 32 + lane;
         const uint32_t lane_addr = tmem_base + ((uint32_t)(q * 32) << 16);
-        int st = 0, buf = 0, slot = 0, parity = 0;
+        int st = 0, slot = 0, parity = 0;
         uint32_t ph = 0, sph = 0, rph = 0;
         bool ok = true;
         for (int t = cid; t < tiles && ok; t += ncl, parity ^= 1) {
             const PairTile ti = pair_tile<C>(p, t, crank);
             // columns below `bound` belong to the first of the tile's two weight blocks
             const int bound = C::BN == 192 ? 128 - (ti.n0 & 127) : 128;
-            uint64_t acc[C::CHUNKS][C::LDW / 2];
+            uint64_t acc[C::PARTS][8];
 #pragma unroll
-            for (int c = 0; c < C::CHUNKS; ++c)
+            for (int c = 0; c < C::PARTS; ++c)
 #pragma unroll
-                for (int j = 0; j < C::LDW / 2; ++j) acc[c][j] = 0;
-            for (int kb = 0; kb < kbs; ++kb) {
-                const int k4 = kb & (C::SC_KB - 1);
-                if (k4 == 0 && !mbar_wait(&sc_full[slot], sph, abort_flag, p.err, DEV_TIMEOUT_CONV)) {
+                for (int j = 0; j < 8; ++j) acc[c][j] = 0;
+            for (int kb0 = 0; kb0 < kbs && ok; kb0 += C::SC_KB) {
+                if (!mbar_wait(&sc_full[slot], sph, abort_flag, p.err, DEV_TIMEOUT_CONV)) {
                     ok = false;
                     break;
                 }
-                const float* scr = sc + (slot * C::SC_KB + k4) * C::SC_PITCH;
-                const float sx = scr[row], s0 = sx * scr[128], s1 = C::BN > 128 ? sx * scr[129] : 0.f;
-                if (!mbar_wait(&done[st], ph, abort_flag, p.err, DEV_TIMEOUT_ACC)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t a0 = lane_addr + (uint32_t)(buf * C::BUF_COLS);
+                const float* scr = sc + slot * C::SC_KB * C::SC_PITCH;
 #pragma unroll
-                for (int c = 0; c < C::CHUNKS; ++c) {
-                    const float sf = chunk_col<C>(cq, c) < bound ? s0 : s1;
-                    const uint64_t s2 = pack2(sf, sf);
+                for (int k = 0; k < C::SC_KB; ++k) {
+                    if (kb0 + k >= kbs) break;
+                    // the scales' product for the thread's columns (both of the tile's blocks
+                    // where its columns reach into both)
+                    const float sx = scr[k * C::SC_PITCH + row];
+                    const float s0 = sx * scr[k * C::SC_PITCH + 128 + (C::BN == 256 && !C::GATED ? cq / (C::GROUPS / 2) : 0)];
+                    const float s1 = C::BN == 192 || C::GATED ? sx * scr[k * C::SC_PITCH + 129] : s0;
+                    if (!mbar_wait(&done[st], ph, abort_flag, p.err, DEV_TIMEOUT_ACC)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const int buf = k & (C::NBUF - 1);
+                    const uint32_t a0 = lane_addr + (uint32_t)(buf * C::BUF_COLS);
 #pragma unroll
-                    for (int l = 0; l < C::LDW / C::LW; ++l) {
+                    for (int x = 0; x < C::CW; x += C::LW) {
                         uint32_t r[C::LW];
-                        if constexpr (C::LW == 32) tmem_ld32(a0 + chunk_col<C>(cq, c) + l * C::LW, r);
-                        else tmem_ld16(a0 + chunk_col<C>(cq, c) + l * C::LW, r);
+                        tmem_ld(a0 + fold_col<C>(cq, x), r);
                         tmem_ld_wait();
-                        if (c == C::CHUNKS - 1 && l == C::LDW / C::LW - 1) {
+                        if (x == C::CW - C::LW) {
                             // every column is in registers: the MMA may write the buffer again
                             tc_fence_before();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive_even(&acc_empty[buf]);
+                            if (lane == 0) mbar_arrive_even(&acc_empty[buf], crank);
                         }
+                        const float sf = C::GATED ? (x < C::CW / 2 ? s0 : s1) : fold_col<C>(cq, x & ~15) < bound ? s0 : s1;
+                        const uint64_t s2 = pack2(sf, sf);
 #pragma unroll
                         for (int j = 0; j < C::LW / 2; ++j) {
-                            uint64_t& y = acc[c][l * C::LW / 2 + j];
+                            uint64_t& y = acc[x / 16][x % 16 / 2 + j];
                             y = fma2(pack2u(r[2 * j], r[2 * j + 1]), s2, y);
                         }
                     }
-                }
-                if (k4 == C::SC_KB - 1 || kb == kbs - 1) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sc_empty[slot]);
-                    if (++slot == C::SC_SLOTS) {
-                        slot = 0;
-                        sph ^= 1u;
+                    if (++st == C::STAGES) {
+                        st = 0;
+                        ph ^= 1u;
                     }
                 }
-                if (++buf == C::NBUF) buf = 0;
-                if (++st == C::STAGES) {
-                    st = 0;
-                    ph ^= 1u;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sc_empty[slot]);
+                if (++slot == C::SC_SLOTS) {
+                    slot = 0;
+                    sph ^= 1u;
                 }
             }
             if (!ok) break;
             if constexpr (!C::GATED) {
                 uint8_t* stg = outs + (warp - 4) * 2048;
 #pragma unroll
-                for (int c = 0; c < C::CHUNKS; ++c)
-                    store_chunk<C::LDW>(p, stg, lane, (long)ti.m0 + q * 32, ti.n0 + chunk_col<C>(cq, c), acc[c]);
+                for (int c = 0; c < C::PARTS; ++c)
+                    store_chunk<16>(p, stg, lane, (long)ti.m0 + q * 32, ti.n0 + fold_col<C>(cq, c * 16), acc[c]);
             } else {
-                // acc[0]: 32 gate columns, acc[1]: the same columns of up
+                // the first half of acc: gate columns; the second half: the same columns of up
+                constexpr int HP = C::PARTS / 2;
                 const long grow = (long)ti.m0 + row;
-                float h[32];
                 float a = 0.f;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float2 g = unpack2(acc[0][j]), u = unpack2(acc[1][j]);
-                    h[2 * j] = swiglu(g.x, u.x);
-                    h[2 * j + 1] = swiglu(g.y, u.y);
-                    a = max_nan(a, max_nan(fabsf(h[2 * j]), fabsf(h[2 * j + 1])));
+                for (int j = 0; j < HP * 8; ++j) {
+                    uint64_t& y = acc[j / 8][j % 8];
+                    const float2 g = unpack2(y), u = unpack2(acc[HP + j / 8][j % 8]);
+                    const float h0 = swiglu(g.x, u.x), h1 = swiglu(g.y, u.y);
+                    a = max_nan(a, max_nan(fabsf(h0), fabsf(h1)));
+                    y = pack2(h0, h1);
                 }
                 float* rm = rowmax + parity * 512 + row;
                 rm[cq * 128] = a;
@@ -203,15 +211,16 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
                 if (lane == 0) mbar_arrive(&rm_full[parity]);
                 if (!mbar_wait(&rm_full[parity], rph, abort_flag, p.err, DEV_TIMEOUT_ACC)) break;
                 rph ^= (uint32_t)parity;
-                a = max_nan(max_nan(rm[0], rm[128]), max_nan(rm[256], rm[384]));
+#pragma unroll
+                for (int i = 0; i < C::GROUPS; ++i) a = max_nan(a, rm[i * 128]);
                 const float s = a / 448.0f;
                 const GroupScale gs = group_scale(s);
                 if (grow < p.M) {
-                    uint4* dst = reinterpret_cast<uint4*>(p.Hq + grow * p.N + ti.n0 + cq * 32);
+                    uint4* dst = reinterpret_cast<uint4*>(p.Hq + grow * p.N + ti.n0 + cq * (C::CW / 2));
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        dst[j] = make_uint4(codes4(gs, h + 16 * j), codes4(gs, h + 16 * j + 4), codes4(gs, h + 16 * j + 8),
-                                            codes4(gs, h + 16 * j + 12));
+                    for (int j = 0; j < HP; ++j)
+                        dst[j] = make_uint4(codes4(gs, acc[j][0], acc[j][1]), codes4(gs, acc[j][2], acc[j][3]),
+                                            codes4(gs, acc[j][4], acc[j][5]), codes4(gs, acc[j][6], acc[j][7]));
                     if (cq == 0) p.Hs[grow * (p.N / 128) + ti.n0 / 128] = s;
                 }
             }
@@ -268,13 +277,15 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
             // issue) frees the stage and publishes the accumulator.
             if (crank == 0) {
                 const uint32_t st0 = smem_u32(stage);
-                int s = 0, buf = 0;
-                uint32_t ph = 0, bph = 0;
+                int s = 0;
+                uint32_t ph = 0, bph = 0;   // bph: a phase bit per buffer
                 bool ok = true;
                 for (int t = cid; t < tiles && ok; t += ncl) {
                     for (int kb = 0; kb < kbs; ++kb) {
-                        const bool got = mbar_wait(&acc_empty[buf], bph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_ACC_EMPTY) &&
-                                         mbar_wait(&full[s], ph, abort_flag, p.err, DEV_TIMEOUT_TMA_FULL);
+                        // (every tile starts with buffer 0, so that the fold's is a constant)
+                        const int buf = kb & (C::NBUF - 1);
+                        const bool got = mbar_wait(&full[s], ph, abort_flag, p.err, DEV_TIMEOUT_TMA_FULL) &&
+                                         mbar_wait(&acc_empty[buf], ((bph >> buf) & 1u) ^ 1u, abort_flag, p.err, DEV_TIMEOUT_ACC_EMPTY);
                         if (__any_sync(0xffffffffu, !got)) {
                             ok = false;
                             break;
@@ -290,10 +301,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
                             tc_commit_pair(&done[s], 3);
                         }
                         __syncwarp();
-                        if (++buf == C::NBUF) {
-                            buf = 0;
-                            bph ^= 1u;
-                        }
+                        bph ^= 1u << buf;
                         if (++s == C::STAGES) {
                             s = 0;
                             ph ^= 1u;
@@ -365,12 +373,6 @@ cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Para
     if (most[dev] == 0) {
         e = cudaFuncSetAttribute(fp8a8_pair_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
-        // the warpgroups' register shares add up to the launch's: launch only if the
-        // kernel is allocated exactly that many (a setmaxnreg.inc past the pool waits)
-        cudaFuncAttributes fa{};
-        e = cudaFuncGetAttributes(&fa, fp8a8_pair_kernel<C>);
-        if (e != cudaSuccess) return e;
-        if (fa.numRegs != C::REGS) return cudaErrorInvalidConfiguration;
     }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
