@@ -918,20 +918,18 @@ qmm_status qmm_add_rmsnorm_q8_1(const void* X, qmm_dtype xdt, int64_t ldx, const
 static qmm_status run_fp8a8(const char* who, DeviceState* d, Fp8a8Params& p, bool gated, cudaStream_t stream) {
     const Fp8a8Plan pl = fp8a8_plan(p.M, p.K, p.N, gated, d->sms);
     p.err = d->err;
-    cudaError_t e;
-    if (pl.x_rows) {
-        qmm_status st;
-        CUtensorMap tx, tw;
-        if ((st = make_tmap(&tx, p.Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, p.M, p.K, 128, pl.x_rows,
-                            CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK)
-            return st;
-        if ((st = make_tmap(&tw, p.W, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, (uint64_t)p.N * (gated ? 2 : 1), p.K, 128,
-                            pl.w_rows, CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK)
-            return st;
-        e = launch_fp8a8_pair(tx, tw, p, gated, pl.bn, d->sms, stream);
-    } else {
-        e = launch_fp8a8(p, gated, stream);
-    }
+    // boxes of 128 codes: 128 activation rows and a CTA's half of the columns (pair), or
+    // the tile's tokens and 128 weight rows
+    qmm_status st;
+    CUtensorMap tx, tw;
+    if ((st = make_tmap(&tx, p.Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, p.M, p.K, 128, pl.pair ? 128 : pl.tn,
+                        CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK)
+        return st;
+    if ((st = make_tmap(&tw, p.W, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, (uint64_t)p.N * (gated ? 2 : 1), p.K, 128,
+                        pl.pair ? pl.bn / 2 : 128, CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK)
+        return st;
+    cudaError_t e = pl.pair ? launch_fp8a8_pair(tx, tw, p, gated, pl.bn, d->sms, stream)
+                            : launch_fp8a8_narrow(tx, tw, p, gated, pl.tn, pl.cs, stream);
     return e == cudaSuccess ? QMM_OK : cuda_fail(e, who);
 }
 

@@ -1,153 +1,53 @@
-// FP8 x FP8 products with block scales (qmm_fp8a8_blk128, qmm_fp8a8_swiglu_blk128).
-//
-//   y[m][n] = sum_kb Xs[m][kb] S[n/128][kb] sum_{k in kb} e4m3(Xq[m][k]) e4m3(W[n][k])
-//   h = silu(y gate) * y up, rounded to E4M3 per 128 columns
-// One thread per output column and 16 tokens per CTA: the block's activations
-// are converted to fp32 in shared memory and read as broadcasts, each thread
-// reads its own weight row 16 bytes at a time.  fp32 throughout.
+// FP8 x FP8 products with block scales: which kernel takes which shape.
 #include "qmm_internal.h"
-#include "quant8.cuh"
 
 namespace qmm {
-namespace {
 
-constexpr int kTok = 16;
-
-__device__ __forceinline__ void e4m3x4_to_f32(uint32_t w, float (&f)[4]) {
-    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
-    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-    const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
-    const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
-    f[0] = fa.x, f[1] = fa.y, f[2] = fb.x, f[3] = fb.y;
-}
-
-// GATED: 256 threads, columns n0 + 0..127 of the gate rows and of the up rows;
-// else 128 threads, columns n0 + 0..127.
-template <bool GATED>
-__global__ void __launch_bounds__(GATED ? 256 : 128) fp8a8_simple_kernel(Fp8a8Params p) {
-    __shared__ float xs[kTok][128];
-    __shared__ float ux[GATED ? 128 : 1][kTok + 1];
-    __shared__ float wmax[4][kTok];
-    constexpr int kThreads = GATED ? 256 : 128;
-    const int n0 = blockIdx.x * 128, half = threadIdx.x >> 7, c = threadIdx.x & 127;
-    const long m0 = (long)blockIdx.y * kTok;
-    const int kbs = (p.K + 127) / 128;
-    const bool col_ok = n0 + c < p.N;
-    const long wrow = (GATED ? (long)half * p.N : 0) + n0 + (col_ok ? c : 0);   // gated: p.N = F
-    const int nblk = (int)((GATED ? (long)half * p.N + n0 : (long)n0) / 128);
-    float acc[kTok];
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) acc[i] = 0.f;
-    for (int kb = 0; kb < kbs; ++kb) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < kTok * 8; i += kThreads) {
-            const int r = i >> 3, k = kb * 128 + (i & 7) * 16;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (m0 + r < p.M && k < p.K) v = *reinterpret_cast<const uint4*>(p.Xq + (m0 + r) * p.K + k);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float f[4];
-                e4m3x4_to_f32(w[j], f);
-                *reinterpret_cast<float4*>(&xs[r][(i & 7) * 16 + j * 4]) = make_float4(f[0], f[1], f[2], f[3]);
-            }
-        }
-        __syncthreads();
-        float part[kTok];
-#pragma unroll
-        for (int i = 0; i < kTok; ++i) part[i] = 0.f;
-        for (int k = 0; k < 128 && kb * 128 + k < p.K; k += 16) {
-            const uint4 v = *reinterpret_cast<const uint4*>(p.W + wrow * p.K + kb * 128 + k);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float f[4];
-                e4m3x4_to_f32(w[j], f);
-#pragma unroll
-                for (int i = 0; i < kTok; ++i) {
-                    const float4 x = *reinterpret_cast<const float4*>(&xs[i][k + j * 4]);
-                    part[i] = fmaf(f[3], x.w, fmaf(f[2], x.z, fmaf(f[1], x.y, fmaf(f[0], x.x, part[i]))));
-                }
-            }
-        }
-        const float sw = p.S[(long)nblk * kbs + kb];
-#pragma unroll
-        for (int i = 0; i < kTok; ++i)
-            if (m0 + i < p.M) acc[i] = fmaf(part[i], p.Xs[(m0 + i) * kbs + kb] * sw, acc[i]);
-    }
-    if constexpr (!GATED) {
-        if (col_ok) {
-#pragma unroll
-            for (int i = 0; i < kTok; ++i) {
-                if (m0 + i >= p.M) break;
-                const long o = (m0 + i) * p.N + n0 + c;
-                if (p.y_bf16) static_cast<__nv_bfloat16*>(p.Y)[o] = __float2bfloat16_rn(acc[i]);
-                else static_cast<float*>(p.Y)[o] = acc[i];
-            }
-        }
-    } else {
-        if (half == 1) {
-#pragma unroll
-            for (int i = 0; i < kTok; ++i) ux[c][i] = acc[i];
-        }
-        __syncthreads();
-        if (half == 0) {
-#pragma unroll
-            for (int i = 0; i < kTok; ++i) {
-                acc[i] = acc[i] / (1.0f + expf(-acc[i])) * ux[c][i];
-                float a = fabsf(acc[i]);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
-                if ((c & 31) == 0) wmax[c >> 5][i] = a;
-            }
-        }
-        __syncthreads();
-        if (half == 0) {
-#pragma unroll
-            for (int i = 0; i < kTok; ++i) {
-                if (m0 + i >= p.M) break;
-                const float a = max_nan(max_nan(wmax[0][i], wmax[1][i]), max_nan(wmax[2][i], wmax[3][i]));
-                const float s = a / 448.0f;
-                const GroupScale gs = group_scale(s);
-                p.Hq[(m0 + i) * p.N + n0 + c] = (uint8_t)__nv_cvt_float_to_fp8(gs(acc[i]), __NV_SATFINITE, __NV_E4M3);
-                if (c == 0) p.Hs[(m0 + i) * (p.N / 128) + n0 / 128] = s;
-            }
-        }
-    }
-}
-
-}  // namespace
-
-// Columns of a prompt tile: the width whose waves of pairs take least, counting a
-// wave as its width plus a fixed part for filling and draining the pipeline.
+// The kernel, tile and split with the least estimated time.  A launch's time is taken
+// as waves x (start and end of a CTA + its K blocks x time of a K block), in
+// microseconds, with the constants fitted to runs of one and of several waves at
+// K = 2048 .. 17408 (the part that all kernels share, launch and memory, left out):
+//   narrow kernel, 128 weight rows x tn tokens, K over cs CTAs, one CTA per SM
+//   pair kernel, 256 tokens x bn columns, one pair per two SMs
+// Measured at 5120 x 5120: 128 tokens narrow 128/3 13.8 us, pair 17.5; 300 tokens pair
+// (192 columns) 21.8, narrow 24.5; 1 token narrow 16/3 8.0, 16/1 13.3, 16/4 (more CTAs than
+// SMs) 13.6; at 2000 x 1000, 128 tokens 32/4 6.4, 128/8 8.5.
 Fp8a8Plan fp8a8_plan(int M, int K, int N, bool gated, int sms) {
-    (void)K;
-    Fp8a8Plan pl{};
-    if (M <= 64) return pl;
-    pl.pair = true;
-    pl.x_rows = 128;
-    pl.bn = 256;
-    if (!gated) {
-        const long pairs = sms / 2, mt = (M + 255) / 256;
-        double best = 1e30;
-        for (int bn : {256, 192, 128}) {
-            const long tiles = mt * ((N + bn - 1) / bn);
-            const double cost = (double)((tiles + pairs - 1) / pairs) * (bn + 16);
-            if (cost < best) {
-                best = cost;
-                pl.bn = bn;
-            }
+    const int kbs = (K + 127) / 128;
+    Fp8a8Plan best{};
+    double least = 1e300;
+    auto consider = [&](const Fp8a8Plan& pl, double tiles, double at_once, double ends, double kb, double per_kb) {
+        const double waves = (double)(long)((tiles + at_once - 1) / at_once);
+        const double t = waves * (ends + kb * per_kb);
+        if (t < least) {
+            least = t;
+            best = pl;
+        }
+    };
+    static const int tns[4] = {16, 32, 64, 128};
+    static const double narrow_kb[2][4] = {{0.21, 0.23, 0.27, 0.49}, {0.27, 0.37, 0.50, 0.0}};
+    for (int i = 0; i < (gated ? 3 : 4); ++i) {
+        const double tiles = (double)((N + 127) / 128) * ((M + tns[i] - 1) / tns[i]);
+        if (tiles > 8.0 * sms) continue;   // the pair kernel's
+        for (int cs = 1; cs <= 8 && cs <= kbs; ++cs) {
+            Fp8a8Plan pl{};
+            pl.tn = tns[i];
+            pl.cs = cs;
+            // (clusters of cs CTAs; adding up costs a little for each)
+            consider(pl, tiles, sms / cs, 2.2 + 0.1 * cs, (kbs + cs - 1) / cs, narrow_kb[gated][i]);
         }
     }
-    pl.w_rows = pl.bn / 2;
-    return pl;
-}
-
-cudaError_t launch_fp8a8(const Fp8a8Params& p, bool gated, cudaStream_t s) {
-    const dim3 grid((p.N + 127) / 128, (p.M + kTok - 1) / kTok);
-    if (gated) fp8a8_simple_kernel<true><<<grid, 256, 0, s>>>(p);
-    else fp8a8_simple_kernel<false><<<grid, 128, 0, s>>>(p);
-    return cudaGetLastError();
+    static const int bns[3] = {256, 192, 128};
+    static const double pair_ends[3] = {4.0, 2.9, 1.5}, pair_kb[3] = {0.43, 0.377, 0.30};
+    for (int i = 0; i < (gated ? 1 : 3); ++i) {
+        const double cols = gated ? 128 : bns[i];
+        const double tiles = (double)((M + 255) / 256) * (double)(long)((N + cols - 1) / cols);
+        Fp8a8Plan pl{};
+        pl.pair = true;
+        pl.bn = bns[i];
+        consider(pl, tiles, sms / 2, pair_ends[i], kbs, pair_kb[i]);
+    }
+    return best;
 }
 
 }  // namespace qmm

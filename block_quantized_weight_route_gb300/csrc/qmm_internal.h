@@ -150,15 +150,16 @@ struct Fp8a8Params {
     uint32_t* err;       // device error word
     int m_tiles, n_tiles;
 };
-// Which kernel takes a product, and the rows of the TMA boxes (128 codes wide) it
-// reads the activations and the weights in (0 rows: the kernel without TMA).
+// Which kernel takes a product: the pair kernel (many tokens) with its tile's columns,
+// or the narrow kernel (few) with its tile's tokens and the CTAs that share its K blocks.
 struct Fp8a8Plan {
     bool pair;
-    int bn;              // columns of a tile
-    int x_rows, w_rows;
+    int bn;      // pair: columns of a tile
+    int tn, cs;  // narrow
 };
 Fp8a8Plan fp8a8_plan(int M, int K, int N, bool gated, int sms);
-cudaError_t launch_fp8a8(const Fp8a8Params& p, bool gated, cudaStream_t s);
+cudaError_t launch_fp8a8_narrow(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, bool gated, int tn,
+                                int cs, cudaStream_t s);
 cudaError_t launch_fp8a8_pair(const CUtensorMap& tx, const CUtensorMap& tw, Fp8a8Params p, bool gated, int bn, int sms,
                               cudaStream_t s);
 
