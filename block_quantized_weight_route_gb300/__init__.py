@@ -229,9 +229,25 @@ def qmm_q8_0_q8_1(Xq, Xd, Wq, Wd, ws=None, fp32_out: bool = False) -> dict:
 
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 _F8 = (torch.float8_e4m3fn, torch.uint8, torch.int8)
+_F32 = (torch.float32,)
 
 
-def _need_rows(t: torch.Tensor, name: str, shape=None) -> torch.Tensor:
+def _check_tensors(*args) -> None:
+    """_need for each (tensor, name, dtypes, shape).  These calls take a few
+    microseconds on the GPU, so the checks that pass are made in one expression each;
+    _need words the error of one that does not."""
+    for t, name, dtypes, shape in args:
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.shape == shape and t.is_contiguous()):
+            _need(t, name, dtypes, shape)
+
+
+def _raw_stream(device):
+    """The current stream's handle, without making a Stream object."""
+    i = device.index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if i is None else i)
+
+
+def _need_rows(t: torch.Tensor, name: str, shape=None) -> None:
     """A CUDA matrix in fp32 or bf16 whose rows are contiguous (any row pitch)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -239,9 +255,8 @@ def _need_rows(t: torch.Tensor, name: str, shape=None) -> torch.Tensor:
         raise TypeError(f"{name} must have dtype in {tuple(_DTYPE)}, got {t.dtype}")
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be a matrix with contiguous rows")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return t
 
 
 def _pitch(t: torch.Tensor) -> int:
@@ -251,24 +266,24 @@ def _pitch(t: torch.Tensor) -> int:
 def _norm_args(X, G, R, eps, Rout, Y, bf16_out):
     """Checked arguments that the two norms share: (T, D, Rout, Y, the call's first 13 arguments)."""
     _need_rows(X, "X")
-    T, D = X.shape
-    _need(G, "G", tuple(_DTYPE), (D,))
+    T, D = shape = X.shape
+    _check_tensors((G, "G", _DTYPE, (D,)))
     if R is None:
         if Rout is not None:
             raise ValueError("Rout without R")
         res = (None, 0, None, 0, 0)
     else:
-        _need_rows(R, "R", (T, D))
+        _need_rows(R, "R", shape)
         if Rout is None:
             Rout = torch.empty((T, D), dtype=R.dtype, device=X.device)
-        _need_rows(Rout, "Rout", (T, D))
+        _need_rows(Rout, "Rout", shape)
         if Rout.dtype != R.dtype:
             raise TypeError("Rout must have R's dtype")
         res = (R.data_ptr(), _pitch(R), Rout.data_ptr(), _pitch(Rout), _DTYPE[R.dtype])
     if Y is None and bf16_out:
         Y = torch.empty((T, D), dtype=torch.bfloat16, device=X.device)
     if Y is not None:
-        _need(Y, "Y", _BF16, (T, D))
+        _check_tensors((Y, "Y", _BF16, (T, D)))
     args = (X.data_ptr(), _DTYPE[X.dtype], _pitch(X), *res, G.data_ptr(), _DTYPE[G.dtype], float(eps), T, D)
     return T, D, Rout, Y, args
 
@@ -283,12 +298,11 @@ def qmm_add_rmsnorm_fp8(X, G, R=None, eps: float = 1e-6, Rout=None, Q=None, S=No
     T, D, Rout, Y, args = _norm_args(X, G, R, eps, Rout, Y, bf16_out)
     if Q is None:
         Q = torch.empty((T, D), dtype=torch.float8_e4m3fn, device=X.device)
-    _need(Q, "Q", _F8, (T, D))
     if S is None:
         S = torch.empty((T, (D + 127) // 128), dtype=torch.float32, device=X.device)
-    _need(S, "S", (torch.float32,), (T, (D + 127) // 128))
+    _check_tensors((Q, "Q", _F8, (T, D)), (S, "S", _F32, (T, (D + 127) // 128)))
     _check("qmm_add_rmsnorm_fp8", lib().qmm_add_rmsnorm_fp8(*args, Q.data_ptr(), S.data_ptr(),
-                                                            None if Y is None else Y.data_ptr(), _stream(X.device)))
+                                                            None if Y is None else Y.data_ptr(), _raw_stream(X.device)))
     return dict(Q=Q, S=S, R=Rout, Y=Y)
 
 
@@ -300,7 +314,7 @@ def qmm_add_rmsnorm_q8_1(X, G, R=None, eps: float = 1e-6, Rout=None, Y=None, bf1
     Yd = torch.empty((T, D // 32), dtype=torch.int16, device=X.device)
     Ys = torch.empty((T, D // 32), dtype=torch.int16, device=X.device)
     _check("qmm_add_rmsnorm_q8_1", lib().qmm_add_rmsnorm_q8_1(*args, Yq.data_ptr(), Yd.data_ptr(), Ys.data_ptr(),
-                                                              None if Y is None else Y.data_ptr(), _stream(X.device)))
+                                                              None if Y is None else Y.data_ptr(), _raw_stream(X.device)))
     return dict(Yq=Yq, Yd=Yd, Ys=Ys, R=Rout, Y=Y)
 
 
@@ -310,17 +324,14 @@ def qmm_fp8a8_blk128(Xq, Xs, W, S, out_dtype=torch.bfloat16, Y=None):
     M, K = Xq.shape
     N = W.shape[0]
     kb = (K + 127) // 128
-    _need(Xq, "Xq", _F8, (M, K))
-    _need(Xs, "Xs", (torch.float32,), (M, kb))
-    _need(W, "W", _F8, (N, K))
-    _need(S, "S", (torch.float32,), ((N + 127) // 128, kb))
     if out_dtype not in _DTYPE:
         raise TypeError("out_dtype must be float32 or bfloat16")
     if Y is None:
         Y = torch.empty((M, N), dtype=out_dtype, device=Xq.device)
-    _need(Y, "Y", (out_dtype,), (M, N))
+    _check_tensors((Xq, "Xq", _F8, (M, K)), (Xs, "Xs", _F32, (M, kb)), (W, "W", _F8, (N, K)),
+                   (S, "S", _F32, ((N + 127) // 128, kb)), (Y, "Y", (out_dtype,), (M, N)))
     _check("qmm_fp8a8_blk128", lib().qmm_fp8a8_blk128(Xq.data_ptr(), Xs.data_ptr(), M, K, N, W.data_ptr(), S.data_ptr(),
-                                                      Y.data_ptr(), _DTYPE[out_dtype], _stream(Xq.device)))
+                                                      Y.data_ptr(), _DTYPE[out_dtype], _raw_stream(Xq.device)))
     return Y
 
 
@@ -331,19 +342,15 @@ def qmm_fp8a8_swiglu_blk128(Xq, Xs, Wgu, Sgu, Hq=None, Hs=None):
     M, K = Xq.shape
     F = Wgu.shape[0] // 2
     kb = (K + 127) // 128
-    _need(Xq, "Xq", _F8, (M, K))
-    _need(Xs, "Xs", (torch.float32,), (M, kb))
-    _need(Wgu, "Wgu", _F8, (2 * F, K))
-    _need(Sgu, "Sgu", (torch.float32,), (2 * F // 128, kb))
     if Hq is None:
         Hq = torch.empty((M, F), dtype=torch.float8_e4m3fn, device=Xq.device)
-    _need(Hq, "Hq", _F8, (M, F))
     if Hs is None:
         Hs = torch.empty((M, F // 128), dtype=torch.float32, device=Xq.device)
-    _need(Hs, "Hs", (torch.float32,), (M, F // 128))
+    _check_tensors((Xq, "Xq", _F8, (M, K)), (Xs, "Xs", _F32, (M, kb)), (Wgu, "Wgu", _F8, (2 * F, K)),
+                   (Sgu, "Sgu", _F32, (2 * F // 128, kb)), (Hq, "Hq", _F8, (M, F)), (Hs, "Hs", _F32, (M, F // 128)))
     _check("qmm_fp8a8_swiglu_blk128", lib().qmm_fp8a8_swiglu_blk128(Xq.data_ptr(), Xs.data_ptr(), M, K, F,
                                                                     Wgu.data_ptr(), Sgu.data_ptr(), Hq.data_ptr(),
-                                                                    Hs.data_ptr(), _stream(Xq.device)))
+                                                                    Hs.data_ptr(), _raw_stream(Xq.device)))
     return Hq, Hs
 
 

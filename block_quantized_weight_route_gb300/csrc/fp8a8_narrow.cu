@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(C::THREADS)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    launch_dependents();
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(&full[i], 1);
@@ -101,6 +102,7 @@ __global__ void __launch_bounds__(C::THREADS)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    wait_prerequisites();
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const int cs = (int)gridDim.x, rank = (int)blockIdx.x;   // one cluster per row of the grid
     const int n0 = (int)blockIdx.y * 128, m0 = (int)blockIdx.z * C::TN;
@@ -317,33 +319,67 @@ __global__ void __launch_bounds__(C::THREADS)
 }
 
 template <class C>
-cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, int cs, cudaStream_t s) {
+cudaError_t prepare(int* dev) {
     static bool ready[64] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    cudaError_t e = cudaGetDevice(dev);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!ready[dev]) {
+    if (*dev < 0 || *dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[*dev]) {
         e = cudaFuncSetAttribute(fp8a8_narrow_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
-        ready[dev] = true;
+        ready[*dev] = true;
     }
+    return cudaSuccess;
+}
+
+template <class C>
+cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, int cs, cudaStream_t s) {
+    int dev = 0;
+    const cudaError_t e = prepare<C>(&dev);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = cs;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1] = overlap_attribute();
     cfg.gridDim = dim3(cs, (p.N + 127) / 128, (p.M + C::TN - 1) / C::TN);
     cfg.blockDim = dim3(C::THREADS, 1, 1);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, fp8a8_narrow_kernel<C>, tx, tw, p);
 }
 
 }  // namespace
+
+// (Every configuration has one CTA on an SM, so any one of them answers for all; a
+// cluster's CTAs are on SMs of one group of SMs, so fewer fit than SMs / cs.)
+int fp8a8_narrow_at_once(int cs) {
+    using C = NarrowCfg<16, false>;
+    static int at_once[64][9] = {};
+    int dev = 0;
+    if (cs < 1 || cs > 8 || prepare<C>(&dev) != cudaSuccess) return 0;
+    if (at_once[dev][cs] == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = cs;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(cs, 64, 1);
+        cfg.blockDim = dim3(C::THREADS, 1, 1);
+        cfg.dynamicSmemBytes = C::SMEM;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, fp8a8_narrow_kernel<C>, &cfg) != cudaSuccess || n < 1) return 0;
+        at_once[dev][cs] = n;
+    }
+    return at_once[dev][cs];
+}
 
 cudaError_t launch_fp8a8_narrow(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, bool gated, int tn,
                                 int cs, cudaStream_t s) {

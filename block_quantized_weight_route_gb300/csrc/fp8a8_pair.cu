@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
     // (read through a shuffle, so that the compiler knows it and the TMEM addresses made
     // from it to be the same in the whole warp)
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    launch_dependents();
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(&full[i], 1);
@@ -110,6 +111,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
     if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
+    wait_prerequisites();
     cluster_sync();   // the peer's barriers are initialised before any copy or commit signals them
     tc_fence_after();
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
@@ -375,16 +377,17 @@ cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Para
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1] = overlap_attribute();
     cfg.blockDim = dim3(C::THREADS, 1, 1);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     if (most[dev] == 0) {
         cfg.gridDim = dim3(2 * (sms / 2), 1, 1);
         int n = 0;

@@ -33,8 +33,10 @@ Fp8a8Plan fp8a8_plan(int M, int K, int N, bool gated, int sms) {
             Fp8a8Plan pl{};
             pl.tn = tns[i];
             pl.cs = cs;
-            // (clusters of cs CTAs; adding up costs a little for each)
-            consider(pl, tiles, sms / cs, 2.2 + 0.1 * cs, (kbs + cs - 1) / cs, narrow_kb[gated][i]);
+            const int at_once = fp8a8_narrow_at_once(cs);
+            if (at_once < 1) continue;
+            // (adding up costs a little for each CTA of a cluster)
+            consider(pl, tiles, at_once, 2.2 + 0.1 * cs, (kbs + cs - 1) / cs, narrow_kb[gated][i]);
         }
     }
     static const int bns[3] = {256, 192, 128};

@@ -15,6 +15,20 @@
 
 namespace qmm {
 
+// Launches of these kernels overlap (programmatic dependent launch): a kernel says at
+// its start that the next one may be started, and before its first access to global
+// memory waits until the one before has finished and its writes are visible.  One
+// after the other, a kernel's start (barriers, TMEM, descriptors) and its launch then
+// run beside the end of the one before: 0.5 to 1 us a call.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+inline cudaLaunchAttribute overlap_attribute() {
+    cudaLaunchAttribute a = {};
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    return a;
+}
+
 // max that hands a NaN on (fmaxf drops it): a group with a NaN has a NaN scale
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;

@@ -52,6 +52,8 @@ __device__ __forceinline__ float lanes_max(float a) {
 template <bool Q81, int NV>
 __global__ void __launch_bounds__(kThreads) rmsnorm8_kernel(NormParams p) {
     __shared__ float part[kThreads / 32];
+    launch_dependents();
+    wait_prerequisites();
     const long t = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float v[NV][8];
@@ -151,12 +153,18 @@ __global__ void __launch_bounds__(kThreads) rmsnorm8_kernel(NormParams p) {
 
 template <bool Q81>
 cudaError_t launch(const NormParams& p, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1] = {overlap_attribute()};
+    cfg.gridDim = dim3(p.T, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     const int nv = (p.D + kThreads * 8 - 1) / (kThreads * 8);
-    if (nv <= 1) rmsnorm8_kernel<Q81, 1><<<p.T, kThreads, 0, s>>>(p);
-    else if (nv <= 2) rmsnorm8_kernel<Q81, 2><<<p.T, kThreads, 0, s>>>(p);
-    else if (nv <= 4) rmsnorm8_kernel<Q81, 4><<<p.T, kThreads, 0, s>>>(p);
-    else rmsnorm8_kernel<Q81, 8><<<p.T, kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    if (nv <= 1) return cudaLaunchKernelEx(&cfg, rmsnorm8_kernel<Q81, 1>, p);
+    if (nv <= 2) return cudaLaunchKernelEx(&cfg, rmsnorm8_kernel<Q81, 2>, p);
+    if (nv <= 4) return cudaLaunchKernelEx(&cfg, rmsnorm8_kernel<Q81, 4>, p);
+    return cudaLaunchKernelEx(&cfg, rmsnorm8_kernel<Q81, 8>, p);
 }
 
 }  // namespace
