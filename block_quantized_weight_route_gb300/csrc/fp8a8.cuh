@@ -73,30 +73,6 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) {
                  : "memory");
 }
 
-// Two fp32 values in one 64-bit register, and their packed multiply-add.
-__device__ __forceinline__ uint64_t pack2u(uint32_t a, uint32_t b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t pack2(float a, float b) { return pack2u(__float_as_uint(a), __float_as_uint(b)); }
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-    uint32_t a, b;
-    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
-    return make_float2(__uint_as_float(a), __uint_as_float(b));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // Wait (bounded) for the completion of the `issued` most recent fills of a ring.
 __device__ __forceinline__ void drain_ring(uint64_t* full, long issued, int stages, uint32_t* err) {
     const long pending = issued < stages ? issued : stages;

@@ -302,13 +302,12 @@ __global__ void __launch_bounds__(C::THREADS)
         } else {
             const float4 u = cluster_sum(a + C::TN * 512, cs);
             const float h[4] = {swiglu(y.x, u.x), swiglu(y.y, u.y), swiglu(y.z, u.z), swiglu(y.w, u.w)};
-            float top = max_nan(max_nan(fabsf(h[0]), fabsf(h[1])), max_nan(fabsf(h[2]), fabsf(h[3])));
+            float top = max_nan_abs(max_nan_abs(h[0], h[1], h[2]), h[3], 0.0f);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float s = top / 448.0f;
-            const GroupScale gs = group_scale(s);
+            const GroupScale gs = group_scale<448>(top);
             *reinterpret_cast<uint32_t*>(p.Hq + m * p.N + n) = e4m3x4(gs(h[0]), gs(h[1]), gs(h[2]), gs(h[3]));
-            if (lane == 0) p.Hs[m * (p.N / 128) + n0 / 128] = s;
+            if (lane == 0) p.Hs[m * (p.N / 128) + n0 / 128] = gs.s;
         }
     }
     cluster_sync();   // no CTA leaves while another may read its sums

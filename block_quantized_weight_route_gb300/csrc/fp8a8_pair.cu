@@ -6,7 +6,7 @@
 // Persistent CTA pairs (cta_group::2), each on one 256 x BN tile: the even CTA
 // issues M = 256, N = BN, K = 32 MMAs over both CTAs' shared memory, each CTA's
 // TMEM holds its 128 rows x BN columns of P_kb.  A block's sum cannot stay in the
-// tensor core (its scale differs by row and by block), so eight warps fold each
+// tensor core (its scale differs by row and by block), so 16 warps fold each
 // P_kb into fp32 running sums in registers, two TMEM buffers apart from the MMA.
 //   warp 0: TMA producer   warp 1: MMA issuer (even CTA)
 //   warps 2, 3: the scales of four K blocks at a time, by asynchronous copies into a ring
@@ -16,9 +16,11 @@
 // the even CTA takes longer than the other buffer's MMA (512 cycles at BN = 256), so the
 // length of the fold's path counts, not its throughput: 16 warps rather than 8, TMEM loads
 // of 8 columns (5268 x 17408 x 5120: 388 us; of 16: 428, of 4: 578; BN = 192, whose path is
-// shorter: 16), four K blocks
-// unrolled and no spilled registers.  At 2.4 PFLOP/s the power limit is near: without any
-// fold the same loop reaches 3.0 PFLOP/s at clocks down to 1.6 GHz.
+// shorter: 16), four K blocks unrolled and no spilled registers.  Not kept: three buffers
+// of 160 columns with 20 fold warps (300 x 5120 x 5120 20.7 us against 21.8, but 72 against 56
+// at 2048 tokens), halves of the tile with MMAs and warps of their own, polling instead
+// of sleeping waits (5% slower).  At 2.4 PFLOP/s the power limit is near: without any fold
+// the same loop reaches 3.0 PFLOP/s at clocks down to 1.6 GHz.
 #include "fp8a8.cuh"
 
 namespace qmm {
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
                     uint64_t& y = acc[j / 8][j % 8];
                     const float2 g = unpack2(y), u = unpack2(acc[HP + j / 8][j % 8]);
                     const float h0 = swiglu(g.x, u.x), h1 = swiglu(g.y, u.y);
-                    a = max_nan(a, max_nan(fabsf(h0), fabsf(h1)));
+                    a = max_nan_abs(a, h0, h1);
                     y = pack2(h0, h1);
                 }
                 float* rm = rowmax + parity * 512 + row;
@@ -215,15 +217,14 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
                 rph ^= (uint32_t)parity;
 #pragma unroll
                 for (int i = 0; i < C::GROUPS; ++i) a = max_nan(a, rm[i * 128]);
-                const float s = a / 448.0f;
-                const GroupScale gs = group_scale(s);
+                const GroupScale gs = group_scale<448>(a);
                 if (grow < p.M) {
                     uint4* dst = reinterpret_cast<uint4*>(p.Hq + grow * p.N + ti.n0 + cq * (C::CW / 2));
 #pragma unroll
                     for (int j = 0; j < HP; ++j)
                         dst[j] = make_uint4(codes4(gs, acc[j][0], acc[j][1]), codes4(gs, acc[j][2], acc[j][3]),
                                             codes4(gs, acc[j][4], acc[j][5]), codes4(gs, acc[j][6], acc[j][7]));
-                    if (cq == 0) p.Hs[grow * (p.N / 128) + ti.n0 / 128] = s;
+                    if (cq == 0) p.Hs[grow * (p.N / 128) + ti.n0 / 128] = gs.s;
                 }
             }
         }
@@ -375,6 +376,12 @@ cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Para
     if (most[dev] == 0) {
         e = cudaFuncSetAttribute(fp8a8_pair_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
+        // the warpgroups' register shares add up to the launch's: launch only if the kernel
+        // is allocated exactly that many (a setmaxnreg.inc past the pool waits)
+        cudaFuncAttributes fa{};
+        e = cudaFuncGetAttributes(&fa, fp8a8_pair_kernel<C>);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs != C::REGS) return cudaErrorInvalidConfiguration;
     }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];

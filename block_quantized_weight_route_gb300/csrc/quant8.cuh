@@ -35,6 +35,40 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+// the same over the magnitudes of three
+__device__ __forceinline__ float max_nan_abs(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Two fp32 values in one 64-bit register, and packed arithmetic on them.
+__device__ __forceinline__ uint64_t pack2u(uint32_t a, uint32_t b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) { return pack2u(__float_as_uint(a), __float_as_uint(b)); }
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    uint32_t a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+    return make_float2(__uint_as_float(a), __uint_as_float(b));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 
 // Four values to E4M3 codes, the first in the low byte; finite values past +-448
 // saturate, NaN stays NaN (0x7F).
@@ -44,20 +78,25 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return lo | (hi << 16);
 }
 
-// The factor that turns a group's values into code units.  y / s is formed as
-// y * (1 / s), within 1.5 ulp of the quotient: a code moves only where y / s lies
-// that close to a rounding boundary.  Below 2^-120 the reciprocal could leave the
-// fp32 range, so such a (denormal or nearly) group is scaled up by 2^120 first.
+// The scale of a group, top / LEVELS, and the factor 1 / scale that turns its values
+// into code units.  Both divisions are products with a reciprocal (1 / LEVELS rounded;
+// the reciprocal instruction, within an ulp), so the scale is within 1 ulp and a quotient
+// within 3 ulp of the formula's: a code moves only where y / s lies that close to a
+// rounding boundary.  A scale below 2^-120, whose reciprocal could leave the fp32 range,
+// has up = 2^120: such a group's values are multiplied by it first.
 struct GroupScale {
-    float pre, inv;
-    __device__ __forceinline__ float operator()(float y) const { return y * pre * inv; }
+    float s, inv, up;
+    __device__ __forceinline__ bool tiny() const { return up != 1.0f; }
+    __device__ __forceinline__ float operator()(float y) const { return y * up * inv; }
 };
-__device__ __forceinline__ GroupScale group_scale(float s) {
-    constexpr float kUp = 1.329227995784916e36f;   // 2^120
+template <int LEVELS>
+__device__ __forceinline__ GroupScale group_scale(float top) {
     GroupScale g;
-    const bool tiny = s < 7.52316384526264e-37f;   // 2^-120
-    g.pre = tiny ? kUp : 1.0f;
-    g.inv = (s == 0.0f) ? 0.0f : 1.0f / (s * g.pre);
+    g.s = top * (1.0f / LEVELS);
+    g.up = g.s < 7.52316384526264e-37f ? 1.329227995784916e36f : 1.0f;   // 2^-120, 2^120
+    float x = g.s * g.up;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(g.inv) : "f"(x));
+    if (g.s == 0.0f) g.inv = 0.0f;
     return g;
 }
 
