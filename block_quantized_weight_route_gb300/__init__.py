@@ -232,60 +232,59 @@ _F8 = (torch.float8_e4m3fn, torch.uint8, torch.int8)
 _F32 = (torch.float32,)
 
 
-def _check_tensors(*args) -> None:
-    """_need for each (tensor, name, dtypes, shape).  These calls take a few
-    microseconds on the GPU, so the checks that pass are made in one expression each;
-    _need words the error of one that does not."""
-    for t, name, dtypes, shape in args:
-        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.shape == shape and t.is_contiguous()):
-            _need(t, name, dtypes, shape)
+def _ok(t, dtypes, shape) -> bool:
+    """Whether _need would pass.  The calls below take a few microseconds on the GPU, so
+    what passes is checked in one expression; _need words the error of what does not."""
+    return isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.shape == shape and t.is_contiguous()
 
 
-def _raw_stream(device):
+def _raw_stream(device) -> int:
     """The current stream's handle, without making a Stream object."""
     i = device.index
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if i is None else i)
 
 
-def _need_rows(t: torch.Tensor, name: str, shape=None) -> None:
-    """A CUDA matrix in fp32 or bf16 whose rows are contiguous (any row pitch)."""
+def _pitch(t: torch.Tensor, name: str, shape) -> int:
+    """The row pitch of a CUDA matrix in fp32 or bf16 whose rows are contiguous."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in _DTYPE and t.shape == shape and t.dim() == 2:
+        if t.is_contiguous():
+            return shape[1]
+        if t.stride(1) == 1:
+            return t.stride(0)
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in _DTYPE:
         raise TypeError(f"{name} must have dtype in {tuple(_DTYPE)}, got {t.dtype}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dim() != 2 or t.shape == shape:
         raise ValueError(f"{name} must be a matrix with contiguous rows")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-
-
-def _pitch(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def _norm_args(X, G, R, eps, Rout, Y, bf16_out):
-    """Checked arguments that the two norms share: (T, D, Rout, Y, the call's first 13 arguments)."""
-    _need_rows(X, "X")
-    T, D = shape = X.shape
-    _check_tensors((G, "G", _DTYPE, (D,)))
+    """Checked arguments that the two norms share: (X's shape, Rout, Y, the call's first 13 arguments)."""
+    shape = X.shape
+    ldx = _pitch(X, "X", shape)
+    T, D = shape
+    if not _ok(G, _DTYPE, (D,)):
+        _need(G, "G", _DTYPE, (D,))
+    if Y is None:
+        if bf16_out:
+            Y = torch.empty((T, D), dtype=torch.bfloat16, device=X.device)
+    elif not _ok(Y, _BF16, shape):
+        _need(Y, "Y", _BF16, shape)
     if R is None:
         if Rout is not None:
             raise ValueError("Rout without R")
-        res = (None, 0, None, 0, 0)
-    else:
-        _need_rows(R, "R", shape)
-        if Rout is None:
-            Rout = torch.empty((T, D), dtype=R.dtype, device=X.device)
-        _need_rows(Rout, "Rout", shape)
-        if Rout.dtype != R.dtype:
-            raise TypeError("Rout must have R's dtype")
-        res = (R.data_ptr(), _pitch(R), Rout.data_ptr(), _pitch(Rout), _DTYPE[R.dtype])
-    if Y is None and bf16_out:
-        Y = torch.empty((T, D), dtype=torch.bfloat16, device=X.device)
-    if Y is not None:
-        _check_tensors((Y, "Y", _BF16, (T, D)))
-    args = (X.data_ptr(), _DTYPE[X.dtype], _pitch(X), *res, G.data_ptr(), _DTYPE[G.dtype], float(eps), T, D)
-    return T, D, Rout, Y, args
+        return shape, None, Y, (X.data_ptr(), _DTYPE[X.dtype], ldx, None, 0, None, 0, 0, G.data_ptr(),
+                                _DTYPE[G.dtype], eps, T, D)
+    ldr = _pitch(R, "R", shape)
+    if Rout is None:
+        Rout = torch.empty((T, D), dtype=R.dtype, device=X.device)
+    ldro = _pitch(Rout, "Rout", shape)
+    if Rout.dtype != R.dtype:
+        raise TypeError("Rout must have R's dtype")
+    return shape, Rout, Y, (X.data_ptr(), _DTYPE[X.dtype], ldx, R.data_ptr(), ldr, Rout.data_ptr(), ldro,
+                            _DTYPE[R.dtype], G.data_ptr(), _DTYPE[G.dtype], eps, T, D)
 
 
 def qmm_add_rmsnorm_fp8(X, G, R=None, eps: float = 1e-6, Rout=None, Q=None, S=None, Y=None,
@@ -295,27 +294,46 @@ def qmm_add_rmsnorm_fp8(X, G, R=None, eps: float = 1e-6, Rout=None, Q=None, S=No
     G are fp32 or bf16; X, R and Rout may be row slices.  Rout=R adds in place.
     bf16_out (or Y given): the normalised rows in bf16 too.  Returns Q, S, R
     (Rout, or None) and Y (or None)."""
-    T, D, Rout, Y, args = _norm_args(X, G, R, eps, Rout, Y, bf16_out)
+    shape, Rout, Y, args = _norm_args(X, G, R, eps, Rout, Y, bf16_out)
+    groups = (shape[0], (shape[1] + 127) // 128)
     if Q is None:
-        Q = torch.empty((T, D), dtype=torch.float8_e4m3fn, device=X.device)
+        Q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=X.device)
+    elif not _ok(Q, _F8, shape):
+        _need(Q, "Q", _F8, shape)
     if S is None:
-        S = torch.empty((T, (D + 127) // 128), dtype=torch.float32, device=X.device)
-    _check_tensors((Q, "Q", _F8, (T, D)), (S, "S", _F32, (T, (D + 127) // 128)))
-    _check("qmm_add_rmsnorm_fp8", lib().qmm_add_rmsnorm_fp8(*args, Q.data_ptr(), S.data_ptr(),
-                                                            None if Y is None else Y.data_ptr(), _raw_stream(X.device)))
-    return dict(Q=Q, S=S, R=Rout, Y=Y)
+        S = torch.empty(groups, dtype=torch.float32, device=X.device)
+    elif not _ok(S, _F32, groups):
+        _need(S, "S", _F32, groups)
+    st = lib().qmm_add_rmsnorm_fp8(*args, Q.data_ptr(), S.data_ptr(), None if Y is None else Y.data_ptr(),
+                                   _raw_stream(X.device))
+    if st:
+        _check("qmm_add_rmsnorm_fp8", st)
+    return {"Q": Q, "S": S, "R": Rout, "Y": Y}
 
 
 def qmm_add_rmsnorm_q8_1(X, G, R=None, eps: float = 1e-6, Rout=None, Y=None, bf16_out: bool = False) -> dict:
     """qmm_add_rmsnorm_fp8 with the rows as q8_1 blocks of 32 (what qmm_q8_0_q8_1
     takes): Yq int8 [T, D], Yd / Ys fp16 bits [T, D/32], R and Y as there."""
-    T, D, Rout, Y, args = _norm_args(X, G, R, eps, Rout, Y, bf16_out)
+    (T, D), Rout, Y, args = _norm_args(X, G, R, eps, Rout, Y, bf16_out)
     Yq = torch.empty((T, D), dtype=torch.int8, device=X.device)
     Yd = torch.empty((T, D // 32), dtype=torch.int16, device=X.device)
     Ys = torch.empty((T, D // 32), dtype=torch.int16, device=X.device)
-    _check("qmm_add_rmsnorm_q8_1", lib().qmm_add_rmsnorm_q8_1(*args, Yq.data_ptr(), Yd.data_ptr(), Ys.data_ptr(),
-                                                              None if Y is None else Y.data_ptr(), _raw_stream(X.device)))
-    return dict(Yq=Yq, Yd=Yd, Ys=Ys, R=Rout, Y=Y)
+    st = lib().qmm_add_rmsnorm_q8_1(*args, Yq.data_ptr(), Yd.data_ptr(), Ys.data_ptr(),
+                                    None if Y is None else Y.data_ptr(), _raw_stream(X.device))
+    if st:
+        _check("qmm_add_rmsnorm_q8_1", st)
+    return {"Yq": Yq, "Yd": Yd, "Ys": Ys, "R": Rout, "Y": Y}
+
+
+def _need_operands(Xq, Xs, W, S, M: int, K: int, rows: int, blocks: int, name_w: str, name_s: str) -> None:
+    """The operands of the two FP8 x FP8 products."""
+    kb = (K + 127) // 128
+    if not (_ok(Xq, _F8, (M, K)) and _ok(Xs, _F32, (M, kb)) and _ok(W, _F8, (rows, K)) and
+            _ok(S, _F32, (blocks, kb))):
+        _need(Xq, "Xq", _F8, (M, K))
+        _need(Xs, "Xs", _F32, (M, kb))
+        _need(W, name_w, _F8, (rows, K))
+        _need(S, name_s, _F32, (blocks, kb))
 
 
 def qmm_fp8a8_blk128(Xq, Xs, W, S, out_dtype=torch.bfloat16, Y=None):
@@ -323,15 +341,17 @@ def qmm_fp8a8_blk128(Xq, Xs, W, S, out_dtype=torch.bfloat16, Y=None):
     Xq [M, K] and W [N, K] E4M3, Xs [M, ceil(K/128)] and S [ceil(N/128), ceil(K/128)] fp32."""
     M, K = Xq.shape
     N = W.shape[0]
-    kb = (K + 127) // 128
     if out_dtype not in _DTYPE:
         raise TypeError("out_dtype must be float32 or bfloat16")
+    _need_operands(Xq, Xs, W, S, M, K, N, (N + 127) // 128, "W", "S")
     if Y is None:
         Y = torch.empty((M, N), dtype=out_dtype, device=Xq.device)
-    _check_tensors((Xq, "Xq", _F8, (M, K)), (Xs, "Xs", _F32, (M, kb)), (W, "W", _F8, (N, K)),
-                   (S, "S", _F32, ((N + 127) // 128, kb)), (Y, "Y", (out_dtype,), (M, N)))
-    _check("qmm_fp8a8_blk128", lib().qmm_fp8a8_blk128(Xq.data_ptr(), Xs.data_ptr(), M, K, N, W.data_ptr(), S.data_ptr(),
-                                                      Y.data_ptr(), _DTYPE[out_dtype], _raw_stream(Xq.device)))
+    elif not _ok(Y, (out_dtype,), (M, N)):
+        _need(Y, "Y", (out_dtype,), (M, N))
+    st = lib().qmm_fp8a8_blk128(Xq.data_ptr(), Xs.data_ptr(), M, K, N, W.data_ptr(), S.data_ptr(), Y.data_ptr(),
+                                _DTYPE[out_dtype], _raw_stream(Xq.device))
+    if st:
+        _check("qmm_fp8a8_blk128", st)
     return Y
 
 
@@ -341,16 +361,19 @@ def qmm_fp8a8_swiglu_blk128(Xq, Xs, Wgu, Sgu, Hq=None, Hs=None):
     rows first), Sgu [2F/128, ceil(K/128)] fp32."""
     M, K = Xq.shape
     F = Wgu.shape[0] // 2
-    kb = (K + 127) // 128
+    _need_operands(Xq, Xs, Wgu, Sgu, M, K, 2 * F, 2 * F // 128, "Wgu", "Sgu")
     if Hq is None:
         Hq = torch.empty((M, F), dtype=torch.float8_e4m3fn, device=Xq.device)
+    elif not _ok(Hq, _F8, (M, F)):
+        _need(Hq, "Hq", _F8, (M, F))
     if Hs is None:
         Hs = torch.empty((M, F // 128), dtype=torch.float32, device=Xq.device)
-    _check_tensors((Xq, "Xq", _F8, (M, K)), (Xs, "Xs", _F32, (M, kb)), (Wgu, "Wgu", _F8, (2 * F, K)),
-                   (Sgu, "Sgu", _F32, (2 * F // 128, kb)), (Hq, "Hq", _F8, (M, F)), (Hs, "Hs", _F32, (M, F // 128)))
-    _check("qmm_fp8a8_swiglu_blk128", lib().qmm_fp8a8_swiglu_blk128(Xq.data_ptr(), Xs.data_ptr(), M, K, F,
-                                                                    Wgu.data_ptr(), Sgu.data_ptr(), Hq.data_ptr(),
-                                                                    Hs.data_ptr(), _raw_stream(Xq.device)))
+    elif not _ok(Hs, _F32, (M, F // 128)):
+        _need(Hs, "Hs", _F32, (M, F // 128))
+    st = lib().qmm_fp8a8_swiglu_blk128(Xq.data_ptr(), Xs.data_ptr(), M, K, F, Wgu.data_ptr(), Sgu.data_ptr(),
+                                       Hq.data_ptr(), Hs.data_ptr(), _raw_stream(Xq.device))
+    if st:
+        _check("qmm_fp8a8_swiglu_blk128", st)
     return Hq, Hs
 
 
