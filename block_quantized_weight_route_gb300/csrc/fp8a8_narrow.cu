@@ -12,6 +12,9 @@
 // the same result every call.
 //   warp 0: TMA producer   warp 1: MMA issuer   warp 2: scales (asynchronous copies)
 //   warps 4..: fold, four warps for each 128 weight rows and 32 tokens
+// With 128 tokens a tile (TOKENS_M) the tokens are the M side and the weights the N side:
+// swapped, every fold thread reads every token's scale from shared memory, 512 cycles a
+// K block for 128 tokens; with a token per lane it reads one.
 #include "fp8a8.cuh"
 
 namespace qmm {
@@ -20,21 +23,24 @@ namespace {
 template <int TN_, bool GATED_>
 struct NarrowCfg {
     static constexpr int TN = TN_, MATS = GATED_ ? 2 : 1;
-    static constexpr bool GATED = GATED_;
+    static constexpr bool GATED = GATED_, TOKENS_M = TN == 128;
     static constexpr int W_BYTES = MATS * 128 * 128, X_BYTES = TN * 128, STAGE_BYTES = W_BYTES + X_BYTES;
     static constexpr int STAGES = 196608 / STAGE_BYTES > 10 ? 10 : 196608 / STAGE_BYTES;
-    static constexpr int ACC_COLS = TN * MATS, TMEM_COLS = ACC_COLS <= 32 ? 128 : ACC_COLS <= 64 ? 256 : 512;
+    static constexpr int ACC_COLS = TN * MATS;
+    static_assert(!TOKENS_M || !GATED, "tokens on the M side: 128 x 128 tiles");
+    static constexpr int TMEM_COLS = ACC_COLS <= 32 ? 128 : ACC_COLS <= 64 ? 256 : 512;
     static constexpr int NBUF_RAW = TMEM_COLS / ACC_COLS, NBUF = NBUF_RAW < STAGES ? NBUF_RAW : (STAGES & ~1);
     static constexpr int SC_SLOTS = 4, SC_KB = 4, SC_PITCH = TN + 4, SC_FLOATS = SC_SLOTS * SC_KB * SC_PITCH;
     // fold warps: four (the lanes) x the matrices x token groups of at most 32
-    static constexpr int CW = TN < 32 ? TN : 32, TG = TN / CW, LW = 16;   // columns of a thread, of a load
-    static constexpr int FOLD_WARPS = 4 * MATS * TG, THREADS = 128 + 32 * FOLD_WARPS;
+    static constexpr int CW = TN < 32 ? TN : 32, TG = TN / CW;
+    static constexpr int FOLD_WARPS = TOKENS_M ? 16 : 4 * MATS * TG, THREADS = 128 + 32 * FOLD_WARPS;
     static constexpr int COPIES = MATS + 1;
     static_assert(COPIES * STAGES <= 32, "a lane per copy");
     static constexpr int BARS = 2 * STAGES + NBUF + 2 * SC_SLOTS + 1;
     static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + SC_FLOATS * 4 + BARS * 8 + 64;
     static_assert(SMEM <= 232448, "shared memory");
     static_assert(TN * 128 * 4 * MATS <= STAGES * STAGE_BYTES, "the sums fit the stages");
+    static_assert(!TOKENS_M || SC_KB % NBUF == 0, "buffer = K block's place in its slot");
     static_assert(NBUF >= 1 && NBUF <= STAGES, "a stage's MMA barrier completes again only after its accumulator was read");
 };
 
@@ -61,6 +67,144 @@ __device__ __forceinline__ float4 cluster_sum(uint32_t local, int cs) {
         v.w += x.w;
     }
     return v;
+}
+
+// The fold of a warp, weights on the M side: lane = weight row, `acc` the tokens.
+template <class C>
+__device__ __forceinline__ void fold_weights_m(const Fp8a8Params& p, int warp, int lane, int kb0, int kb1, uint32_t tmem_base,
+                                               const float* sc, float* sums, uint64_t* done, uint64_t* acc_empty,
+                                               uint64_t* sc_full, uint64_t* sc_empty, volatile int* abort_flag) {
+    constexpr int LD = 16;   // columns of a TMEM load
+    const int set = (warp - 4) >> 2, q = warp & 3, row = q * 32 + lane;
+    const int mat = set % C::MATS, tg = set / C::MATS;
+    const uint32_t lane_addr = tmem_base + ((uint32_t)(q * 32) << 16) + mat * C::TN + tg * C::CW;
+    int st = 0, slot = 0, buf = 0;
+    uint32_t ph = 0, sph = 0;
+    bool ok = true;
+    uint64_t acc[C::CW / 2];
+#pragma unroll
+    for (int j = 0; j < C::CW / 2; ++j) acc[j] = 0;
+    for (int kb = kb0; kb < kb1 && ok; kb += C::SC_KB) {
+        if (!mbar_wait(&sc_full[slot], sph, abort_flag, p.err, DEV_TIMEOUT_CONV)) break;
+#pragma unroll
+        for (int k = 0; k < C::SC_KB; ++k) {
+            if (kb + k >= kb1) break;
+            const float* scr = sc + (slot * C::SC_KB + k) * C::SC_PITCH;
+            const float sw = scr[C::TN + mat];
+            const uint64_t sw2 = pack2(sw, sw);
+            const ulonglong2* sx = reinterpret_cast<const ulonglong2*>(scr + tg * C::CW);
+            if (!mbar_wait(&done[st], ph, abort_flag, p.err, DEV_TIMEOUT_ACC)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t a0 = lane_addr + (uint32_t)(buf * C::ACC_COLS);
+#pragma unroll
+            for (int x = 0; x < C::CW; x += LD) {
+                uint32_t r[LD];
+                tmem_ld(a0 + x, r);
+                tmem_ld_wait();
+                if (x + LD == C::CW) {
+                    // every column is in registers: the MMA may write the buffer again
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&acc_empty[buf]);
+                }
+#pragma unroll
+                for (int j = 0; j < LD / 4; ++j) {
+                    const ulonglong2 s = sx[x / 4 + j];   // four tokens' scales
+                    uint64_t& y0 = acc[x / 2 + 2 * j];
+                    uint64_t& y1 = acc[x / 2 + 2 * j + 1];
+                    y0 = fma2(pack2u(r[4 * j], r[4 * j + 1]), mul2(s.x, sw2), y0);
+                    y1 = fma2(pack2u(r[4 * j + 2], r[4 * j + 3]), mul2(s.y, sw2), y1);
+                }
+            }
+            if (++buf == C::NBUF) buf = 0;
+            if (++st == C::STAGES) {
+                st = 0;
+                ph ^= 1u;
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc_empty[slot]);
+        if (++slot == C::SC_SLOTS) {
+            slot = 0;
+            sph ^= 1u;
+        }
+    }
+    // This warp saw the last K block's barrier: every MMA is complete, so every copy has
+    // landed and been read, and the stages become the sums' buffer.  (After a time-out
+    // the sums mean nothing.)
+#pragma unroll
+    for (int j = 0; j < C::CW / 2; ++j) {
+        const float2 f = unpack2(acc[j]);
+        float* dst = sums + (mat * C::TN + tg * C::CW + 2 * j) * 128 + row;
+        dst[0] = f.x;
+        dst[128] = f.y;
+    }
+}
+
+// Tokens on the M side: lane = token, `acc` 32 weight rows.
+template <class C>
+__device__ __forceinline__ void fold_tokens_m(const Fp8a8Params& p, int warp, int lane, int kb0, int kb1, uint32_t tmem_base,
+                                              const float* sc, float* sums, uint64_t* done, uint64_t* acc_empty,
+                                              uint64_t* sc_full, uint64_t* sc_empty, volatile int* abort_flag) {
+    constexpr int COLS = 32, LD = 32;   // weight rows of a thread; columns of a TMEM load
+    const int q = warp & 3, cg = (warp - 4) >> 2, row = q * 32 + lane;
+    const uint32_t lane_addr = tmem_base + ((uint32_t)(q * 32) << 16) + cg * 32;
+    int st = 0, slot = 0;
+    uint32_t ph = 0, sph = 0;
+    bool ok = true;
+    uint64_t acc[COLS / 2];
+#pragma unroll
+    for (int j = 0; j < COLS / 2; ++j) acc[j] = 0;
+    for (int kb = kb0; kb < kb1 && ok; kb += C::SC_KB) {
+        if (!mbar_wait(&sc_full[slot], sph, abort_flag, p.err, DEV_TIMEOUT_CONV)) break;
+        const float* scr = sc + slot * C::SC_KB * C::SC_PITCH;
+#pragma unroll
+        for (int k = 0; k < C::SC_KB; ++k) {
+            if (kb + k >= kb1) break;
+            const float sf = scr[k * C::SC_PITCH + row] * scr[k * C::SC_PITCH + C::TN];
+            const uint64_t s2 = pack2(sf, sf);
+            if (!mbar_wait(&done[st], ph, abort_flag, p.err, DEV_TIMEOUT_ACC)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const int buf = k % C::NBUF;   // (SC_KB is a multiple of NBUF)
+            const uint32_t a0 = lane_addr + (uint32_t)(buf * C::ACC_COLS);
+#pragma unroll
+            for (int x = 0; x < COLS; x += LD) {
+                uint32_t r[LD];
+                tmem_ld(a0 + x, r);
+                tmem_ld_wait();
+                if (x + LD == COLS) {
+                    // every column is in registers: the MMA may write the buffer again
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&acc_empty[buf]);
+                }
+#pragma unroll
+                for (int j = 0; j < LD / 2; ++j) acc[x / 2 + j] = fma2(pack2u(r[2 * j], r[2 * j + 1]), s2, acc[x / 2 + j]);
+            }
+            if (++st == C::STAGES) {
+                st = 0;
+                ph ^= 1u;
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc_empty[slot]);
+        if (++slot == C::SC_SLOTS) {
+            slot = 0;
+            sph ^= 1u;
+        }
+    }
+    // (the stages are free, as above)  16-byte chunk c of a token's row at c ^ (token % 32)
+#pragma unroll
+    for (int j = 0; j < COLS / 4; ++j) {
+        const float2 a = unpack2(acc[2 * j]), b = unpack2(acc[2 * j + 1]);
+        *reinterpret_cast<float4*>(sums + row * 128 + (((cg * 8 + j) ^ lane) << 2)) = make_float4(a.x, a.y, b.x, b.y);
+    }
 }
 
 template <class C>
@@ -110,74 +254,8 @@ __global__ void __launch_bounds__(C::THREADS)
     const int kb0 = (int)((long)rank * kbs / cs), kb1 = (int)((long)(rank + 1) * kbs / cs);
 
     if (warp >= 4) {
-        // ------------------------------------------------------------ fold
-        const int set = (warp - 4) >> 2, q = warp & 3, row = q * 32 + lane;
-        const int mat = set % C::MATS, tg = set / C::MATS;
-        const uint32_t lane_addr = tmem_base + ((uint32_t)(q * 32) << 16) + mat * C::TN + tg * C::CW;
-        int st = 0, slot = 0, buf = 0;
-        uint32_t ph = 0, sph = 0;
-        bool ok = true;
-        uint64_t acc[C::CW / 2];
-#pragma unroll
-        for (int j = 0; j < C::CW / 2; ++j) acc[j] = 0;
-        for (int kb = kb0; kb < kb1 && ok; kb += C::SC_KB) {
-            if (!mbar_wait(&sc_full[slot], sph, abort_flag, p.err, DEV_TIMEOUT_CONV)) break;
-#pragma unroll
-            for (int k = 0; k < C::SC_KB; ++k) {
-                if (kb + k >= kb1) break;
-                const float* scr = sc + (slot * C::SC_KB + k) * C::SC_PITCH;
-                const float sw = scr[C::TN + mat];
-                const uint64_t sw2 = pack2(sw, sw);
-                const ulonglong2* sx = reinterpret_cast<const ulonglong2*>(scr + tg * C::CW);
-                if (!mbar_wait(&done[st], ph, abort_flag, p.err, DEV_TIMEOUT_ACC)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t a0 = lane_addr + (uint32_t)(buf * C::ACC_COLS);
-#pragma unroll
-                for (int x = 0; x < C::CW; x += C::LW) {
-                    uint32_t r[C::LW];
-                    tmem_ld(a0 + x, r);
-                    tmem_ld_wait();
-                    if (x + C::LW == C::CW) {
-                        // every column is in registers: the MMA may write the buffer again
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&acc_empty[buf]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < C::LW / 4; ++j) {
-                        const ulonglong2 s = sx[x / 4 + j];   // four tokens' scales
-                        uint64_t& y0 = acc[x / 2 + 2 * j];
-                        uint64_t& y1 = acc[x / 2 + 2 * j + 1];
-                        y0 = fma2(pack2u(r[4 * j], r[4 * j + 1]), mul2(s.x, sw2), y0);
-                        y1 = fma2(pack2u(r[4 * j + 2], r[4 * j + 3]), mul2(s.y, sw2), y1);
-                    }
-                }
-                if (++buf == C::NBUF) buf = 0;
-                if (++st == C::STAGES) {
-                    st = 0;
-                    ph ^= 1u;
-                }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sc_empty[slot]);
-            if (++slot == C::SC_SLOTS) {
-                slot = 0;
-                sph ^= 1u;
-            }
-        }
-        // This warp saw the last K block's barrier: every MMA is complete, so every copy has
-        // landed and been read, and the stages become the sums' buffer.  (After a time-out
-        // the sums mean nothing.)
-#pragma unroll
-        for (int j = 0; j < C::CW / 2; ++j) {
-            const float2 f = unpack2(acc[j]);
-            float* dst = sums + (mat * C::TN + tg * C::CW + 2 * j) * 128 + row;
-            dst[0] = f.x;
-            dst[128] = f.y;
-        }
+        if constexpr (C::TOKENS_M) fold_tokens_m<C>(p, warp, lane, kb0, kb1, tmem_base, sc, sums, done, acc_empty, sc_full, sc_empty, abort_flag);
+        else fold_weights_m<C>(p, warp, lane, kb0, kb1, tmem_base, sc, sums, done, acc_empty, sc_full, sc_empty, abort_flag);
     } else if (warp == 0) {
         // ------------------------------------------------------------ producer
         int s = 0;
@@ -217,12 +295,19 @@ __global__ void __launch_bounds__(C::THREADS)
             const uint64_t xd = smem_desc_sw128(sa + C::W_BYTES);
             const uint32_t d = tmem_base + (uint32_t)(buf * C::ACC_COLS);
             if (elect_one_sync()) {
-#pragma unroll
-                for (int m = 0; m < C::MATS; ++m) {
-                    const uint64_t wd = smem_desc_sw128(sa + m * 128 * 128);
+                if constexpr (C::TOKENS_M) {
+                    const uint64_t wd = smem_desc_sw128(sa);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)   // 32 codes (32 bytes) per MMA
-                        tc_mma_f8(d + m * C::TN, wd + (uint64_t)(k * 2), xd + (uint64_t)(k * 2), idesc_e4m3(128, C::TN), k > 0);
+                        tc_mma_f8(d, xd + (uint64_t)(k * 2), wd + (uint64_t)(k * 2), idesc_e4m3(128, 128), k > 0);
+                } else {
+#pragma unroll
+                    for (int m = 0; m < C::MATS; ++m) {
+                        const uint64_t wd = smem_desc_sw128(sa + m * 128 * 128);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc_mma_f8(d + m * C::TN, wd + (uint64_t)(k * 2), xd + (uint64_t)(k * 2), idesc_e4m3(128, C::TN), k > 0);
+                    }
                 }
                 tc_commit(&done[s]);
             }
@@ -271,7 +356,7 @@ __global__ void __launch_bounds__(C::THREADS)
     cluster_sync();   // every CTA's sums are in its shared memory
     for (int t = rank + cs * warp; t < C::TN && m0 + t < p.M; t += cs * (C::THREADS / 32)) {
         const long m = (long)m0 + t;
-        const uint32_t a = smem_u32(sums + t * 128 + lane * 4);
+        const uint32_t a = smem_u32(sums + t * 128 + (C::TOKENS_M ? lane ^ (t & 31) : lane) * 4);
         const float4 y = cluster_sum(a, cs);
         const int n = n0 + lane * 4;
         if constexpr (!C::GATED) {

@@ -9,8 +9,8 @@ namespace qmm {
 // K = 2048 .. 17408 (the part that all kernels share, launch and memory, left out):
 //   narrow kernel, 128 weight rows x tn tokens, K over cs CTAs, one CTA per SM
 //   pair kernel, 256 tokens x bn columns, one pair per two SMs
-// Measured at 5120 x 5120: 128 tokens narrow 128/3 13.8 us, pair 17.5; 300 tokens pair
-// (192 columns) 21.8, narrow 24.5; 1 token narrow 16/3 8.0, 16/1 13.3, 16/4 (more CTAs than
+// Measured at 5120 x 5120: 128 tokens narrow 128/3 10.5 us, pair 17.5; 300 tokens narrow
+// 128/1 16.8, pair (192 columns) 20.9; 600 tokens 31 and 24; 1 token narrow 16/3 8.0, 16/1 13.3, 16/4 (more CTAs than
 // SMs) 13.6; at 2000 x 1000, 128 tokens 32/4 6.4, 128/8 8.5.
 Fp8a8Plan fp8a8_plan(int M, int K, int N, bool gated, int sms) {
     const int kbs = (K + 127) / 128;
@@ -25,7 +25,7 @@ Fp8a8Plan fp8a8_plan(int M, int K, int N, bool gated, int sms) {
         }
     };
     static const int tns[4] = {16, 32, 64, 128};
-    static const double narrow_kb[2][4] = {{0.21, 0.23, 0.27, 0.49}, {0.27, 0.37, 0.50, 0.0}};
+    static const double narrow_kb[2][4] = {{0.21, 0.23, 0.27, 0.30}, {0.27, 0.37, 0.50, 0.0}};
     for (int i = 0; i < (gated ? 3 : 4); ++i) {
         const double tiles = (double)((N + 127) / 128) * ((M + tns[i] - 1) / tns[i]);
         if (tiles > 8.0 * sms) continue;   // the pair kernel's
