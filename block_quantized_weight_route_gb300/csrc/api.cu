@@ -916,21 +916,27 @@ qmm_status qmm_add_rmsnorm_q8_1(const void* X, qmm_dtype xdt, int64_t ldx, const
 // ---------------------------------------------------------------- FP8 x FP8 products
 
 static qmm_status run_fp8a8(const char* who, DeviceState* d, Fp8a8Params& p, bool gated, cudaStream_t stream) {
-    const Fp8a8Plan pl = fp8a8_plan(p.M, p.K, p.N, gated, d->sms);
+    const Fp8a8Plans plans = fp8a8_plan(p.M, p.K, p.N, gated, d->sms);
     p.err = d->err;
-    // boxes of 128 codes: 128 activation rows and a CTA's half of the columns (pair), or
-    // the tile's tokens and 128 weight rows
-    qmm_status st;
-    CUtensorMap tx, tw;
-    if ((st = make_tmap(&tx, p.Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, p.M, p.K, 128, pl.pair ? 128 : pl.tn,
-                        CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK)
-        return st;
-    if ((st = make_tmap(&tw, p.W, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, (uint64_t)p.N * (gated ? 2 : 1), p.K, 128,
-                        pl.pair ? pl.bn / 2 : 128, CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK)
-        return st;
-    cudaError_t e = pl.pair ? launch_fp8a8_pair(tx, tw, p, gated, pl.bn, d->sms, stream)
-                            : launch_fp8a8_narrow(tx, tw, p, gated, pl.tn, pl.cs, stream);
-    return e == cudaSuccess ? QMM_OK : cuda_fail(e, who);
+    for (int part = 0; part < (plans.split < p.N ? 2 : 1); ++part) {
+        const Fp8a8Plan& pl = part ? plans.second : plans.first;
+        p.n_first = part ? plans.split : 0;
+        p.n_end = part ? p.N : plans.split;
+        // boxes of 128 codes: 128 activation rows and a CTA's half of the columns (pair), or
+        // the tile's tokens and 128 weight rows
+        qmm_status st;
+        CUtensorMap tx, tw;
+        if ((st = make_tmap(&tx, p.Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, p.M, p.K, 128, pl.pair ? 128 : pl.tn,
+                            CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK)
+            return st;
+        if ((st = make_tmap(&tw, p.W, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, (uint64_t)p.N * (gated ? 2 : 1), p.K, 128,
+                            pl.pair ? pl.bn / 2 : 128, CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK)
+            return st;
+        const cudaError_t e = pl.pair ? launch_fp8a8_pair(tx, tw, p, gated, pl.bn, d->sms, stream)
+                                      : launch_fp8a8_narrow(tx, tw, p, gated, pl.tn, pl.cs, stream);
+        if (e != cudaSuccess) return cuda_fail(e, who);
+    }
+    return QMM_OK;
 }
 
 qmm_status qmm_fp8a8_blk128(const uint8_t* Xq, const float* Xs, int M, int K, int N, const uint8_t* W, const float* S,

@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(C::THREADS)
     wait_prerequisites();
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const int cs = (int)gridDim.x, rank = (int)blockIdx.x;   // one cluster per row of the grid
-    const int n0 = (int)blockIdx.y * 128, m0 = (int)blockIdx.z * C::TN;
+    const int n0 = p.n_first + (int)blockIdx.y * 128, m0 = (int)blockIdx.z * C::TN;
     const int kbs = (p.K + 127) / 128;
     const int kb0 = (int)((long)rank * kbs / cs), kb1 = (int)((long)(rank + 1) * kbs / cs);
 
@@ -428,7 +428,7 @@ cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Para
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1] = overlap_attribute();
-    cfg.gridDim = dim3(cs, (p.N + 127) / 128, (p.M + C::TN - 1) / C::TN);
+    cfg.gridDim = dim3(cs, (p.n_end - p.n_first + 127) / 128, (p.M + C::TN - 1) / C::TN);
     cfg.blockDim = dim3(C::THREADS, 1, 1);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;

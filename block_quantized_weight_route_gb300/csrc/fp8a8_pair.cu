@@ -13,14 +13,15 @@
 //   warps 4..19: fold; warp w reads TMEM lanes 32 (w % 4) .. +31 (a row per lane) and
 //                quarter (w - 4) / 4 of the columns
 // What bounds it: a TMEM buffer's way from the MMA's end through the fold and back to
-// the even CTA takes longer than the other buffer's MMA (512 cycles at BN = 256), so the
-// length of the fold's path counts, not its throughput: 16 warps rather than 8, TMEM loads
-// of 8 columns (5268 x 17408 x 5120: 388 us; of 16: 428, of 4: 578; BN = 192, whose path is
-// shorter: 16), four K blocks unrolled and no spilled registers.  Not kept: three buffers
-// of 160 columns with 20 fold warps (300 x 5120 x 5120 20.7 us against 21.8, but 72 against 56
-// at 2048 tokens), halves of the tile with MMAs and warps of their own, polling instead
-// of sleeping waits (5% slower).  At 2.4 PFLOP/s the power limit is near: without any fold
-// the same loop reaches 3.0 PFLOP/s at clocks down to 1.6 GHz.
+// the even CTA takes about 1000 cycles, even with nothing folded (MMA latency, the commit's
+// and the release's way across the pair): with two buffers that is more than the other
+// buffer's MMA (512 cycles at BN = 256), so the length of the fold's path counts, not its
+// throughput.  BN = 128 has four buffers and is bound by shared memory (48 KB written and
+// read a K block, 470 cycles).  Per K block: 0.42 us at BN = 256, 0.375 at 192, 0.245 at 128.
+// Not kept: three buffers of 160 columns with 20 fold warps, halves of the tile with MMAs
+// and warps of their own, two MMA issuers, a producer warp per operand (all within 5%),
+// polling instead of sleeping waits (5% slower).  At 2.4 PFLOP/s the power limit is near:
+// without any fold the same loop reaches 3.0 PFLOP/s at clocks down to 1.6 GHz.
 #include "fp8a8.cuh"
 
 namespace qmm {
@@ -36,11 +37,15 @@ struct PairCfg {
     static constexpr int SC_SLOTS = 4, SC_KB = 4;                 // ring of scales: slots of 4 K blocks
     static constexpr int SC_PITCH = 128 + 4;                      // per K block: the rows' scales, the two blocks'
     static constexpr int SC_FLOATS = SC_SLOTS * SC_KB * SC_PITCH;
-    static constexpr int FOLD_WARPS = 16, GROUPS = FOLD_WARPS / 4;                  // column groups
-    static constexpr int CW = BN / GROUPS, PARTS = CW / 16, LW = BN == 192 ? 16 : 8;// columns of a fold thread, of a load
+    // Fold threads: a row and CW columns, LW of them a TMEM load.  Few large loads are best
+    // where the registers hold them (8 fold warps: all 64 columns at once, 37 us against 45
+    // with loads of 32 at 256 x 17408 x 5120; 12 warps: 32); 16 warps need more than an even
+    // share of the registers for their sums (a register split) and loads of 8 to spill nothing.
+    static constexpr int CW = 64, GROUPS = BN / CW, FOLD_WARPS = 4 * GROUPS, LW = BN == 256 ? 8 : BN == 192 ? 32 : 64;
     static constexpr int OUT_BYTES = GATED ? 2 * GROUPS * 128 * 4 : FOLD_WARPS * 2048;   // row maxima, or output staging
-    static constexpr int THREADS = 128 + 32 * FOLD_WARPS, REGS = 96, REGS_FOLD = 104, REGS_OTHER = 64;
-    static_assert(REGS_FOLD * 32 * FOLD_WARPS + REGS_OTHER * 128 == REGS * THREADS, "register shares = launch registers");
+    static constexpr bool REG_SPLIT = BN == 256;
+    static constexpr int THREADS = 128 + 32 * FOLD_WARPS, REGS = 65536 / THREADS / 8 * 8, REGS_FOLD = 104, REGS_OTHER = 64;
+    static_assert(!REG_SPLIT || REGS_FOLD * 32 * FOLD_WARPS + REGS_OTHER * 128 == REGS * THREADS, "register shares = launch registers");
     static constexpr int BARS = 2 * STAGES + NBUF + 2 * SC_SLOTS + 3;
     static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + OUT_BYTES + SC_FLOATS * 4 + BARS * 8 + 64;
     static_assert(SMEM <= 232448, "shared memory");
@@ -57,7 +62,7 @@ __device__ __forceinline__ PairTile pair_tile(const Fp8a8Params& p, int t, int c
     const int mt = t % p.m_tiles, nt = t / p.m_tiles;
     PairTile r;
     r.m0 = mt * 256 + crank * 128;
-    r.n0 = nt * (C::GATED ? 128 : C::BN);
+    r.n0 = p.n_first + nt * (C::GATED ? 128 : C::BN);
     return r;
 }
 
@@ -122,7 +127,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
     const int tiles = p.m_tiles * p.n_tiles, kbs = (p.K + 127) / 128;
 
     if (warp >= 4) {
-        setmaxnreg_inc<C::REGS_FOLD>();
+        if constexpr (C::REG_SPLIT) setmaxnreg_inc<C::REGS_FOLD>();
         // ------------------------------------------------------------ fold
         const int q = warp & 3, cq = (warp - 4) >> 2, row = q * 32 + lane;
         const uint32_t lane_addr = tmem_base + ((uint32_t)(q * 32) << 16);
@@ -131,13 +136,12 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
         bool ok = true;
         for (int t = cid; t < tiles && ok; t += ncl, parity ^= 1) {
             const PairTile ti = pair_tile<C>(p, t, crank);
-            // columns below `bound` belong to the first of the tile's two weight blocks
-            const int bound = C::BN == 192 ? 128 - (ti.n0 & 127) : 128;
-            uint64_t acc[C::PARTS][8];
+            // which of the tile's two weight blocks the thread's 64 columns are in (gated: the
+            // first half in one, the second in the other)
+            const int blk = !C::GATED && cq * C::CW >= 128 - (ti.n0 & 127);
+            uint64_t acc[C::CW / 2];
 #pragma unroll
-            for (int c = 0; c < C::PARTS; ++c)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) acc[c][j] = 0;
+            for (int j = 0; j < C::CW / 2; ++j) acc[j] = 0;
             for (int kb0 = 0; kb0 < kbs && ok; kb0 += C::SC_KB) {
                 if (!mbar_wait(&sc_full[slot], sph, abort_flag, p.err, DEV_TIMEOUT_CONV)) {
                     ok = false;
@@ -147,11 +151,9 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
 #pragma unroll
                 for (int k = 0; k < C::SC_KB; ++k) {
                     if (kb0 + k >= kbs) break;
-                    // the scales' product for the thread's columns (both of the tile's blocks
-                    // where its columns reach into both)
                     const float sx = scr[k * C::SC_PITCH + row];
-                    const float s0 = sx * scr[k * C::SC_PITCH + 128 + (C::BN == 256 && !C::GATED ? cq / (C::GROUPS / 2) : 0)];
-                    const float s1 = C::BN == 192 || C::GATED ? sx * scr[k * C::SC_PITCH + 129] : s0;
+                    const float s0 = sx * scr[k * C::SC_PITCH + 128 + blk];
+                    const float s1 = C::GATED ? sx * scr[k * C::SC_PITCH + 129] : s0;
                     if (!mbar_wait(&done[st], ph, abort_flag, p.err, DEV_TIMEOUT_ACC)) {
                         ok = false;
                         break;
@@ -170,12 +172,11 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
                             __syncwarp();
                             if (lane == 0) mbar_arrive_even(&acc_empty[buf], crank);
                         }
-                        const float sf = C::GATED ? (x < C::CW / 2 ? s0 : s1) : fold_col<C>(cq, x & ~15) < bound ? s0 : s1;
+                        const float sf = x < C::CW / 2 ? s0 : s1;
                         const uint64_t s2 = pack2(sf, sf);
 #pragma unroll
                         for (int j = 0; j < C::LW / 2; ++j) {
-                            uint64_t& y = acc[x / 16][x % 16 / 2 + j];
-                            y = fma2(pack2u(r[2 * j], r[2 * j + 1]), s2, y);
+                            acc[x / 2 + j] = fma2(pack2u(r[2 * j], r[2 * j + 1]), s2, acc[x / 2 + j]);
                         }
                     }
                     if (++st == C::STAGES) {
@@ -194,20 +195,19 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
             if constexpr (!C::GATED) {
                 uint8_t* stg = outs + (warp - 4) * 2048;
 #pragma unroll
-                for (int c = 0; c < C::PARTS; ++c)
-                    store_chunk<16>(p, stg, lane, (long)ti.m0 + q * 32, ti.n0 + fold_col<C>(cq, c * 16), acc[c]);
+                for (int c = 0; c < C::CW; c += 16)
+                    store_chunk<16>(p, stg, lane, (long)ti.m0 + q * 32, ti.n0 + fold_col<C>(cq, c), acc + c / 2);
             } else {
                 // the first half of acc: gate columns; the second half: the same columns of up
-                constexpr int HP = C::PARTS / 2;
+                constexpr int HP = C::CW / 4;   // pairs
                 const long grow = (long)ti.m0 + row;
                 float a = 0.f;
 #pragma unroll
-                for (int j = 0; j < HP * 8; ++j) {
-                    uint64_t& y = acc[j / 8][j % 8];
-                    const float2 g = unpack2(y), u = unpack2(acc[HP + j / 8][j % 8]);
+                for (int j = 0; j < HP; ++j) {
+                    const float2 g = unpack2(acc[j]), u = unpack2(acc[HP + j]);
                     const float h0 = swiglu(g.x, u.x), h1 = swiglu(g.y, u.y);
                     a = max_nan_abs(a, h0, h1);
-                    y = pack2(h0, h1);
+                    acc[j] = pack2(h0, h1);
                 }
                 float* rm = rowmax + parity * 512 + row;
                 rm[cq * 128] = a;
@@ -221,15 +221,16 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
                 if (grow < p.M) {
                     uint4* dst = reinterpret_cast<uint4*>(p.Hq + grow * p.N + ti.n0 + cq * (C::CW / 2));
 #pragma unroll
-                    for (int j = 0; j < HP; ++j)
-                        dst[j] = make_uint4(codes4(gs, acc[j][0], acc[j][1]), codes4(gs, acc[j][2], acc[j][3]),
-                                            codes4(gs, acc[j][4], acc[j][5]), codes4(gs, acc[j][6], acc[j][7]));
+                    for (int j = 0; j < HP / 8; ++j) {
+                        const uint64_t* v = acc + 8 * j;
+                        dst[j] = make_uint4(codes4(gs, v[0], v[1]), codes4(gs, v[2], v[3]), codes4(gs, v[4], v[5]), codes4(gs, v[6], v[7]));
+                    }
                     if (cq == 0) p.Hs[grow * (p.N / 128) + ti.n0 / 128] = gs.s;
                 }
             }
         }
     } else {
-        setmaxnreg_dec<C::REGS_OTHER>();
+        if constexpr (C::REG_SPLIT) setmaxnreg_dec<C::REGS_OTHER>();
         if (warp == 0) {
             // ------------------------------------------------------------ producer
             // Both CTAs' copies complete on the even CTA's barrier, which expects all of
@@ -376,12 +377,14 @@ cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Para
     if (most[dev] == 0) {
         e = cudaFuncSetAttribute(fp8a8_pair_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
-        // the warpgroups' register shares add up to the launch's: launch only if the kernel
-        // is allocated exactly that many (a setmaxnreg.inc past the pool waits)
-        cudaFuncAttributes fa{};
-        e = cudaFuncGetAttributes(&fa, fp8a8_pair_kernel<C>);
-        if (e != cudaSuccess) return e;
-        if (fa.numRegs != C::REGS) return cudaErrorInvalidConfiguration;
+        if constexpr (C::REG_SPLIT) {
+            // the warpgroups' register shares add up to the launch's: launch only if the kernel
+            // is allocated exactly that many (a setmaxnreg.inc past the pool waits)
+            cudaFuncAttributes fa{};
+            e = cudaFuncGetAttributes(&fa, fp8a8_pair_kernel<C>);
+            if (e != cudaSuccess) return e;
+            if (fa.numRegs != C::REGS) return cudaErrorInvalidConfiguration;
+        }
     }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -413,7 +416,7 @@ cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Para
 cudaError_t launch_fp8a8_pair(const CUtensorMap& tx, const CUtensorMap& tw, Fp8a8Params p, bool gated, int bn, int sms,
                               cudaStream_t s) {
     p.m_tiles = (p.M + 255) / 256;
-    p.n_tiles = gated ? p.N / 128 : (p.N + bn - 1) / bn;
+    p.n_tiles = (p.n_end - p.n_first + (gated ? 127 : bn - 1)) / (gated ? 128 : bn);
     if (gated) return launch<PairCfg<256, true>>(tx, tw, p, sms, s);
     if (bn == 256) return launch<PairCfg<256, false>>(tx, tw, p, sms, s);
     if (bn == 192) return launch<PairCfg<192, false>>(tx, tw, p, sms, s);

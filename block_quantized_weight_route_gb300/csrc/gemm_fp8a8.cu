@@ -3,53 +3,89 @@
 
 namespace qmm {
 
-// The kernel, tile and split with the least estimated time.  A launch's time is taken
-// as waves x (start and end of a CTA + its K blocks x time of a K block), in
-// microseconds, with the constants fitted to runs of one and of several waves at
-// K = 2048 .. 17408 (the part that all kernels share, launch and memory, left out):
+namespace {
+
+constexpr int kBn[3] = {256, 192, 128};
+constexpr double kPairEnds[3] = {4.0, 2.9, 1.5}, kPairKb[3] = {0.42, 0.375, 0.245};
+constexpr int kTn[4] = {16, 32, 64, 128};
+constexpr double kNarrowKb[2][4] = {{0.21, 0.23, 0.27, 0.30}, {0.27, 0.37, 0.50, 0.0}};
+
+constexpr double kSecondLaunch = 1.5;
+
+double pair_time(long tiles, long pairs, int i, int kbs) {
+    return (double)((tiles + pairs - 1) / pairs) * (kPairEnds[i] + kbs * kPairKb[i]);
+}
+
+// The kernel, tile and split of K with the least estimated time for one launch over
+// `cols` columns.  A launch's time is taken as waves x (start and end of a CTA + its K
+// blocks x time of a K block), in microseconds, with the constants fitted to runs of one and of
+// several waves at K = 2048 .. 17408 (what all kernels share, launch and memory, left out):
 //   narrow kernel, 128 weight rows x tn tokens, K over cs CTAs, one CTA per SM
 //   pair kernel, 256 tokens x bn columns, one pair per two SMs
-// Measured at 5120 x 5120: 128 tokens narrow 128/3 10.5 us, pair 17.5; 300 tokens narrow
-// 128/1 16.8, pair (192 columns) 20.9; 600 tokens 31 and 24; 1 token narrow 16/3 8.0, 16/1 13.3, 16/4 (more CTAs than
-// SMs) 13.6; at 2000 x 1000, 128 tokens 32/4 6.4, 128/8 8.5.
-Fp8a8Plan fp8a8_plan(int M, int K, int N, bool gated, int sms) {
-    const int kbs = (K + 127) / 128;
+// Measured at 5120 x 5120: 128 tokens narrow 128/3 10.5 us, pair 13.9; 300 tokens narrow
+// 128/1 16.8, pair (192 columns) 20.9; 600 tokens 31 and 24; 1 token narrow 16/3 8.0,
+// 16/1 13.3, 16/4 (more CTAs than SMs) 13.6; at 2000 x 1000, 128 tokens 32/4 6.4, 128/8 8.5.
+Fp8a8Plan one_launch(int M, int kbs, int cols, bool gated, int sms, double* time) {
     Fp8a8Plan best{};
-    double least = 1e300;
-    auto consider = [&](const Fp8a8Plan& pl, double tiles, double at_once, double ends, double kb, double per_kb) {
-        const double waves = (double)(long)((tiles + at_once - 1) / at_once);
-        const double t = waves * (ends + kb * per_kb);
-        if (t < least) {
-            least = t;
+    *time = 1e300;
+    auto consider = [&](const Fp8a8Plan& pl, double t) {
+        if (t < *time) {
+            *time = t;
             best = pl;
         }
     };
-    static const int tns[4] = {16, 32, 64, 128};
-    static const double narrow_kb[2][4] = {{0.21, 0.23, 0.27, 0.30}, {0.27, 0.37, 0.50, 0.0}};
     for (int i = 0; i < (gated ? 3 : 4); ++i) {
-        const double tiles = (double)((N + 127) / 128) * ((M + tns[i] - 1) / tns[i]);
-        if (tiles > 8.0 * sms) continue;   // the pair kernel's
+        const long tiles = (long)((cols + 127) / 128) * ((M + kTn[i] - 1) / kTn[i]);
+        if (tiles > 8L * sms) continue;   // the pair kernel's
         for (int cs = 1; cs <= 8 && cs <= kbs; ++cs) {
-            Fp8a8Plan pl{};
-            pl.tn = tns[i];
-            pl.cs = cs;
             const int at_once = fp8a8_narrow_at_once(cs);
             if (at_once < 1) continue;
+            Fp8a8Plan pl{};
+            pl.tn = kTn[i];
+            pl.cs = cs;
             // (adding up costs a little for each CTA of a cluster)
-            consider(pl, tiles, at_once, 2.2 + 0.1 * cs, (kbs + cs - 1) / cs, narrow_kb[gated][i]);
+            consider(pl, (double)((tiles + at_once - 1) / at_once) *
+                             (2.2 + 0.1 * cs + (kbs + cs - 1) / cs * kNarrowKb[gated][i]));
         }
     }
-    static const int bns[3] = {256, 192, 128};
-    static const double pair_ends[3] = {4.0, 2.9, 1.5}, pair_kb[3] = {0.43, 0.377, 0.30};
     for (int i = 0; i < (gated ? 1 : 3); ++i) {
-        const double cols = gated ? 128 : bns[i];
-        const double tiles = (double)((M + 255) / 256) * (double)(long)((N + cols - 1) / cols);
+        const int width = gated ? 128 : kBn[i];
         Fp8a8Plan pl{};
         pl.pair = true;
-        pl.bn = bns[i];
-        consider(pl, tiles, sms / 2, pair_ends[i], kbs, pair_kb[i]);
+        pl.bn = kBn[i];
+        consider(pl, pair_time((long)((M + 255) / 256) * ((cols + width - 1) / width), sms / 2, i, kbs));
     }
     return best;
+}
+
+}  // namespace
+
+// One launch, or the columns of the whole waves of widest pair tiles in one and the rest
+// in a second with a plan of its own, where that takes less by more than the second
+// launch costs (2048 x 5120 x 5120: 152 tiles in two waves and 256 columns left).
+Fp8a8Plans fp8a8_plan(int M, int K, int N, bool gated, int sms) {
+    const int kbs = (K + 127) / 128;
+    Fp8a8Plans r{};
+    double least;
+    r.first = one_launch(M, kbs, N, gated, sms, &least);
+    r.split = N;
+    const long mt = (M + 255) / 256, pairs = sms / 2;
+    const int width = gated ? 128 : kBn[0];
+    const long waves = mt * ((N + width - 1) / width) / pairs;
+    const long whole = waves * pairs / mt * width;
+    if (waves >= 1 && whole > 0 && whole < N) {
+        double rest;
+        const Fp8a8Plan second = one_launch(M, kbs, N - (int)whole, gated, sms, &rest);
+        const double t = pair_time(mt * (whole / width), pairs, 0, kbs) + rest + kSecondLaunch;
+        if (t < 0.97 * least) {
+            r.first = Fp8a8Plan{};
+            r.first.pair = true;
+            r.first.bn = kBn[0];
+            r.second = second;
+            r.split = (int)whole;
+        }
+    }
+    return r;
 }
 
 }  // namespace qmm

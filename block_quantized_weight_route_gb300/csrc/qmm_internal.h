@@ -148,6 +148,7 @@ struct Fp8a8Params {
     uint8_t* Hq;         // gated: [M][F] E4M3
     float* Hs;           // gated: [M][F/128]
     uint32_t* err;       // device error word
+    int n_first, n_end;  // the launch's columns (n_first a multiple of 128)
     int m_tiles, n_tiles;
 };
 // Which kernel takes a product: the pair kernel (many tokens) with its tile's columns,
@@ -157,7 +158,12 @@ struct Fp8a8Plan {
     int bn;      // pair: columns of a tile
     int tn, cs;  // narrow
 };
-Fp8a8Plan fp8a8_plan(int M, int K, int N, bool gated, int sms);
+// The columns [0, split) go to one launch, [split, N) to a second one (none if split = N).
+struct Fp8a8Plans {
+    Fp8a8Plan first, second;
+    int split;
+};
+Fp8a8Plans fp8a8_plan(int M, int K, int N, bool gated, int sms);
 int fp8a8_narrow_at_once(int cs);   // clusters of cs CTAs that the device holds at once (0: error)
 cudaError_t launch_fp8a8_narrow(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, bool gated, int tn,
                                 int cs, cudaStream_t s);
