@@ -87,6 +87,13 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) {
                  : "memory");
 }
 
+// Prefetch of a box into L2.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
+
 // Wait (bounded) for the completion of the `issued` most recent fills of a ring.
 __device__ __forceinline__ void drain_ring(uint64_t* full, long issued, int stages, uint32_t* err) {
     const long pending = issued < stages ? issued : stages;

@@ -25,7 +25,11 @@ struct NarrowCfg {
     static constexpr int TN = TN_, MATS = GATED_ ? 2 : 1;
     static constexpr bool GATED = GATED_, TOKENS_M = TN == 128;
     static constexpr int W_BYTES = MATS * 128 * 128, X_BYTES = TN * 128, STAGE_BYTES = W_BYTES + X_BYTES;
-    static constexpr int STAGES = 196608 / STAGE_BYTES > 10 ? 10 : 196608 / STAGE_BYTES;
+    // Two CTAs on an SM where a stage (and a fold thread) is small: one's start and end run beside the other's
+    // stream, and a product of few tiles is split over more CTAs (one token, 5120 x 5120:
+    // 6.7 us over 240 CTAs, 7.5 over 120, 7.9 with one CTA of twice the stages)
+    static constexpr int PER_SM = TN * MATS <= 32 ? 2 : 1;
+    static constexpr int STAGES = (PER_SM == 2 ? 106496 : 196608) / STAGE_BYTES;
     static constexpr int ACC_COLS = TN * MATS;
     static_assert(!TOKENS_M || !GATED, "tokens on the M side: 128 x 128 tiles");
     static constexpr int TMEM_COLS = ACC_COLS <= 32 ? 128 : ACC_COLS <= 64 ? 256 : 512;
@@ -38,7 +42,7 @@ struct NarrowCfg {
     static_assert(COPIES * STAGES <= 32, "a lane per copy");
     static constexpr int BARS = 2 * STAGES + NBUF + 2 * SC_SLOTS + 1;
     static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + SC_FLOATS * 4 + BARS * 8 + 64;
-    static_assert(SMEM <= 232448, "shared memory");
+    static_assert(PER_SM * (SMEM + 1024) <= 233472 && PER_SM * TMEM_COLS <= 512, "shared memory and TMEM");
     static_assert(TN * 128 * 4 * MATS <= STAGES * STAGE_BYTES, "the sums fit the stages");
     static_assert(!TOKENS_M || SC_KB % NBUF == 0, "buffer = K block's place in its slot");
     static_assert(NBUF >= 1 && NBUF <= STAGES, "a stage's MMA barrier completes again only after its accumulator was read");
@@ -208,7 +212,7 @@ __device__ __forceinline__ void fold_tokens_m(const Fp8a8Params& p, int warp, in
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS)
+__global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     fp8a8_narrow_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, Fp8a8Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stage = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -242,16 +246,22 @@ __global__ void __launch_bounds__(C::THREADS)
         tma_prefetch_desc(&tmX);
         tma_prefetch_desc(&tmW);
     }
+    const int cs = (int)gridDim.x, rank = (int)blockIdx.x;   // one cluster per row of the grid
+    const int n0 = p.n_first + (int)blockIdx.y * 128, m0 = (int)blockIdx.z * C::TN;
+    const int kbs = (p.K + 127) / 128;
+    const int kb0 = (int)((long)rank * kbs / cs), kb1 = (int)((long)(rank + 1) * kbs / cs);
+    if (warp == 0) {
+        // The first stages' weights on their way to L2 while the kernel before may still run
+        // (only a hint: whatever that kernel writes, the copies below read after it)
+        const int kb = kb0 + lane / C::MATS, m = lane % C::MATS;
+        if (lane < C::STAGES * C::MATS && kb < kb1) tma_prefetch_2d(&tmW, kb * 128, m * p.N + n0);
+    }
     if (warp == 1) tmem_alloc(tmem_slot, C::TMEM_COLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     wait_prerequisites();
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-    const int cs = (int)gridDim.x, rank = (int)blockIdx.x;   // one cluster per row of the grid
-    const int n0 = p.n_first + (int)blockIdx.y * 128, m0 = (int)blockIdx.z * C::TN;
-    const int kbs = (p.K + 127) / 128;
-    const int kb0 = (int)((long)rank * kbs / cs), kb1 = (int)((long)(rank + 1) * kbs / cs);
 
     if (warp >= 4) {
         if constexpr (C::TOKENS_M) fold_tokens_m<C>(p, warp, lane, kb0, kb1, tmem_base, sc, sums, done, acc_empty, sc_full, sc_empty, abort_flag);
@@ -439,10 +449,10 @@ cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Para
 
 }  // namespace
 
-// (Every configuration has one CTA on an SM, so any one of them answers for all; a
-// cluster's CTAs are on SMs of one group of SMs, so fewer fit than SMs / cs.)
-int fp8a8_narrow_at_once(int cs) {
-    using C = NarrowCfg<16, false>;
+namespace {
+
+template <class C>
+int clusters_at_once(int cs) {
     static int at_once[64][9] = {};
     int dev = 0;
     if (cs < 1 || cs > 8 || prepare<C>(&dev) != cudaSuccess) return 0;
@@ -460,22 +470,37 @@ int fp8a8_narrow_at_once(int cs) {
         cfg.numAttrs = 1;
         int n = 0;
         if (cudaOccupancyMaxActiveClusters(&n, fp8a8_narrow_kernel<C>, &cfg) != cudaSuccess || n < 1) return 0;
-        at_once[dev][cs] = n;
+        // (the query counts one CTA per SM for a kernel that allocates TMEM; two whose shared
+        // memory, registers and TMEM fit do run side by side)
+        at_once[dev][cs] = n * C::PER_SM;
     }
     return at_once[dev][cs];
 }
 
+// f(configuration) for the kernel of tn tokens a tile
+template <class F>
+auto with_config(bool gated, int tn, F f) {
+    if (gated) {
+        if (tn == 16) return f(NarrowCfg<16, true>{});
+        if (tn == 32) return f(NarrowCfg<32, true>{});
+        return f(NarrowCfg<64, true>{});
+    }
+    if (tn == 16) return f(NarrowCfg<16, false>{});
+    if (tn == 32) return f(NarrowCfg<32, false>{});
+    if (tn == 64) return f(NarrowCfg<64, false>{});
+    return f(NarrowCfg<128, false>{});
+}
+
+}  // namespace
+
+// (A cluster's CTAs are on SMs of one group of SMs, so fewer fit than slots / cs.)
+int fp8a8_narrow_at_once(bool gated, int tn, int cs) {
+    return with_config(gated, tn, [&](auto c) { return clusters_at_once<decltype(c)>(cs); });
+}
+
 cudaError_t launch_fp8a8_narrow(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, bool gated, int tn,
                                 int cs, cudaStream_t s) {
-    if (gated) {
-        if (tn == 16) return launch<NarrowCfg<16, true>>(tx, tw, p, cs, s);
-        if (tn == 32) return launch<NarrowCfg<32, true>>(tx, tw, p, cs, s);
-        return launch<NarrowCfg<64, true>>(tx, tw, p, cs, s);
-    }
-    if (tn == 16) return launch<NarrowCfg<16, false>>(tx, tw, p, cs, s);
-    if (tn == 32) return launch<NarrowCfg<32, false>>(tx, tw, p, cs, s);
-    if (tn == 64) return launch<NarrowCfg<64, false>>(tx, tw, p, cs, s);
-    return launch<NarrowCfg<128, false>>(tx, tw, p, cs, s);
+    return with_config(gated, tn, [&](auto c) { return launch<decltype(c)>(tx, tw, p, cs, s); });
 }
 
 }  // namespace qmm

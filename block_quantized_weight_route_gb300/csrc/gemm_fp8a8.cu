@@ -12,19 +12,23 @@ constexpr double kNarrowKb[2][4] = {{0.21, 0.23, 0.27, 0.30}, {0.27, 0.37, 0.50,
 
 constexpr double kSecondLaunch = 1.5;
 
+// microseconds for what the tiles read through L2: `rows` operand rows of 128 bytes a K block
+double traffic_time(long tiles, int kbs, int rows) { return (double)tiles * kbs * rows * 128 / 30e6; }
+
 double pair_time(long tiles, long pairs, int i, int kbs) {
-    return (double)((tiles + pairs - 1) / pairs) * (kPairEnds[i] + kbs * kPairKb[i]);
+    return (double)((tiles + pairs - 1) / pairs) * (kPairEnds[i] + kbs * kPairKb[i]) + traffic_time(tiles, kbs, 256 + kBn[i]);
 }
 
 // The kernel, tile and split of K with the least estimated time for one launch over
 // `cols` columns.  A launch's time is taken as waves x (start and end of a CTA + its K
 // blocks x time of a K block), in microseconds, with the constants fitted to runs of one and of
-// several waves at K = 2048 .. 17408 (what all kernels share, launch and memory, left out):
-//   narrow kernel, 128 weight rows x tn tokens, K over cs CTAs, one CTA per SM
+// several waves at K = 2048 .. 17408 (the launch, which all share, left out), plus a charge
+// for the operands' way through L2, which tells tilings of equal waves apart:
+//   narrow kernel, 128 weight rows x tn tokens, K over cs CTAs
 //   pair kernel, 256 tokens x bn columns, one pair per two SMs
 // Measured at 5120 x 5120: 128 tokens narrow 128/3 10.5 us, pair 13.9; 300 tokens narrow
-// 128/1 16.8, pair (192 columns) 20.9; 600 tokens 31 and 24; 1 token narrow 16/3 8.0,
-// 16/1 13.3, 16/4 (more CTAs than SMs) 13.6; at 2000 x 1000, 128 tokens 32/4 6.4, 128/8 8.5.
+// 128/1 16.8, pair (192 columns) 20.9; 600 tokens 31 and 24; 1 token narrow 16/6 6.7,
+// 16/3 7.5, 16/7 (more CTAs than fit at once) 11.3; at 2000 x 1000, 128 tokens 32/4 6.4, 128/8 8.5.
 Fp8a8Plan one_launch(int M, int kbs, int cols, bool gated, int sms, double* time) {
     Fp8a8Plan best{};
     *time = 1e300;
@@ -38,14 +42,15 @@ Fp8a8Plan one_launch(int M, int kbs, int cols, bool gated, int sms, double* time
         const long tiles = (long)((cols + 127) / 128) * ((M + kTn[i] - 1) / kTn[i]);
         if (tiles > 8L * sms) continue;   // the pair kernel's
         for (int cs = 1; cs <= 8 && cs <= kbs; ++cs) {
-            const int at_once = fp8a8_narrow_at_once(cs);
+            const int at_once = fp8a8_narrow_at_once(gated, kTn[i], cs);
             if (at_once < 1) continue;
             Fp8a8Plan pl{};
             pl.tn = kTn[i];
             pl.cs = cs;
             // (adding up costs a little for each CTA of a cluster)
             consider(pl, (double)((tiles + at_once - 1) / at_once) *
-                             (2.2 + 0.1 * cs + (kbs + cs - 1) / cs * kNarrowKb[gated][i]));
+                                 (2.2 + 0.1 * cs + (kbs + cs - 1) / cs * kNarrowKb[gated][i]) +
+                             traffic_time(tiles, kbs, kTn[i] + (gated ? 256 : 128)));
         }
     }
     for (int i = 0; i < (gated ? 1 : 3); ++i) {
