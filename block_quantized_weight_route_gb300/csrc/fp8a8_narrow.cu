@@ -31,13 +31,16 @@ struct NarrowCfg {
     static constexpr int PER_SM = TN * MATS <= 32 ? 2 : 1;
     static constexpr int STAGES = (PER_SM == 2 ? 106496 : 196608) / STAGE_BYTES;
     static constexpr int ACC_COLS = TN * MATS;
-    static_assert(!TOKENS_M || !GATED, "tokens on the M side: 128 x 128 tiles");
     static constexpr int TMEM_COLS = ACC_COLS <= 32 ? 128 : ACC_COLS <= 64 ? 256 : 512;
     static constexpr int NBUF_RAW = TMEM_COLS / ACC_COLS, NBUF = NBUF_RAW < STAGES ? NBUF_RAW : (STAGES & ~1);
     static constexpr int SC_SLOTS = 4, SC_KB = 4, SC_PITCH = TN + 4, SC_FLOATS = SC_SLOTS * SC_KB * SC_PITCH;
     // fold warps: four (the lanes) x the matrices x token groups of at most 32
     static constexpr int CW = TN < 32 ? TN : 32, TG = TN / CW;
     static constexpr int FOLD_WARPS = TOKENS_M ? 16 : 4 * MATS * TG, THREADS = 128 + 32 * FOLD_WARPS;
+    // 64 sums a thread (tokens on the M side, gate and up): more registers for the fold warps
+    static constexpr bool REG_SPLIT = TOKENS_M && GATED;
+    static constexpr int REGS = 96, REGS_FOLD = 104, REGS_OTHER = 64;
+    static_assert(!REG_SPLIT || REGS_FOLD * 32 * FOLD_WARPS + REGS_OTHER * 128 == REGS * THREADS, "register shares = launch registers");
     static constexpr int COPIES = MATS + 1;
     static_assert(COPIES * STAGES <= 32, "a lane per copy");
     static constexpr int BARS = 2 * STAGES + NBUF + 2 * SC_SLOTS + 1;
@@ -148,12 +151,12 @@ __device__ __forceinline__ void fold_weights_m(const Fp8a8Params& p, int warp, i
     }
 }
 
-// Tokens on the M side: lane = token, `acc` 32 weight rows.
+// Tokens on the M side: lane = token, `acc` 32 weight rows (GATED: 32 gate, then 32 up).
 template <class C>
 __device__ __forceinline__ void fold_tokens_m(const Fp8a8Params& p, int warp, int lane, int kb0, int kb1, uint32_t tmem_base,
                                               const float* sc, float* sums, uint64_t* done, uint64_t* acc_empty,
                                               uint64_t* sc_full, uint64_t* sc_empty, volatile int* abort_flag) {
-    constexpr int COLS = 32, LD = 32;   // weight rows of a thread; columns of a TMEM load
+    constexpr int COLS = 32 * C::MATS, LD = C::GATED ? 16 : 32;   // sums of a thread; columns of a TMEM load
     const int q = warp & 3, cg = (warp - 4) >> 2, row = q * 32 + lane;
     const uint32_t lane_addr = tmem_base + ((uint32_t)(q * 32) << 16) + cg * 32;
     int st = 0, slot = 0;
@@ -168,8 +171,8 @@ __device__ __forceinline__ void fold_tokens_m(const Fp8a8Params& p, int warp, in
 #pragma unroll
         for (int k = 0; k < C::SC_KB; ++k) {
             if (kb + k >= kb1) break;
-            const float sf = scr[k * C::SC_PITCH + row] * scr[k * C::SC_PITCH + C::TN];
-            const uint64_t s2 = pack2(sf, sf);
+            const float sx = scr[k * C::SC_PITCH + row], s0 = sx * scr[k * C::SC_PITCH + C::TN];
+            const float s1 = C::GATED ? sx * scr[k * C::SC_PITCH + C::TN + 1] : s0;
             if (!mbar_wait(&done[st], ph, abort_flag, p.err, DEV_TIMEOUT_ACC)) {
                 ok = false;
                 break;
@@ -180,14 +183,15 @@ __device__ __forceinline__ void fold_tokens_m(const Fp8a8Params& p, int warp, in
 #pragma unroll
             for (int x = 0; x < COLS; x += LD) {
                 uint32_t r[LD];
-                tmem_ld(a0 + x, r);
+                tmem_ld(a0 + (x / 32) * 128 + x % 32, r);
                 tmem_ld_wait();
                 if (x + LD == COLS) {
-                    // every column is in registers: the MMA may write the buffer again
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&acc_empty[buf]);
                 }
+                const float sf = x < 32 ? s0 : s1;
+                const uint64_t s2 = pack2(sf, sf);
 #pragma unroll
                 for (int j = 0; j < LD / 2; ++j) acc[x / 2 + j] = fma2(pack2u(r[2 * j], r[2 * j + 1]), s2, acc[x / 2 + j]);
             }
@@ -207,7 +211,7 @@ __device__ __forceinline__ void fold_tokens_m(const Fp8a8Params& p, int warp, in
 #pragma unroll
     for (int j = 0; j < COLS / 4; ++j) {
         const float2 a = unpack2(acc[2 * j]), b = unpack2(acc[2 * j + 1]);
-        *reinterpret_cast<float4*>(sums + row * 128 + (((cg * 8 + j) ^ lane) << 2)) = make_float4(a.x, a.y, b.x, b.y);
+        *reinterpret_cast<float4*>(sums + ((j / 8) * C::TN + row) * 128 + (((cg * 8 + j % 8) ^ lane) << 2)) = make_float4(a.x, a.y, b.x, b.y);
     }
 }
 
@@ -264,102 +268,106 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
     if (warp >= 4) {
+        if constexpr (C::REG_SPLIT) setmaxnreg_inc<C::REGS_FOLD>();
         if constexpr (C::TOKENS_M) fold_tokens_m<C>(p, warp, lane, kb0, kb1, tmem_base, sc, sums, done, acc_empty, sc_full, sc_empty, abort_flag);
         else fold_weights_m<C>(p, warp, lane, kb0, kb1, tmem_base, sc, sums, done, acc_empty, sc_full, sc_empty, abort_flag);
-    } else if (warp == 0) {
-        // ------------------------------------------------------------ producer
-        int s = 0;
-        uint32_t ph = 0;
-        long issued = 0;
-        for (int kb = kb0; kb < kb1; ++kb) {
-            const bool got = mbar_wait(&done[s], ph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_TMA_EMPTY);
-            if (__any_sync(0xffffffffu, !got)) break;
-            // one copy at a time executes per thread: each copy of a stage on its own lane
-            const int c = lane - s * C::COPIES;
-            if (c == 0) mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
-            __syncwarp();
-            uint8_t* dst = stage + s * C::STAGE_BYTES + c * 128 * 128;
-            if (c >= 0 && c < C::MATS) tma_load_2d(dst, &tmW, &full[s], kb * 128, c * p.N + n0);
-            else if (c == C::MATS) tma_load_2d(dst, &tmX, &full[s], kb * 128, m0);
-            __syncwarp();
-            ++issued;
-            if (++s == C::STAGES) {
-                s = 0;
-                ph ^= 1u;
-            }
-        }
-        if (lane == 0) drain_ring(full, issued, C::STAGES, p.err);
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        // (In order: the fold's waits rely on a K block's MMAs completing after those of
-        // the blocks before it.)
-        const uint32_t st0 = smem_u32(stage);
-        int s = 0, buf = 0;
-        uint32_t ph = 0, bph = 0;
-        for (int kb = kb0; kb < kb1; ++kb) {
-            const bool got = mbar_wait(&full[s], ph, abort_flag, p.err, DEV_TIMEOUT_TMA_FULL) &&
-                             mbar_wait(&acc_empty[buf], bph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_ACC_EMPTY);
-            if (__any_sync(0xffffffffu, !got)) break;
-            tc_fence_after();
-            const uint32_t sa = st0 + (uint32_t)(s * C::STAGE_BYTES);
-            const uint64_t xd = smem_desc_sw128(sa + C::W_BYTES);
-            const uint32_t d = tmem_base + (uint32_t)(buf * C::ACC_COLS);
-            if (elect_one_sync()) {
-                if constexpr (C::TOKENS_M) {
-                    const uint64_t wd = smem_desc_sw128(sa);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)   // 32 codes (32 bytes) per MMA
-                        tc_mma_f8(d, xd + (uint64_t)(k * 2), wd + (uint64_t)(k * 2), idesc_e4m3(128, 128), k > 0);
-                } else {
-#pragma unroll
-                    for (int m = 0; m < C::MATS; ++m) {
-                        const uint64_t wd = smem_desc_sw128(sa + m * 128 * 128);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tc_mma_f8(d + m * C::TN, wd + (uint64_t)(k * 2), xd + (uint64_t)(k * 2), idesc_e4m3(128, C::TN), k > 0);
-                    }
+    } else {
+        if constexpr (C::REG_SPLIT) setmaxnreg_dec<C::REGS_OTHER>();
+        if (warp == 0) {
+            // ------------------------------------------------------------ producer
+            int s = 0;
+            uint32_t ph = 0;
+            long issued = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                const bool got = mbar_wait(&done[s], ph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_TMA_EMPTY);
+                if (__any_sync(0xffffffffu, !got)) break;
+                // one copy at a time executes per thread: each copy of a stage on its own lane
+                const int c = lane - s * C::COPIES;
+                if (c == 0) mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
+                __syncwarp();
+                uint8_t* dst = stage + s * C::STAGE_BYTES + c * 128 * 128;
+                if (c >= 0 && c < C::MATS) tma_load_2d(dst, &tmW, &full[s], kb * 128, c * p.N + n0);
+                else if (c == C::MATS) tma_load_2d(dst, &tmX, &full[s], kb * 128, m0);
+                __syncwarp();
+                ++issued;
+                if (++s == C::STAGES) {
+                    s = 0;
+                    ph ^= 1u;
                 }
-                tc_commit(&done[s]);
             }
+            if (lane == 0) drain_ring(full, issued, C::STAGES, p.err);
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ MMA issuer
+            // (In order: the fold's waits rely on a K block's MMAs completing after those of
+            // the blocks before it.)
+            const uint32_t st0 = smem_u32(stage);
+            int s = 0, buf = 0;
+            uint32_t ph = 0, bph = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                const bool got = mbar_wait(&full[s], ph, abort_flag, p.err, DEV_TIMEOUT_TMA_FULL) &&
+                                 mbar_wait(&acc_empty[buf], bph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_ACC_EMPTY);
+                if (__any_sync(0xffffffffu, !got)) break;
+                tc_fence_after();
+                const uint32_t sa = st0 + (uint32_t)(s * C::STAGE_BYTES);
+                const uint64_t xd = smem_desc_sw128(sa + C::W_BYTES);
+                const uint32_t d = tmem_base + (uint32_t)(buf * C::ACC_COLS);
+                if (elect_one_sync()) {
+                    if constexpr (C::TOKENS_M) {
+                        const uint64_t wd = smem_desc_sw128(sa);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)   // 32 codes (32 bytes) per MMA
+                            tc_mma_f8(d, xd + (uint64_t)(k * 2), wd + (uint64_t)(k * 2), idesc_e4m3(128, C::ACC_COLS), k > 0);
+                    } else {
+#pragma unroll
+                        for (int m = 0; m < C::MATS; ++m) {
+                            const uint64_t wd = smem_desc_sw128(sa + m * 128 * 128);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                tc_mma_f8(d + m * C::TN, wd + (uint64_t)(k * 2), xd + (uint64_t)(k * 2), idesc_e4m3(128, C::TN), k > 0);
+                        }
+                    }
+                    tc_commit(&done[s]);
+                }
+                __syncwarp();
+                if (++buf == C::NBUF) {
+                    buf = 0;
+                    bph ^= 1u;
+                }
+                if (++s == C::STAGES) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (elect_one_sync()) tc_commit(drain);
             __syncwarp();
-            if (++buf == C::NBUF) {
-                buf = 0;
-                bph ^= 1u;
+            if (lane == 0) drain_ring(drain, 1, 1, p.err);
+            __syncwarp();
+        } else if (warp == 2) {
+            // ------------------------------------------------------------ scales
+            int slot = 0;
+            uint32_t sph = 0;
+            const long b0 = n0 / 128, b1 = (p.N + n0) / 128;   // weight blocks (gated: gate, up)
+            for (int kb = kb0; kb < kb1; kb += C::SC_KB) {
+                if (!mbar_wait(&sc_empty[slot], sph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_CONV_EMPTY)) break;
+                float* dst = sc + slot * C::SC_KB * C::SC_PITCH;
+                for (int i = lane; i < C::SC_KB * C::TN; i += 32) {
+                    const int k = i / C::TN, r = i % C::TN;
+                    const bool in = kb + k < kb1 && m0 + r < p.M;
+                    cp_async4(dst + k * C::SC_PITCH + r, in ? p.Xs + (long)(m0 + r) * kbs + kb + k : p.Xs, in);
+                }
+                if (lane < C::MATS * C::SC_KB) {
+                    const int k = lane / C::MATS, m = lane % C::MATS;
+                    const bool in = kb + k < kb1;
+                    cp_async4(dst + k * C::SC_PITCH + C::TN + m, in ? p.S + (m ? b1 : b0) * kbs + kb + k : p.S, in);
+                }
+                cp_async_arrive(&sc_full[slot]);
+                if (++slot == C::SC_SLOTS) {
+                    slot = 0;
+                    sph ^= 1u;
+                }
             }
-            if (++s == C::STAGES) {
-                s = 0;
-                ph ^= 1u;
-            }
+            cp_async_wait_all();
         }
-        if (elect_one_sync()) tc_commit(drain);
-        __syncwarp();
-        if (lane == 0) drain_ring(drain, 1, 1, p.err);
-        __syncwarp();
-    } else if (warp == 2) {
-        // ------------------------------------------------------------ scales
-        int slot = 0;
-        uint32_t sph = 0;
-        const long b0 = n0 / 128, b1 = (p.N + n0) / 128;   // weight blocks (gated: gate, up)
-        for (int kb = kb0; kb < kb1; kb += C::SC_KB) {
-            if (!mbar_wait(&sc_empty[slot], sph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_CONV_EMPTY)) break;
-            float* dst = sc + slot * C::SC_KB * C::SC_PITCH;
-            for (int i = lane; i < C::SC_KB * C::TN; i += 32) {
-                const int k = i / C::TN, r = i % C::TN;
-                const bool in = kb + k < kb1 && m0 + r < p.M;
-                cp_async4(dst + k * C::SC_PITCH + r, in ? p.Xs + (long)(m0 + r) * kbs + kb + k : p.Xs, in);
-            }
-            if (lane < C::MATS * C::SC_KB) {
-                const int k = lane / C::MATS, m = lane % C::MATS;
-                const bool in = kb + k < kb1;
-                cp_async4(dst + k * C::SC_PITCH + C::TN + m, in ? p.S + (m ? b1 : b0) * kbs + kb + k : p.S, in);
-            }
-            cp_async_arrive(&sc_full[slot]);
-            if (++slot == C::SC_SLOTS) {
-                slot = 0;
-                sph ^= 1u;
-            }
-        }
-        cp_async_wait_all();
     }
 
     __syncthreads();
@@ -421,6 +429,14 @@ cudaError_t prepare(int* dev) {
     if (!ready[*dev]) {
         e = cudaFuncSetAttribute(fp8a8_narrow_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
+        if constexpr (C::REG_SPLIT) {
+            // the warpgroups' shares add up to the launch's registers: launch only if the
+            // kernel is allocated exactly that many (a setmaxnreg.inc past the pool waits)
+            cudaFuncAttributes fa{};
+            e = cudaFuncGetAttributes(&fa, fp8a8_narrow_kernel<C>);
+            if (e != cudaSuccess) return e;
+            if (fa.numRegs != C::REGS) return cudaErrorInvalidConfiguration;
+        }
         ready[*dev] = true;
     }
     return cudaSuccess;
@@ -483,7 +499,8 @@ auto with_config(bool gated, int tn, F f) {
     if (gated) {
         if (tn == 16) return f(NarrowCfg<16, true>{});
         if (tn == 32) return f(NarrowCfg<32, true>{});
-        return f(NarrowCfg<64, true>{});
+        if (tn == 64) return f(NarrowCfg<64, true>{});
+        return f(NarrowCfg<128, true>{});
     }
     if (tn == 16) return f(NarrowCfg<16, false>{});
     if (tn == 32) return f(NarrowCfg<32, false>{});

@@ -8,7 +8,7 @@ namespace {
 constexpr int kBn[3] = {256, 192, 128};
 constexpr double kPairEnds[3] = {4.0, 2.9, 1.5}, kPairKb[3] = {0.42, 0.375, 0.245};
 constexpr int kTn[4] = {16, 32, 64, 128};
-constexpr double kNarrowKb[2][4] = {{0.21, 0.23, 0.27, 0.30}, {0.27, 0.37, 0.50, 0.0}};
+constexpr double kNarrowKb[2][4] = {{0.21, 0.23, 0.27, 0.30}, {0.27, 0.37, 0.50, 0.65}};
 
 constexpr double kSecondLaunch = 1.5;
 
@@ -38,7 +38,7 @@ Fp8a8Plan one_launch(int M, int kbs, int cols, bool gated, int sms, double* time
             best = pl;
         }
     };
-    for (int i = 0; i < (gated ? 3 : 4); ++i) {
+    for (int i = 0; i < 4; ++i) {
         const long tiles = (long)((cols + 127) / 128) * ((M + kTn[i] - 1) / kTn[i]);
         if (tiles > 8L * sms) continue;   // the pair kernel's
         for (int cs = 1; cs <= 8 && cs <= kbs; ++cs) {
@@ -47,9 +47,10 @@ Fp8a8Plan one_launch(int M, int kbs, int cols, bool gated, int sms, double* time
             Fp8a8Plan pl{};
             pl.tn = kTn[i];
             pl.cs = cs;
-            // (adding up costs a little for each CTA of a cluster)
+            // (adding up costs a little for each CTA of a cluster and for each token)
             consider(pl, (double)((tiles + at_once - 1) / at_once) *
-                                 (2.2 + 0.1 * cs + (kbs + cs - 1) / cs * kNarrowKb[gated][i]) +
+                                 (2.0 + 0.1 * cs + 0.011 * kTn[i] * (gated ? 2 : 1) +
+                                  (kbs + cs - 1) / cs * kNarrowKb[gated][i]) +
                              traffic_time(tiles, kbs, kTn[i] + (gated ? 256 : 128)));
         }
     }
