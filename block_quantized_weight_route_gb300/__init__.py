@@ -230,18 +230,18 @@ def qmm_q8_0_q8_1(Xq, Xd, Wq, Wd, ws=None, fp32_out: bool = False) -> dict:
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 _F8 = (torch.float8_e4m3fn, torch.uint8, torch.int8)
 _F32 = (torch.float32,)
+_Tensor = torch.Tensor
 
 
 def _ok(t, dtypes, shape) -> bool:
     """Whether _need would pass.  The calls below take a few microseconds on the GPU, so
     what passes is checked in one expression; _need words the error of what does not."""
-    return isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.shape == shape and t.is_contiguous()
+    return isinstance(t, _Tensor) and t.is_cuda and t.dtype in dtypes and t.shape == shape and t.is_contiguous()
 
 
 def _raw_stream(device) -> int:
     """The current stream's handle, without making a Stream object."""
-    i = device.index
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if i is None else i)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _pitch(t: torch.Tensor, name: str, shape) -> int:
@@ -328,12 +328,10 @@ def qmm_add_rmsnorm_q8_1(X, G, R=None, eps: float = 1e-6, Rout=None, Y=None, bf1
 def _need_operands(Xq, Xs, W, S, M: int, K: int, rows: int, blocks: int, name_w: str, name_s: str) -> None:
     """The operands of the two FP8 x FP8 products."""
     kb = (K + 127) // 128
-    if not (_ok(Xq, _F8, (M, K)) and _ok(Xs, _F32, (M, kb)) and _ok(W, _F8, (rows, K)) and
-            _ok(S, _F32, (blocks, kb))):
-        _need(Xq, "Xq", _F8, (M, K))
-        _need(Xs, "Xs", _F32, (M, kb))
-        _need(W, name_w, _F8, (rows, K))
-        _need(S, name_s, _F32, (blocks, kb))
+    _need(Xq, "Xq", _F8, (M, K))
+    _need(Xs, "Xs", _F32, (M, kb))
+    _need(W, name_w, _F8, (rows, K))
+    _need(S, name_s, _F32, (blocks, kb))
 
 
 def qmm_fp8a8_blk128(Xq, Xs, W, S, out_dtype=torch.bfloat16, Y=None):
@@ -343,7 +341,10 @@ def qmm_fp8a8_blk128(Xq, Xs, W, S, out_dtype=torch.bfloat16, Y=None):
     N = W.shape[0]
     if out_dtype not in _DTYPE:
         raise TypeError("out_dtype must be float32 or bfloat16")
-    _need_operands(Xq, Xs, W, S, M, K, N, (N + 127) // 128, "W", "S")
+    kb = (K + 127) // 128
+    if not (_ok(Xq, _F8, Xq.shape) and _ok(Xs, _F32, (M, kb)) and _ok(W, _F8, (N, K)) and
+            _ok(S, _F32, ((N + 127) // 128, kb))):
+        _need_operands(Xq, Xs, W, S, M, K, N, (N + 127) // 128, "W", "S")
     if Y is None:
         Y = torch.empty((M, N), dtype=out_dtype, device=Xq.device)
     elif not _ok(Y, (out_dtype,), (M, N)):
@@ -361,7 +362,10 @@ def qmm_fp8a8_swiglu_blk128(Xq, Xs, Wgu, Sgu, Hq=None, Hs=None):
     rows first), Sgu [2F/128, ceil(K/128)] fp32."""
     M, K = Xq.shape
     F = Wgu.shape[0] // 2
-    _need_operands(Xq, Xs, Wgu, Sgu, M, K, 2 * F, 2 * F // 128, "Wgu", "Sgu")
+    kb = (K + 127) // 128
+    if not (_ok(Xq, _F8, Xq.shape) and _ok(Xs, _F32, (M, kb)) and _ok(Wgu, _F8, (2 * F, K)) and
+            _ok(Sgu, _F32, (2 * F // 128, kb))):
+        _need_operands(Xq, Xs, Wgu, Sgu, M, K, 2 * F, 2 * F // 128, "Wgu", "Sgu")
     if Hq is None:
         Hq = torch.empty((M, F), dtype=torch.float8_e4m3fn, device=Xq.device)
     elif not _ok(Hq, _F8, (M, F)):

@@ -47,6 +47,7 @@ struct DeviceState {
     qmm_status status = QMM_OK;
     std::string why;
     int sms = 0;
+    int index = 0;
     uint32_t* err = nullptr;
 };
 
@@ -64,6 +65,7 @@ qmm_status device_state(DeviceState** out) {
     std::lock_guard<std::mutex> lock(g_mu);
     DeviceState& d = g_dev[dev];
     if (!d.ready) {
+        d.index = dev;
         int major = 0, minor = 0;
         cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
@@ -916,7 +918,7 @@ qmm_status qmm_add_rmsnorm_q8_1(const void* X, qmm_dtype xdt, int64_t ldx, const
 // ---------------------------------------------------------------- FP8 x FP8 products
 
 static qmm_status run_fp8a8(const char* who, DeviceState* d, Fp8a8Params& p, bool gated, cudaStream_t stream) {
-    const Fp8a8Plans plans = fp8a8_plan(p.M, p.K, p.N, gated, d->sms);
+    const Fp8a8Plans plans = fp8a8_plan(p.M, p.K, p.N, gated, d->sms, d->index);
     p.err = d->err;
     for (int part = 0; part < (plans.split < p.N ? 2 : 1); ++part) {
         const Fp8a8Plan& pl = part ? plans.second : plans.first;
@@ -932,8 +934,8 @@ static qmm_status run_fp8a8(const char* who, DeviceState* d, Fp8a8Params& p, boo
         if ((st = make_tmap(&tw, p.W, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, (uint64_t)p.N * (gated ? 2 : 1), p.K, 128,
                             pl.pair ? pl.bn / 2 : 128, CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK)
             return st;
-        const cudaError_t e = pl.pair ? launch_fp8a8_pair(tx, tw, p, gated, pl.bn, d->sms, stream)
-                                      : launch_fp8a8_narrow(tx, tw, p, gated, pl.tn, pl.cs, stream);
+        const cudaError_t e = pl.pair ? launch_fp8a8_pair(tx, tw, p, gated, pl.bn, d->sms, d->index, stream)
+                                      : launch_fp8a8_narrow(tx, tw, p, gated, pl.tn, pl.cs, d->index, stream);
         if (e != cudaSuccess) return cuda_fail(e, who);
     }
     return QMM_OK;

@@ -420,14 +420,12 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     }
 }
 
+// One-time set-up on device `dev` (the current one, below 64).
 template <class C>
-cudaError_t prepare(int* dev) {
+cudaError_t prepare(int dev) {
     static bool ready[64] = {};
-    cudaError_t e = cudaGetDevice(dev);
-    if (e != cudaSuccess) return e;
-    if (*dev < 0 || *dev >= 64) return cudaErrorInvalidDevice;
-    if (!ready[*dev]) {
-        e = cudaFuncSetAttribute(fp8a8_narrow_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (!ready[dev]) {
+        cudaError_t e = cudaFuncSetAttribute(fp8a8_narrow_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
         if constexpr (C::REG_SPLIT) {
             // the warpgroups' shares add up to the launch's registers: launch only if the
@@ -437,15 +435,14 @@ cudaError_t prepare(int* dev) {
             if (e != cudaSuccess) return e;
             if (fa.numRegs != C::REGS) return cudaErrorInvalidConfiguration;
         }
-        ready[*dev] = true;
+        ready[dev] = true;
     }
     return cudaSuccess;
 }
 
 template <class C>
-cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, int cs, cudaStream_t s) {
-    int dev = 0;
-    const cudaError_t e = prepare<C>(&dev);
+cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, int cs, int dev, cudaStream_t s) {
+    const cudaError_t e = prepare<C>(dev);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -468,11 +465,10 @@ cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Para
 namespace {
 
 template <class C>
-int clusters_at_once(int cs) {
+int clusters_at_once(int cs, int dev) {
     static int at_once[64][9] = {};
-    int dev = 0;
-    if (cs < 1 || cs > 8 || prepare<C>(&dev) != cudaSuccess) return 0;
     if (at_once[dev][cs] == 0) {
+        if (prepare<C>(dev) != cudaSuccess) return 0;
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -511,13 +507,13 @@ auto with_config(bool gated, int tn, F f) {
 }  // namespace
 
 // (A cluster's CTAs are on SMs of one group of SMs, so fewer fit than slots / cs.)
-int fp8a8_narrow_at_once(bool gated, int tn, int cs) {
-    return with_config(gated, tn, [&](auto c) { return clusters_at_once<decltype(c)>(cs); });
+int fp8a8_narrow_at_once(bool gated, int tn, int cs, int dev) {
+    return with_config(gated, tn, [&](auto c) { return clusters_at_once<decltype(c)>(cs, dev); });
 }
 
 cudaError_t launch_fp8a8_narrow(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, bool gated, int tn,
-                                int cs, cudaStream_t s) {
-    return with_config(gated, tn, [&](auto c) { return launch<decltype(c)>(tx, tw, p, cs, s); });
+                                int cs, int dev, cudaStream_t s) {
+    return with_config(gated, tn, [&](auto c) { return launch<decltype(c)>(tx, tw, p, cs, dev, s); });
 }
 
 }  // namespace qmm

@@ -368,12 +368,9 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
 }
 
 template <class C>
-cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, int sms, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, int sms, int dev, cudaStream_t s) {
     static int most[64] = {};   // pairs that fit the device at once
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    cudaError_t e;
     if (most[dev] == 0) {
         e = cudaFuncSetAttribute(fp8a8_pair_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
@@ -414,13 +411,13 @@ cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Para
 }  // namespace
 
 cudaError_t launch_fp8a8_pair(const CUtensorMap& tx, const CUtensorMap& tw, Fp8a8Params p, bool gated, int bn, int sms,
-                              cudaStream_t s) {
+                              int dev, cudaStream_t s) {
     p.m_tiles = (p.M + 255) / 256;
     p.n_tiles = (p.n_end - p.n_first + (gated ? 127 : bn - 1)) / (gated ? 128 : bn);
-    if (gated) return launch<PairCfg<256, true>>(tx, tw, p, sms, s);
-    if (bn == 256) return launch<PairCfg<256, false>>(tx, tw, p, sms, s);
-    if (bn == 192) return launch<PairCfg<192, false>>(tx, tw, p, sms, s);
-    return launch<PairCfg<128, false>>(tx, tw, p, sms, s);
+    if (gated) return launch<PairCfg<256, true>>(tx, tw, p, sms, dev, s);
+    if (bn == 256) return launch<PairCfg<256, false>>(tx, tw, p, sms, dev, s);
+    if (bn == 192) return launch<PairCfg<192, false>>(tx, tw, p, sms, dev, s);
+    return launch<PairCfg<128, false>>(tx, tw, p, sms, dev, s);
 }
 
 }  // namespace qmm

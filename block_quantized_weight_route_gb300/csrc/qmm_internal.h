@@ -163,12 +163,12 @@ struct Fp8a8Plans {
     Fp8a8Plan first, second;
     int split;
 };
-Fp8a8Plans fp8a8_plan(int M, int K, int N, bool gated, int sms);
-int fp8a8_narrow_at_once(bool gated, int tn, int cs);   // clusters of cs CTAs that the device holds at once (0: error)
+Fp8a8Plans fp8a8_plan(int M, int K, int N, bool gated, int sms, int dev);
+int fp8a8_narrow_at_once(bool gated, int tn, int cs, int dev);   // clusters of cs CTAs that the device holds at once (0: error)
 cudaError_t launch_fp8a8_narrow(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, bool gated, int tn,
-                                int cs, cudaStream_t s);
+                                int cs, int dev, cudaStream_t s);
 cudaError_t launch_fp8a8_pair(const CUtensorMap& tx, const CUtensorMap& tw, Fp8a8Params p, bool gated, int bn, int sms,
-                              cudaStream_t s);
+                              int dev, cudaStream_t s);
 
 // Set the calling thread's message returned by qmm_last_error().
 void set_last_error(const char* msg);
