@@ -8,6 +8,10 @@
 // whose loads (x, the residual and g) are issued before anything waits on them.  A CTA
 // takes one row, or, for rows of at most 1024 values, each warp one.  16 (or 4)
 // consecutive lanes hold one group, whose maximum is a few shuffles.
+// Measured: 21504 x 2560, fp32 rows and residual, bf16 rows out beside the codes (830 MB)
+// 118 us = 7.0 TB/s; all bf16 56 us = 6.9 TB/s; 2048 x 5120 bf16 (74 MB) 14.0 us = 5.3 TB/s;
+// 5268 x 2048, fp32 rows, bf16 residual, q8_1 (98 MB) 17.6 us = 5.6 TB/s; one row 2.2 us,
+// the launch.  Not kept: a persistent grid that loads the next row ahead (slower).
 #include "qmm_internal.h"
 #include "quant8.cuh"
 
@@ -23,13 +27,27 @@ __device__ __forceinline__ void unpack_bf16(const uint4& u, uint64_t (&v)[4]) {
     for (int j = 0; j < 4; ++j) v[j] = pack2u(w[j] << 16, w[j] & 0xFFFF0000u);
 }
 
-__device__ __forceinline__ void load8(const void* p, long i, bool bf16, uint64_t (&v)[4]) {
+// Eight consecutive values as they lie in memory.  Turned into fp32 only when all of a
+// thread's loads are on their way: with the conversion in the same branch as the load,
+// the next load waits for it.
+struct Raw8 {
+    uint4 lo, hi;   // (bf16: lo only)
+};
+
+__device__ __forceinline__ Raw8 load8(const void* p, long i, bool bf16) {
+    Raw8 u;
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + i * (bf16 ? 2 : 4));
+    u.lo = q[0];
+    u.hi = bf16 ? make_uint4(0, 0, 0, 0) : q[1];
+    return u;
+}
+
+__device__ __forceinline__ void widen8(const Raw8& u, bool bf16, uint64_t (&v)[4]) {
     if (bf16) {
-        unpack_bf16(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i), v);
+        unpack_bf16(u.lo, v);
     } else {
-        const ulonglong2* q = reinterpret_cast<const ulonglong2*>(static_cast<const float*>(p) + i);
-        const ulonglong2 a = q[0], b = q[1];
-        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+        v[0] = pack2u(u.lo.x, u.lo.y), v[1] = pack2u(u.lo.z, u.lo.w);
+        v[2] = pack2u(u.hi.x, u.hi.y), v[3] = pack2u(u.hi.z, u.hi.w);
     }
 }
 
@@ -51,8 +69,9 @@ __device__ __forceinline__ float lanes_max(float a) {
     return a;
 }
 
-template <bool Q81, int NV, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rmsnorm8_kernel(NormParams p) {
+// HALF: x, the residual and g are all bf16
+template <bool Q81, int NV, bool WARP, bool HALF>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : HALF && NV > 1 ? 512 : 1024, !WARP && NV == 4 ? 2 : 0) rmsnorm8_kernel(NormParams p) {
     __shared__ float part[32];
     launch_dependents();
     wait_prerequisites();
@@ -60,26 +79,30 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rmsnorm8_kernel(
     const long t = WARP ? (long)blockIdx.x * kWarpRows + warp : (long)blockIdx.x;
     const int first = WARP ? lane : (int)threadIdx.x, step = WARP ? 32 : (int)blockDim.x;
     if (WARP && t >= p.T) return;
-    uint64_t v[NV][4], r[NV][4], g[NV][4];
+    const Raw8 none = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    Raw8 vr[NV], rr[NV], gr[NV];
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
         const int i = (n * step + first) * 8;
+        vr[n] = rr[n] = gr[n] = none;
         if (i < p.D) {
-            load8(p.X, t * p.ldx + i, p.x_bf16, v[n]);
-            if (p.R) load8(p.R, t * p.ldr + i, p.r_bf16, r[n]);
-            load8(p.G, i, p.g_bf16, g[n]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[n][j] = r[n][j] = g[n][j] = 0;
+            vr[n] = load8(p.X, t * p.ldx + i, HALF || p.x_bf16);
+            if (p.R) rr[n] = load8(p.R, t * p.ldr + i, HALF || p.r_bf16);
+            gr[n] = load8(p.G, i, HALF || p.g_bf16);
         }
     }
+    uint64_t v[NV][4];
+#pragma unroll
+    for (int n = 0; n < NV; ++n) widen8(vr[n], HALF || p.x_bf16, v[n]);
     if (p.R) {
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const int i = (n * step + first) * 8;
+            uint64_t r[4];
+            widen8(rr[n], HALF || p.r_bf16, r);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[n][j] = add2(v[n][j], r[n][j]);
-            if (p.r_bf16) {
+            for (int j = 0; j < 4; ++j) v[n][j] = add2(v[n][j], r[j]);
+            if (HALF || p.r_bf16) {
                 // the stored sum is what the next layer adds to, so the norm is of the
                 // stored (rounded) sum
                 const uint4 u = pack_bf16(v[n]);
@@ -113,11 +136,12 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rmsnorm8_kernel(
     for (int n = 0; n < NV; ++n) {
         const int i = (n * step + first) * 8;
         const bool in = i < p.D;
-        uint64_t y[4];
+        uint64_t y[4], g[4];
+        widen8(gr[n], HALF || p.g_bf16, g);
         float f[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            y[j] = mul2(mul2(v[n][j], pack2(rstd, rstd)), g[n][j]);   // (0 past the row's end)
+            y[j] = mul2(mul2(v[n][j], pack2(rstd, rstd)), g[j]);   // (0 past the row's end)
             const float2 h = unpack2(y[j]);
             f[2 * j] = h.x, f[2 * j + 1] = h.y;
         }
@@ -173,20 +197,23 @@ cudaError_t launch(const NormParams& p, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const int vecs = (p.D + 7) / 8;
+    const bool half = p.x_bf16 && p.g_bf16 && (!p.R || p.r_bf16);
     if (vecs <= 128) {
         cfg.gridDim = dim3((p.T + kWarpRows - 1) / kWarpRows, 1, 1);
         cfg.blockDim = dim3(32 * kWarpRows, 1, 1);
-        if (vecs <= 32) return cudaLaunchKernelEx(&cfg, rmsnorm8_kernel<Q81, 1, true>, p);
-        if (vecs <= 64) return cudaLaunchKernelEx(&cfg, rmsnorm8_kernel<Q81, 2, true>, p);
-        return cudaLaunchKernelEx(&cfg, rmsnorm8_kernel<Q81, 4, true>, p);
+        if (vecs <= 32) return cudaLaunchKernelEx(&cfg, half ? rmsnorm8_kernel<Q81, 1, true, true> : rmsnorm8_kernel<Q81, 1, true, false>, p);
+        if (vecs <= 64) return cudaLaunchKernelEx(&cfg, half ? rmsnorm8_kernel<Q81, 2, true, true> : rmsnorm8_kernel<Q81, 2, true, false>, p);
+        return cudaLaunchKernelEx(&cfg, half ? rmsnorm8_kernel<Q81, 4, true, true> : rmsnorm8_kernel<Q81, 4, true, false>, p);
     }
-    // one vector a thread while a CTA has the threads (two: 24 us against 20 at 2048 x 5120
-    // bf16 with residual, 3.1 against 2.6 for one row; four: 32 and 5.7)
-    const int nv = vecs <= 1024 ? 1 : 2;
+    // What is in flight on an SM sets the bandwidth: bf16 vectors are half as large and their
+    // kernel needs fewer registers, so a thread takes two (21504 x 2560: 56 us against 63 with
+    // one; one row 0.1 us more), above 8192 four (4096 x 16384: 73 us against 87 with two);
+    // fp32 vectors one, above 8192 two
+    const int nv = half ? (vecs <= 1024 ? 2 : 4) : vecs <= 1024 ? 1 : 2;
     cfg.gridDim = dim3(p.T, 1, 1);
     cfg.blockDim = dim3(((vecs + nv - 1) / nv + 31) / 32 * 32, 1, 1);
-    if (nv == 1) return cudaLaunchKernelEx(&cfg, rmsnorm8_kernel<Q81, 1, false>, p);
-    return cudaLaunchKernelEx(&cfg, rmsnorm8_kernel<Q81, 2, false>, p);
+    if (half) return cudaLaunchKernelEx(&cfg, nv == 2 ? rmsnorm8_kernel<Q81, 2, false, true> : rmsnorm8_kernel<Q81, 4, false, true>, p);
+    return cudaLaunchKernelEx(&cfg, nv == 1 ? rmsnorm8_kernel<Q81, 1, false, false> : rmsnorm8_kernel<Q81, 2, false, false>, p);
 }
 
 }  // namespace
