@@ -15,6 +15,11 @@
 // With 128 tokens a tile (TOKENS_M) the tokens are the M side and the weights the N side:
 // swapped, every fold thread reads every token's scale from shared memory, 512 cycles a
 // K block for 128 tokens; with a token per lane it reads one.
+// What bounds it: with a few tokens the weights' way from HBM once it flows (gate/up of one
+// token, 178 MB: 29 us, 6.1 TB/s = 0.90 of a plain copy) and, for a single small matrix, the
+// launch and the cluster's sum (5120 x 5120, 26 MB: 6.6 us, 4.0 TB/s); at 128 tokens a tile
+// shared memory (32 KB written and read a K block, 0.27 of the 0.30 us it takes; 300 x 5120 x
+// 5120: 17.2 us).
 #include "fp8a8.cuh"
 
 namespace qmm {

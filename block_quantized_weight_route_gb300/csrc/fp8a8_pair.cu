@@ -6,21 +6,27 @@
 // Persistent CTA pairs (cta_group::2), each on one 256 x BN tile: the even CTA
 // issues M = 256, N = BN, K = 32 MMAs over both CTAs' shared memory, each CTA's
 // TMEM holds its 128 rows x BN columns of P_kb.  A block's sum cannot stay in the
-// tensor core (its scale differs by row and by block), so 16 warps fold each
-// P_kb into fp32 running sums in registers, two TMEM buffers apart from the MMA.
+// tensor core (its scale differs by row and by block), so the fold warps take each
+// P_kb out of TMEM into fp32 running sums in registers, two or four TMEM buffers
+// apart from the MMA.
 //   warp 0: TMA producer   warp 1: MMA issuer (even CTA)
 //   warps 2, 3: the scales of four K blocks at a time, by asynchronous copies into a ring
-//   warps 4..19: fold; warp w reads TMEM lanes 32 (w % 4) .. +31 (a row per lane) and
-//                quarter (w - 4) / 4 of the columns
+//   warps 4..: fold, four warps for each 64 columns (16, 12 or 8 in all); warp w reads
+//              TMEM lanes 32 (w % 4) .. +31 (a row per lane), columns 64 ((w - 4) / 4) .. +63
 // What bounds it: a TMEM buffer's way from the MMA's end through the fold and back to
 // the even CTA takes about 1000 cycles, even with nothing folded (MMA latency, the commit's
 // and the release's way across the pair): with two buffers that is more than the other
 // buffer's MMA (512 cycles at BN = 256), so the length of the fold's path counts, not its
 // throughput.  BN = 128 has four buffers and is bound by shared memory (48 KB written and
 // read a K block, 470 cycles).  Per K block: 0.42 us at BN = 256, 0.375 at 192, 0.245 at 128.
+// Measured: 2048 x 5120 x 5120 53.8 us (2.0 PFLOP/s; the last 256 columns in the narrow
+// kernel), 5268 x 17408 x 5120 379 us (2.48 PFLOP/s, 410 us in a row of calls that
+// meets the power limit), gate/up 2048 x 5120 x 2 x 17408 294 us (2.49 PFLOP/s, 311 in a row);
+// the tensor pipe is busy for 52% of the cycles there, the issue slots for 63%.
 // Not kept: three buffers of 160 columns with 20 fold warps, halves of the tile with MMAs
 // and warps of their own, two MMA issuers, a producer warp per operand (all within 5%),
-// polling instead of sleeping waits (5% slower).  At 2.4 PFLOP/s the power limit is near:
+// polling instead of sleeping waits (5% slower), 8 fold warps of 128 columns at BN = 256 (as
+// fast for the product, 9% slower for gate/up).  At 2.4 PFLOP/s the power limit is near:
 // without any fold the same loop reaches 3.0 PFLOP/s at clocks down to 1.6 GHz.
 #include "fp8a8.cuh"
 
@@ -40,7 +46,8 @@ struct PairCfg {
     // Fold threads: a row and CW columns, LW of them a TMEM load.  Few large loads are best
     // where the registers hold them (8 fold warps: all 64 columns at once, 37 us against 45
     // with loads of 32 at 256 x 17408 x 5120; 12 warps: 32); 16 warps need more than an even
-    // share of the registers for their sums (a register split) and loads of 8 to spill nothing.
+    // share of the registers for their sums (a register split) and loads of 8 to spill nothing
+    // (loads of 16 spill 24 bytes and take 20% longer).
     static constexpr int CW = 64, GROUPS = BN / CW, FOLD_WARPS = 4 * GROUPS, LW = BN == 256 ? 8 : BN == 192 ? 32 : 64;
     static constexpr int OUT_BYTES = GATED ? 2 * GROUPS * 128 * 4 : FOLD_WARPS * 2048;   // row maxima, or output staging
     static constexpr bool REG_SPLIT = BN == 256;
