@@ -113,6 +113,27 @@ def test_swiglu(q, M, K, F):
     check_swiglu(Hq, Hs, y, tol)
 
 
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_columns_past_the_last_whole_wave(q, dt):
+    """One wave of full tiles and a remainder that goes in a launch of its own (4 x 20 tiles of
+    256 x 256 or 256 x (128 + 128) for 76 pairs of SMs), with a ragged end on both sides."""
+    M, K = 1021, 5120
+    ops = operands(5, M, K, 4999)
+    y, tol = formula(*ops)
+    big = torch.full((M + 1, 4999), 7.0, dtype=dt, device="cuda")
+    q.qmm_fp8a8_blk128(*ops, out_dtype=dt, Y=big[:M])
+    q.qmm_check_status()
+    if dt == BF16:
+        tol = tol + half_bf16_step(np.abs(y) + tol)
+    assert np.all(np.abs(big[:M].double().cpu().numpy() - y) <= tol) and bool((big[M] == 7).all())
+    if dt == F32:
+        ops = operands(6, M, K, 2 * 2560)
+        y, tol = formula(*ops)
+        Hq, Hs = q.qmm_fp8a8_swiglu_blk128(*ops)
+        q.qmm_check_status()
+        check_swiglu(Hq, Hs, y, tol)
+
+
 @pytest.mark.parametrize("M,N", [(1, 128), (24, 200), (130, 512), (600, 384)])
 def test_integers_are_exact(q, M, N):
     """Small integer codes and power-of-two scales: every partial sum is exact."""
