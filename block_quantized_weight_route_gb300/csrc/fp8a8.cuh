@@ -139,6 +139,18 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// Eight outputs as bf16.
+__device__ __forceinline__ uint4 bf16x8(const uint64_t* v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack2(v[i]);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // A warp's staged 32 rows x NC 16-byte chunks (chunk c of row r at c ^ stage_swz<NC>(r),
 // which leaves bank conflicts of two ways at most on both sides) to Y at (row0, col):
 // consecutive lanes write consecutive chunks of a row.
@@ -158,56 +170,83 @@ __device__ __forceinline__ void flush_stage(const Fp8a8Params& p, const uint8_t*
     }
 }
 
+// A lane's 16 consecutive outputs (two per element of `v`) to its row of the staging: as bf16 from
+// chunk c0 of NC on, or as four chunks of fp32.
+template <bool BF16, int NC>
+__device__ __forceinline__ void stage16(uint8_t* stg, int lane, int c0, const uint64_t* v) {
+    if constexpr (BF16) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            *reinterpret_cast<uint4*>(stg + (lane * NC + ((c0 + c) ^ stage_swz<NC>(lane))) * 16) = bf16x8(v + 4 * c);
+    } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float2 a = unpack2(v[2 * c]), b = unpack2(v[2 * c + 1]);
+            *reinterpret_cast<float4*>(stg + (lane * 4 + (c ^ stage_swz<4>(lane))) * 16) = make_float4(a.x, a.y, b.x, b.y);
+        }
+    }
+}
+
+// A warp's staged 32 rows x 64 bytes to rows of Y whose pitch is no multiple of 16 bytes: 16
+// lanes to a row with 4 bytes each.  A row of bf16 that starts at an odd element (4-byte
+// stores are aligned) is shifted by one: its lane 0 writes the first element and the last.
+template <bool BF16>
+__device__ __forceinline__ void flush_ragged(const Fp8a8Params& p, const uint8_t* stg, int lane, long row0, int col) {
+    const int half = lane / 16, w = lane % 16, rows = p.M - (int)row0, cols = p.N - col;
+    auto word = [&](int r, int i) { return reinterpret_cast<const uint32_t*>(stg + (r * 4 + ((i / 4) ^ stage_swz<4>(r))) * 16)[i % 4]; };
+    if constexpr (!BF16) {
+        if (w >= cols) return;
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+            const int r = 2 * i + half;
+            if (r < rows) static_cast<uint32_t*>(p.Y)[(row0 + r) * p.N + col + w] = word(r, w);
+        }
+        return;
+    }
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+        const int r = 2 * i + half;
+        if (r >= rows) break;
+        const int odd = ((int)row0 + r) & p.N & 1, e = 2 * w - odd;   // the word's elements: e, e + 1 (or 31, 0)
+        uint32_t d = word(r, w);
+        if (odd) d = (d << 16) | (word(r, (w + 15) & 15) >> 16);
+        uint16_t* dst = static_cast<uint16_t*>(p.Y) + (row0 + r) * p.N + col + e;
+        if (e >= 0 && e + 1 < cols) {
+            *reinterpret_cast<uint32_t*>(dst) = d;
+        } else {
+            if (e >= 0 && e < cols) dst[0] = (uint16_t)d;
+            if (e < 0 && 31 < cols) dst[32] = (uint16_t)d;
+            if (e < 0 && 0 < cols) dst[1] = (uint16_t)(d >> 16);
+        }
+    }
+}
+
 // A warp's 32 rows x W columns (lane = row, `v` its W consecutive outputs, two per element) to Y at
-// (row0, col), through the warp's 2 KB of staging so that a store instruction writes
-// whole runs of a few rows rather than 16 bytes of 32 rows; element by element where
-// the row pitch is not a multiple of 16 bytes.
-template <int W>
-__device__ __forceinline__ void store_chunk(const Fp8a8Params& p, uint8_t* stg, int lane, long row0, int col,
-                                            const uint64_t* v) {
-    const bool rows16 = (((long)p.N * (p.y_bf16 ? 2 : 4)) & 15) == 0;
-    if (rows16 && p.y_bf16) {
-        constexpr int NC = W / 8;
-        __syncwarp();
+// (row0, col), through the warp's 2 KB of staging, so that a store instruction writes whole
+// runs of a few rows rather than 16 bytes, or one element, of 32 rows (5268 x 1024 x 5119
+// element by element: 262 us; this way 64).  In ragged rows not unrolled: the kernel
+// spills otherwise (2048 x 5120 x 9727: 136 us against 100).
+template <int W, bool BF16, bool RAGGED>
+__device__ __forceinline__ void store_columns(const Fp8a8Params& p, uint8_t* stg, int lane, long row0, int col,
+                                              const uint64_t* v) {
+    if constexpr (!RAGGED) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack2(v[4 * c + i]);
-                const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
-                w[i] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-            *reinterpret_cast<uint4*>(stg + (lane * NC + (c ^ stage_swz<NC>(lane))) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int c = 0; c < W; c += 16) {
+            __syncwarp();
+            stage16<BF16, 2>(stg, lane, 0, v + c / 2);
+            __syncwarp();
+            flush_stage<BF16 ? 2 : 4>(p, stg, lane, row0, col + c, BF16 ? 2 : 4);
         }
-        __syncwarp();
-        flush_stage<NC>(p, stg, lane, row0, col, 2);
-    } else if (rows16) {
-#pragma unroll
-        for (int h = 0; h < W / 16; ++h) {
+    } else {
+        constexpr int STEP = BF16 ? 32 : 16;
+#pragma unroll 1
+        for (int c = 0; c < W; c += STEP) {
             __syncwarp();
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float2 a = unpack2(v[8 * h + 2 * c]), b = unpack2(v[8 * h + 2 * c + 1]);
-                *reinterpret_cast<float4*>(stg + (lane * 4 + (c ^ stage_swz<4>(lane))) * 16) = make_float4(a.x, a.y, b.x, b.y);
-            }
+            for (int k = 0; k < W; k += 16)
+                if (k / STEP * STEP == c) stage16<BF16, 4>(stg, lane, k / 8 & 2, v + k / 2);
             __syncwarp();
-            flush_stage<4>(p, stg, lane, row0, col + 16 * h, 4);
-        }
-    } else if (row0 + lane < p.M) {
-        const long o = (row0 + lane) * p.N + col;
-#pragma unroll
-        for (int j = 0; j < W / 2; ++j) {
-            const float2 f = unpack2(v[j]);
-            if (p.y_bf16) {
-                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.Y) + o + 2 * j;
-                if (col + 2 * j < p.N) dst[0] = __float2bfloat16_rn(f.x);
-                if (col + 2 * j + 1 < p.N) dst[1] = __float2bfloat16_rn(f.y);
-            } else {
-                float* dst = static_cast<float*>(p.Y) + o + 2 * j;
-                if (col + 2 * j < p.N) dst[0] = f.x;
-                if (col + 2 * j + 1 < p.N) dst[1] = f.y;
-            }
+            flush_ragged<BF16>(p, stg, lane, row0, col + c);
         }
     }
 }

@@ -20,8 +20,8 @@
 // throughput.  BN = 128 has four buffers and is bound by shared memory (48 KB written and
 // read a K block, 470 cycles).  Per K block: 0.42 us at BN = 256, 0.375 at 192, 0.245 at 128.
 // Measured: 2048 x 5120 x 5120 53.8 us (2.0 PFLOP/s; the last 256 columns in the narrow
-// kernel), 5268 x 17408 x 5120 379 us (2.48 PFLOP/s, 410 us in a row of calls that
-// meets the power limit), gate/up 2048 x 5120 x 2 x 17408 294 us (2.49 PFLOP/s, 311 in a row);
+// kernel), 5268 x 17408 x 5120 367 us (2.56 PFLOP/s, 400 us in a row of calls that
+// meets the power limit), gate/up 2048 x 5120 x 2 x 17408 289 us (2.53 PFLOP/s, 310 in a row);
 // the tensor pipe is busy for 52% of the cycles there, the issue slots for 63%.
 // Not kept: three buffers of 160 columns with 20 fold warps, halves of the tile with MMAs
 // and warps of their own, two MMA issuers, a producer warp per operand (all within 5%),
@@ -33,10 +33,12 @@
 namespace qmm {
 namespace {
 
-template <int BN_, bool GATED_>
+// RAGGED: Y's row pitch is no multiple of 16 bytes.  BF16: Y is bf16, not fp32.  (One kernel with
+// all four ways to store makes the fold spill.)
+template <int BN_, bool GATED_, bool BF16_ = true, bool RAGGED_ = false>
 struct PairCfg {
     static constexpr int BN = BN_;
-    static constexpr bool GATED = GATED_;
+    static constexpr bool GATED = GATED_, RAGGED = RAGGED_, BF16 = BF16_;
     static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / 2 * 128, STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGES = 163840 / STAGE_BYTES;           // 160 KB of operands
     static constexpr int NBUF = BN <= 128 ? 4 : 2, BUF_COLS = 512 / NBUF;
@@ -46,9 +48,10 @@ struct PairCfg {
     // Fold threads: a row and CW columns, LW of them a TMEM load.  Few large loads are best
     // where the registers hold them (8 fold warps: all 64 columns at once, 37 us against 45
     // with loads of 32 at 256 x 17408 x 5120; 12 warps: 32); 16 warps need more than an even
-    // share of the registers for their sums (a register split) and loads of 8 to spill nothing
-    // (loads of 16 spill 24 bytes and take 20% longer).
-    static constexpr int CW = 64, GROUPS = BN / CW, FOLD_WARPS = 4 * GROUPS, LW = BN == 256 ? 8 : BN == 192 ? 32 : 64;
+    // share of the registers for their sums (a register split) and loads of 16 (367 us against 374
+    // with loads of 8 at 5268 x 17408 x 5120), gate/up of 8 (289 us against 330 with 16 at
+    // 2048 x 5120 x 2 x 17408).
+    static constexpr int CW = 64, GROUPS = BN / CW, FOLD_WARPS = 4 * GROUPS, LW = GATED ? 8 : BN == 256 ? 16 : BN == 192 ? 32 : 64;
     static constexpr int OUT_BYTES = GATED ? 2 * GROUPS * 128 * 4 : FOLD_WARPS * 2048;   // row maxima, or output staging
     static constexpr bool REG_SPLIT = BN == 256;
     static constexpr int THREADS = 128 + 32 * FOLD_WARPS, REGS = 65536 / THREADS / 8 * 8, REGS_FOLD = 104, REGS_OTHER = 64;
@@ -142,10 +145,9 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
         uint32_t ph = 0, sph = 0, rph = 0;
         bool ok = true;
         for (int t = cid; t < tiles && ok; t += ncl, parity ^= 1) {
-            const PairTile ti = pair_tile<C>(p, t, crank);
             // which of the tile's two weight blocks the thread's 64 columns are in (gated: the
             // first half in one, the second in the other)
-            const int blk = !C::GATED && cq * C::CW >= 128 - (ti.n0 & 127);
+            const int blk = !C::GATED && cq * C::CW >= 128 - (pair_tile<C>(p, t, crank).n0 & 127);
             uint64_t acc[C::CW / 2];
 #pragma unroll
             for (int j = 0; j < C::CW / 2; ++j) acc[j] = 0;
@@ -199,11 +201,12 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
                 }
             }
             if (!ok) break;
+            int te = t;   // (the tile's place is worked out again, not kept in registers through its K blocks)
+            asm volatile("" : "+r"(te));
+            const PairTile ti = pair_tile<C>(p, te, crank);
             if constexpr (!C::GATED) {
                 uint8_t* stg = outs + (warp - 4) * 2048;
-#pragma unroll
-                for (int c = 0; c < C::CW; c += 16)
-                    store_chunk<16>(p, stg, lane, (long)ti.m0 + q * 32, ti.n0 + fold_col<C>(cq, c), acc + c / 2);
+                store_columns<C::CW, C::BF16, C::RAGGED>(p, stg, lane, (long)ti.m0 + q * 32, ti.n0 + fold_col<C>(cq, 0), acc);
             } else {
                 // the first half of acc: gate columns; the second half: the same columns of up
                 constexpr int HP = C::CW / 4;   // pairs
@@ -415,6 +418,16 @@ cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Para
     return cudaLaunchKernelEx(&cfg, fp8a8_pair_kernel<C>, tx, tw, p);
 }
 
+template <int BN>
+cudaError_t launch_product(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, int sms, int dev, cudaStream_t s) {
+    const bool ragged = (long)p.N * (p.y_bf16 ? 2 : 4) % 16 != 0;
+    if (p.y_bf16)
+        return ragged ? launch<PairCfg<BN, false, true, true>>(tx, tw, p, sms, dev, s)
+                      : launch<PairCfg<BN, false, true, false>>(tx, tw, p, sms, dev, s);
+    return ragged ? launch<PairCfg<BN, false, false, true>>(tx, tw, p, sms, dev, s)
+                  : launch<PairCfg<BN, false, false, false>>(tx, tw, p, sms, dev, s);
+}
+
 }  // namespace
 
 cudaError_t launch_fp8a8_pair(const CUtensorMap& tx, const CUtensorMap& tw, Fp8a8Params p, bool gated, int bn, int sms,
@@ -422,9 +435,9 @@ cudaError_t launch_fp8a8_pair(const CUtensorMap& tx, const CUtensorMap& tw, Fp8a
     p.m_tiles = (p.M + 255) / 256;
     p.n_tiles = (p.n_end - p.n_first + (gated ? 127 : bn - 1)) / (gated ? 128 : bn);
     if (gated) return launch<PairCfg<256, true>>(tx, tw, p, sms, dev, s);
-    if (bn == 256) return launch<PairCfg<256, false>>(tx, tw, p, sms, dev, s);
-    if (bn == 192) return launch<PairCfg<192, false>>(tx, tw, p, sms, dev, s);
-    return launch<PairCfg<128, false>>(tx, tw, p, sms, dev, s);
+    if (bn == 256) return launch_product<256>(tx, tw, p, sms, dev, s);
+    if (bn == 192) return launch_product<192>(tx, tw, p, sms, dev, s);
+    return launch_product<128>(tx, tw, p, sms, dev, s);
 }
 
 }  // namespace qmm
