@@ -156,7 +156,7 @@ __device__ __forceinline__ uint4 bf16x8(const uint64_t* v) {
 // consecutive lanes write consecutive chunks of a row.
 template <int NC>
 __device__ __forceinline__ int stage_swz(int r) {
-    return NC == 4 ? (r >> 1) & 3 : (r >> 2) & 1;
+    return NC == 8 ? r & 7 : NC == 4 ? (r >> 1) & 3 : (r >> 2) & 1;
 }
 template <int NC>
 __device__ __forceinline__ void flush_stage(const Fp8a8Params& p, const uint8_t* stg, int lane, long row0, int col, int esz) {
@@ -170,83 +170,79 @@ __device__ __forceinline__ void flush_stage(const Fp8a8Params& p, const uint8_t*
     }
 }
 
-// A lane's 16 consecutive outputs (two per element of `v`) to its row of the staging: as bf16 from
-// chunk c0 of NC on, or as four chunks of fp32.
+// A lane's 16 consecutive outputs (two per element of `v`) to its row of the staging, chunk c0 of
+// NC and on.
 template <bool BF16, int NC>
 __device__ __forceinline__ void stage16(uint8_t* stg, int lane, int c0, const uint64_t* v) {
-    if constexpr (BF16) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-            *reinterpret_cast<uint4*>(stg + (lane * NC + ((c0 + c) ^ stage_swz<NC>(lane))) * 16) = bf16x8(v + 4 * c);
-    } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const float2 a = unpack2(v[2 * c]), b = unpack2(v[2 * c + 1]);
-            *reinterpret_cast<float4*>(stg + (lane * 4 + (c ^ stage_swz<4>(lane))) * 16) = make_float4(a.x, a.y, b.x, b.y);
-        }
-    }
-}
-
-// A warp's staged 32 rows x 64 bytes to rows of Y whose pitch is no multiple of 16 bytes: 16
-// lanes to a row with 4 bytes each.  A row of bf16 that starts at an odd element (4-byte
-// stores are aligned) is shifted by one: its lane 0 writes the first element and the last.
-template <bool BF16>
-__device__ __forceinline__ void flush_ragged(const Fp8a8Params& p, const uint8_t* stg, int lane, long row0, int col) {
-    const int half = lane / 16, w = lane % 16, rows = p.M - (int)row0, cols = p.N - col;
-    auto word = [&](int r, int i) { return reinterpret_cast<const uint32_t*>(stg + (r * 4 + ((i / 4) ^ stage_swz<4>(r))) * 16)[i % 4]; };
-    if constexpr (!BF16) {
-        if (w >= cols) return;
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
-            const int r = 2 * i + half;
-            if (r < rows) static_cast<uint32_t*>(p.Y)[(row0 + r) * p.N + col + w] = word(r, w);
-        }
-        return;
-    }
-#pragma unroll 1
-    for (int i = 0; i < 16; ++i) {
-        const int r = 2 * i + half;
-        if (r >= rows) break;
-        const int odd = ((int)row0 + r) & p.N & 1, e = 2 * w - odd;   // the word's elements: e, e + 1 (or 31, 0)
-        uint32_t d = word(r, w);
-        if (odd) d = (d << 16) | (word(r, (w + 15) & 15) >> 16);
-        uint16_t* dst = static_cast<uint16_t*>(p.Y) + (row0 + r) * p.N + col + e;
-        if (e >= 0 && e + 1 < cols) {
-            *reinterpret_cast<uint32_t*>(dst) = d;
+    for (int c = 0; c < (BF16 ? 2 : 4); ++c) {
+        uint4 d;
+        if constexpr (BF16) {
+            d = bf16x8(v + 4 * c);
         } else {
-            if (e >= 0 && e < cols) dst[0] = (uint16_t)d;
-            if (e < 0 && 31 < cols) dst[32] = (uint16_t)d;
-            if (e < 0 && 0 < cols) dst[1] = (uint16_t)(d >> 16);
+            const float2 a = unpack2(v[2 * c]), b = unpack2(v[2 * c + 1]);
+            d = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+        }
+        *reinterpret_cast<uint4*>(stg + (lane * NC + ((c0 + c) ^ stage_swz<NC>(lane))) * 16) = d;
+    }
+}
+
+// A warp's staged 32 rows x 128 bytes (chunk c of row r at c ^ (r % 8)) to rows of Y whose pitch is
+// no multiple of 16 bytes: a row at a time, 4 bytes a lane.  A row of bf16 that starts at an
+// odd element (4-byte stores are aligned) is shifted by one; the first and the last
+// element of such rows follow, a row per lane.
+template <bool BF16, int UNROLL>
+__device__ __forceinline__ void flush_ragged(const Fp8a8Params& p, const uint8_t* stg, int lane, long row0, int col) {
+    const int rows = p.M - (int)row0 < 32 ? p.M - (int)row0 : 32, cols = p.N - col;
+    auto word = [&](int r, int i) { return reinterpret_cast<const uint32_t*>(stg + (r * 8 + ((i / 4) ^ (r & 7))) * 16)[i % 4]; };
+    if constexpr (!BF16) {
+        if (lane >= cols) return;
+        uint32_t* dst = static_cast<uint32_t*>(p.Y) + row0 * p.N + col + lane;
+#pragma unroll UNROLL
+        for (int r = 0; r < rows; ++r) dst[(long)r * p.N] = word(r, lane);
+    } else {
+        uint16_t* dst = static_cast<uint16_t*>(p.Y) + row0 * p.N + col;
+#pragma unroll UNROLL
+        for (int r = 0; r < rows; ++r) {
+            const int odd = ((int)row0 + r) & p.N & 1, e = 2 * lane - odd;   // the lane's elements: e, e + 1
+            uint32_t d = word(r, lane);
+            if (odd) d = (d << 16) | (word(r, (lane + 31) & 31) >> 16);
+            uint16_t* at = dst + (long)r * p.N + e;
+            if (e >= 0 && e + 1 < cols) *reinterpret_cast<uint32_t*>(at) = d;
+            else if (e >= 0 && e < cols) at[0] = (uint16_t)d;
+        }
+        if (lane < rows && (((int)row0 + lane) & p.N & 1)) {
+            if (cols > 0) dst[(long)lane * p.N] = (uint16_t)word(lane, 0);
+            if (cols > 63) dst[(long)lane * p.N + 63] = (uint16_t)(word(lane, 31) >> 16);
         }
     }
 }
 
-// A warp's 32 rows x W columns (lane = row, `v` its W consecutive outputs, two per element) to Y at
-// (row0, col), through the warp's 2 KB of staging, so that a store instruction writes whole
-// runs of a few rows rather than 16 bytes, or one element, of 32 rows (5268 x 1024 x 5119
-// element by element: 262 us; this way 64).  In ragged rows not unrolled: the kernel
-// spills otherwise (2048 x 5120 x 9727: 136 us against 100).
-template <int W, bool BF16, bool RAGGED>
+// A warp's 32 rows x 64 columns (lane = row, `v` its 64 consecutive outputs, two per element) to Y
+// at (row0, col), through the warp's staging (2 KB, RAGGED 4 KB), so that a store instruction
+// writes whole runs of a few rows rather than 16 bytes, or one element, of 32 rows
+// (5268 x 1024 x 5119 element by element: 262 us; this way 50,
+// with N = 5120 41).  Ragged rows are copied out UNROLL at a time (what the kernel's registers allow).
+template <bool BF16, bool RAGGED, int UNROLL>
 __device__ __forceinline__ void store_columns(const Fp8a8Params& p, uint8_t* stg, int lane, long row0, int col,
                                               const uint64_t* v) {
     if constexpr (!RAGGED) {
 #pragma unroll
-        for (int c = 0; c < W; c += 16) {
+        for (int c = 0; c < 64; c += 16) {
             __syncwarp();
-            stage16<BF16, 2>(stg, lane, 0, v + c / 2);
+            stage16<BF16, BF16 ? 2 : 4>(stg, lane, 0, v + c / 2);
             __syncwarp();
             flush_stage<BF16 ? 2 : 4>(p, stg, lane, row0, col + c, BF16 ? 2 : 4);
         }
     } else {
-        constexpr int STEP = BF16 ? 32 : 16;
-#pragma unroll 1
-        for (int c = 0; c < W; c += STEP) {
+        constexpr int STEP = BF16 ? 64 : 32;
+#pragma unroll
+        for (int c = 0; c < 64; c += STEP) {
             __syncwarp();
 #pragma unroll
-            for (int k = 0; k < W; k += 16)
-                if (k / STEP * STEP == c) stage16<BF16, 4>(stg, lane, k / 8 & 2, v + k / 2);
+            for (int k = 0; k < STEP; k += 16) stage16<BF16, 8>(stg, lane, k * 8 / STEP, v + (c + k) / 2);
             __syncwarp();
-            flush_ragged<BF16>(p, stg, lane, row0, col + c);
+            flush_ragged<BF16, UNROLL>(p, stg, lane, row0, col + c);
         }
     }
 }

@@ -40,7 +40,10 @@ struct PairCfg {
     static constexpr int BN = BN_;
     static constexpr bool GATED = GATED_, RAGGED = RAGGED_, BF16 = BF16_;
     static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / 2 * 128, STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES = 163840 / STAGE_BYTES;           // 160 KB of operands
+    // A fold warp's staging for its outputs.  Ragged rows are written in runs of 128 bytes: in runs
+    // of 64 more sectors are written in part (5268 x 1024 x 5119: 64 us against 50).
+    static constexpr int STAGING = RAGGED ? 4096 : 2048;
+    static constexpr int STAGES = (RAGGED && BN == 256 ? 131072 : 163840) / STAGE_BYTES;   // 160 KB of operands (128)
     static constexpr int NBUF = BN <= 128 ? 4 : 2, BUF_COLS = 512 / NBUF;
     static constexpr int SC_SLOTS = 4, SC_KB = 4;                 // ring of scales: slots of 4 K blocks
     static constexpr int SC_PITCH = 128 + 4;                      // per K block: the rows' scales, the two blocks'
@@ -52,7 +55,7 @@ struct PairCfg {
     // with loads of 8 at 5268 x 17408 x 5120), gate/up of 8 (289 us against 330 with 16 at
     // 2048 x 5120 x 2 x 17408).
     static constexpr int CW = 64, GROUPS = BN / CW, FOLD_WARPS = 4 * GROUPS, LW = GATED ? 8 : BN == 256 ? 16 : BN == 192 ? 32 : 64;
-    static constexpr int OUT_BYTES = GATED ? 2 * GROUPS * 128 * 4 : FOLD_WARPS * 2048;   // row maxima, or output staging
+    static constexpr int OUT_BYTES = GATED ? 2 * GROUPS * 128 * 4 : FOLD_WARPS * STAGING;   // row maxima, or output staging
     static constexpr bool REG_SPLIT = BN == 256;
     static constexpr int THREADS = 128 + 32 * FOLD_WARPS, REGS = 65536 / THREADS / 8 * 8, REGS_FOLD = 104, REGS_OTHER = 64;
     static_assert(!REG_SPLIT || REGS_FOLD * 32 * FOLD_WARPS + REGS_OTHER * 128 == REGS * THREADS, "register shares = launch registers");
@@ -87,7 +90,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
     fp8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, Fp8a8Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stage = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* outs = stage + C::STAGES * C::STAGE_BYTES;         // output staging, 2 KB per fold warp
+    uint8_t* outs = stage + C::STAGES * C::STAGE_BYTES;         // output staging of the fold warps
     float* rowmax = reinterpret_cast<float*>(outs);              // gated: [tile parity][quarter][128]
     float* sc = reinterpret_cast<float*>(outs + C::OUT_BYTES);   // [slot][kb][128 rows, 2 weight blocks]
     uint64_t* bars = reinterpret_cast<uint64_t*>(sc + C::SC_FLOATS);
@@ -205,8 +208,8 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
             asm volatile("" : "+r"(te));
             const PairTile ti = pair_tile<C>(p, te, crank);
             if constexpr (!C::GATED) {
-                uint8_t* stg = outs + (warp - 4) * 2048;
-                store_columns<C::CW, C::BF16, C::RAGGED>(p, stg, lane, (long)ti.m0 + q * 32, ti.n0 + fold_col<C>(cq, 0), acc);
+                uint8_t* stg = outs + (warp - 4) * C::STAGING;
+                store_columns<C::BF16, C::RAGGED, C::BN == 256 ? 4 : 8>(p, stg, lane, (long)ti.m0 + q * 32, ti.n0 + fold_col<C>(cq, 0), acc);
             } else {
                 // the first half of acc: gate columns; the second half: the same columns of up
                 constexpr int HP = C::CW / 4;   // pairs

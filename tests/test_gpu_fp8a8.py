@@ -134,6 +134,21 @@ def test_columns_past_the_last_whole_wave(q, dt):
         check_swiglu(Hq, Hs, y, tol)
 
 
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("M,K,N", [(257, 128, 1), (257, 256, 4097), (600, 128, 66), (700, 128, 777), (1000, 384, 2047),
+                                   (1000, 384, 2049), (1000, 384, 2050), (2047, 144, 5117), (4000, 128, 3331)])
+def test_rows_of_any_pitch(q, M, K, N, dt):
+    """Row pitches that are no multiple of 16 bytes, down to a single element, in tiles of many tokens."""
+    ops = operands(M + N, M, K, N)
+    y, tol = formula(*ops)
+    big = torch.full((M + 2, N), 7.0, dtype=dt, device="cuda")
+    q.qmm_fp8a8_blk128(*ops, out_dtype=dt, Y=big[:M])
+    q.qmm_check_status()
+    if dt == BF16:
+        tol = tol + half_bf16_step(np.abs(y) + tol)
+    assert np.all(np.abs(big[:M].double().cpu().numpy() - y) <= tol) and bool((big[M:] == 7).all())
+
+
 @pytest.mark.parametrize("M,N", [(1, 128), (24, 200), (130, 512), (600, 384)])
 def test_integers_are_exact(q, M, N):
     """Small integer codes and power-of-two scales: every partial sum is exact."""
