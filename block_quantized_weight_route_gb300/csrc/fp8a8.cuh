@@ -151,28 +151,21 @@ __device__ __forceinline__ uint4 bf16x8(const uint64_t* v) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A warp's staged 32 rows x NC 16-byte chunks (chunk c of row r at c ^ stage_swz<NC>(r),
-// which leaves bank conflicts of two ways at most on both sides) to Y at (row0, col):
-// consecutive lanes write consecutive chunks of a row.
-template <int NC>
-__device__ __forceinline__ int stage_swz(int r) {
-    return NC == 8 ? r & 7 : NC == 4 ? (r >> 1) & 3 : (r >> 2) & 1;
-}
-template <int NC>
-__device__ __forceinline__ void flush_stage(const Fp8a8Params& p, const uint8_t* stg, int lane, long row0, int col, int esz) {
+// A warp's staging for outputs: 32 rows x 128 bytes, 16-byte chunk c of row r at c ^ (r % 8) (no bank
+// conflicts on either side).  Copied to Y at (row0, col): eight lanes to a row.
+__device__ __forceinline__ void flush_aligned(const Fp8a8Params& p, const uint8_t* stg, int lane, long row0, int col, int esz) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const int r = (i * 32 + lane) / NC, c = (i * 32 + lane) % NC;
-        const uint4 d = *reinterpret_cast<const uint4*>(stg + (r * NC + (c ^ stage_swz<NC>(r))) * 16);
+    for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + lane / 8, c = lane % 8;
+        const uint4 d = *reinterpret_cast<const uint4*>(stg + (r * 8 + (c ^ (r & 7))) * 16);
         const int cc = col + c * (16 / esz);
         if (row0 + r < p.M && cc < p.N)
             *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.Y) + ((row0 + r) * p.N + cc) * esz) = d;
     }
 }
 
-// A lane's 16 consecutive outputs (two per element of `v`) to its row of the staging, chunk c0 of
-// NC and on.
-template <bool BF16, int NC>
+// A lane's 16 consecutive outputs (two per element of `v`) to its row of the staging, chunk c0 and on.
+template <bool BF16>
 __device__ __forceinline__ void stage16(uint8_t* stg, int lane, int c0, const uint64_t* v) {
 #pragma unroll
     for (int c = 0; c < (BF16 ? 2 : 4); ++c) {
@@ -183,12 +176,12 @@ __device__ __forceinline__ void stage16(uint8_t* stg, int lane, int c0, const ui
             const float2 a = unpack2(v[2 * c]), b = unpack2(v[2 * c + 1]);
             d = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
         }
-        *reinterpret_cast<uint4*>(stg + (lane * NC + ((c0 + c) ^ stage_swz<NC>(lane))) * 16) = d;
+        *reinterpret_cast<uint4*>(stg + (lane * 8 + ((c0 + c) ^ (lane & 7))) * 16) = d;
     }
 }
 
-// A warp's staged 32 rows x 128 bytes (chunk c of row r at c ^ (r % 8)) to rows of Y whose pitch is
-// no multiple of 16 bytes: a row at a time, 4 bytes a lane.  A row of bf16 that starts at an
+// The same to rows of Y whose pitch is no multiple of 16 bytes: a row at a time, 4 bytes a lane.
+// A row of bf16 that starts at an
 // odd element (4-byte stores are aligned) is shifted by one; the first and the last
 // element of such rows follow, a row per lane.
 template <bool BF16, int UNROLL>
@@ -219,31 +212,23 @@ __device__ __forceinline__ void flush_ragged(const Fp8a8Params& p, const uint8_t
 }
 
 // A warp's 32 rows x 64 columns (lane = row, `v` its 64 consecutive outputs, two per element) to Y
-// at (row0, col), through the warp's staging (2 KB, RAGGED 4 KB), so that a store instruction
-// writes whole runs of a few rows rather than 16 bytes, or one element, of 32 rows
-// (5268 x 1024 x 5119 element by element: 262 us; this way 50,
-// with N = 5120 41).  Ragged rows are copied out UNROLL at a time (what the kernel's registers allow).
+// at (row0, col), through the warp's staging, so that a store instruction writes runs of 128
+// bytes.  Runs of 32 (with 2 KB of staging) took 46 us instead of 35 at 5268 x 1024 x 5120,
+// single elements in ragged rows 262 instead of 50 at 5268 x 1024 x 5119 (there a run's two
+// ends are sectors written in part).  Ragged rows are copied UNROLL at a time, what the
+// kernel's registers allow.
 template <bool BF16, bool RAGGED, int UNROLL>
 __device__ __forceinline__ void store_columns(const Fp8a8Params& p, uint8_t* stg, int lane, long row0, int col,
                                               const uint64_t* v) {
-    if constexpr (!RAGGED) {
+    constexpr int STEP = BF16 ? 64 : 32;
 #pragma unroll
-        for (int c = 0; c < 64; c += 16) {
-            __syncwarp();
-            stage16<BF16, BF16 ? 2 : 4>(stg, lane, 0, v + c / 2);
-            __syncwarp();
-            flush_stage<BF16 ? 2 : 4>(p, stg, lane, row0, col + c, BF16 ? 2 : 4);
-        }
-    } else {
-        constexpr int STEP = BF16 ? 64 : 32;
+    for (int c = 0; c < 64; c += STEP) {
+        __syncwarp();
 #pragma unroll
-        for (int c = 0; c < 64; c += STEP) {
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < STEP; k += 16) stage16<BF16, 8>(stg, lane, k * 8 / STEP, v + (c + k) / 2);
-            __syncwarp();
-            flush_ragged<BF16, UNROLL>(p, stg, lane, row0, col + c);
-        }
+        for (int k = 0; k < STEP; k += 16) stage16<BF16>(stg, lane, k * 8 / STEP, v + (c + k) / 2);
+        __syncwarp();
+        if constexpr (RAGGED) flush_ragged<BF16, UNROLL>(p, stg, lane, row0, col + c);
+        else flush_aligned(p, stg, lane, row0, col + c, BF16 ? 2 : 4);
     }
 }
 

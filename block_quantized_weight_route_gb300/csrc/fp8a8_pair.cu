@@ -40,10 +40,9 @@ struct PairCfg {
     static constexpr int BN = BN_;
     static constexpr bool GATED = GATED_, RAGGED = RAGGED_, BF16 = BF16_;
     static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / 2 * 128, STAGE_BYTES = A_BYTES + B_BYTES;
-    // A fold warp's staging for its outputs.  Ragged rows are written in runs of 128 bytes: in runs
-    // of 64 more sectors are written in part (5268 x 1024 x 5119: 64 us against 50).
-    static constexpr int STAGING = RAGGED ? 4096 : 2048;
-    static constexpr int STAGES = (RAGGED && BN == 256 ? 131072 : 163840) / STAGE_BYTES;   // 160 KB of operands (128)
+    static constexpr int STAGING = 4096;   // of a fold warp, for its outputs
+    // 160 KB of operands (256 columns to a product: 128 KB beside the 64 KB of staging, as fast)
+    static constexpr int STAGES = (!GATED && BN == 256 ? 131072 : 163840) / STAGE_BYTES;
     static constexpr int NBUF = BN <= 128 ? 4 : 2, BUF_COLS = 512 / NBUF;
     static constexpr int SC_SLOTS = 4, SC_KB = 4;                 // ring of scales: slots of 4 K blocks
     static constexpr int SC_PITCH = 128 + 4;                      // per K block: the rows' scales, the two blocks'
