@@ -19,15 +19,17 @@
 // buffer's MMA (512 cycles at BN = 256), so the length of the fold's path counts, not its
 // throughput.  BN = 128 has four buffers and is bound by shared memory (48 KB written and
 // read a K block, 470 cycles).  Per K block: 0.42 us at BN = 256, 0.375 at 192, 0.245 at 128.
-// Measured: 2048 x 5120 x 5120 53.8 us (2.0 PFLOP/s; the last 256 columns in the narrow
-// kernel), 5268 x 17408 x 5120 367 us (2.56 PFLOP/s, 400 us in a row of calls that
-// meets the power limit), gate/up 2048 x 5120 x 2 x 17408 289 us (2.53 PFLOP/s, 310 in a row);
-// the tensor pipe is busy for 52% of the cycles there, the issue slots for 63%.
+// Measured: 2048 x 5120 x 5120 50.1 us (2.14 PFLOP/s; the last 256 columns in the narrow
+// kernel), 5268 x 17408 x 5120 362 us (2.59 PFLOP/s; 403 us in a row of calls that meets the
+// power limit), gate/up 2048 x 5120 x 2 x 17408 286 us (2.56 PFLOP/s; 308 in a row); the
+// tensor pipe is busy for 56% of the cycles, the issue slots for 62%: 131 instructions a K
+// block and fold warp, 32 of them the packed FMAs.  A spill in the K loop costs 20 to 40%.
 // Not kept: three buffers of 160 columns with 20 fold warps, halves of the tile with MMAs
 // and warps of their own, two MMA issuers, a producer warp per operand (all within 5%),
-// polling instead of sleeping waits (5% slower), 8 fold warps of 128 columns at BN = 256 (as
-// fast for the product, 9% slower for gate/up).  At 2.4 PFLOP/s the power limit is near:
-// without any fold the same loop reaches 3.0 PFLOP/s at clocks down to 1.6 GHz.
+// polling instead of sleeping waits (5% slower), sleeping without a look first (10%), 8 fold
+// warps of 128 columns at BN = 256 (as fast for the product, 9% slower for gate/up), a fold
+// loop of one or two K blocks (8 to 25%), unpacked FMAs (12%).  At 2.5 PFLOP/s the power
+// limit is near: without any fold the same loop reaches 3.0 PFLOP/s at clocks down to 1.6 GHz.
 #include "fp8a8.cuh"
 
 namespace qmm {
