@@ -10,7 +10,7 @@
 // P_kb out of TMEM into fp32 running sums in registers, two or four TMEM buffers
 // apart from the MMA.
 //   warp 0: TMA producer   warp 1: MMA issuer (even CTA)
-//   warps 2, 3: the scales of four K blocks at a time, by asynchronous copies into a ring
+//   warps 2, 3: the scales of four or eight K blocks at a time, by asynchronous copies into a ring
 //   warps 4..: fold, four warps for each 64 columns (16, 12 or 8 in all); warp w reads
 //              TMEM lanes 32 (w % 4) .. +31 (a row per lane), columns 64 ((w - 4) / 4) .. +63
 // What bounds it: a TMEM buffer's way from the MMA's end through the fold and back to
@@ -19,17 +19,18 @@
 // buffer's MMA (512 cycles at BN = 256), so the length of the fold's path counts, not its
 // throughput.  BN = 128 has four buffers and is bound by shared memory (48 KB written and
 // read a K block, 470 cycles).  Per K block: 0.42 us at BN = 256, 0.375 at 192, 0.245 at 128.
-// Measured: 2048 x 5120 x 5120 50.1 us (2.14 PFLOP/s; the last 256 columns in the narrow
-// kernel), 5268 x 17408 x 5120 362 us (2.59 PFLOP/s; 403 us in a row of calls that meets the
-// power limit), gate/up 2048 x 5120 x 2 x 17408 286 us (2.56 PFLOP/s; 308 in a row); the
-// tensor pipe is busy for 56% of the cycles, the issue slots for 62%: 131 instructions a K
-// block and fold warp, 32 of them the packed FMAs.  A spill in the K loop costs 20 to 40%.
+// Measured: 2048 x 5120 x 5120 48.5 us (2.21 PFLOP/s; the last 256 columns in the narrow
+// kernel), 5268 x 17408 x 5120 348 us (2.70 PFLOP/s; 399 us in a row of calls that meets the
+// power limit), gate/up 2048 x 5120 x 2 x 17408 286 us (2.56 PFLOP/s; 309 in a row).
+// Next to that way the fold's instructions count: 112 a K block and fold warp (gate/up 137),
+// 32 of them the packed FMAs; a spill in the K loop costs 20 to 40%.
 // Not kept: three buffers of 160 columns with 20 fold warps, halves of the tile with MMAs
 // and warps of their own, two MMA issuers, a producer warp per operand (all within 5%),
 // polling instead of sleeping waits (5% slower), sleeping without a look first (10%), 8 fold
 // warps of 128 columns at BN = 256 (as fast for the product, 9% slower for gate/up), a fold
-// loop of one or two K blocks (8 to 25%), unpacked FMAs (12%).  At 2.5 PFLOP/s the power
-// limit is near: without any fold the same loop reaches 3.0 PFLOP/s at clocks down to 1.6 GHz.
+// loop of one or two K blocks (8 to 25%), unpacked FMAs (12%), gate/up with gate and up columns
+// in different warps that exchange halves at the end (18%).  At 2.7 PFLOP/s the power limit
+// is near: without any fold the same loop reaches 3.0 PFLOP/s at clocks down to 1.6 GHz.
 #include "fp8a8.cuh"
 
 namespace qmm {
@@ -46,16 +47,18 @@ struct PairCfg {
     // 160 KB of operands (256 columns to a product: 128 KB beside the 64 KB of staging, as fast)
     static constexpr int STAGES = (!GATED && BN == 256 ? 131072 : 163840) / STAGE_BYTES;
     static constexpr int NBUF = BN <= 128 ? 4 : 2, BUF_COLS = 512 / NBUF;
-    static constexpr int SC_SLOTS = 4, SC_KB = 4;                 // ring of scales: slots of 4 K blocks
+    // Ring of scales: slots of SC_KB K blocks, which is also how many the fold loop unrolls: the
+    // loop's end moves sums between registers (131 instructions a K block unrolled by four,
+    // 112 by eight; 362 and 348 us at 5268 x 17408 x 5120).  Gate/up unrolled by eight spills.
+    static constexpr int SC_KB = GATED ? 4 : 8, SC_SLOTS = 16 / SC_KB;
     static constexpr int SC_PITCH = 128 + 4;                      // per K block: the rows' scales, the two blocks'
     static constexpr int SC_FLOATS = SC_SLOTS * SC_KB * SC_PITCH;
     // Fold threads: a row and CW columns, LW of them a TMEM load.  Few large loads are best
     // where the registers hold them (8 fold warps: all 64 columns at once, 37 us against 45
     // with loads of 32 at 256 x 17408 x 5120; 12 warps: 32); 16 warps need more than an even
-    // share of the registers for their sums (a register split) and loads of 16 (367 us against 374
-    // with loads of 8 at 5268 x 17408 x 5120), gate/up of 8 (289 us against 330 with 16 at
-    // 2048 x 5120 x 2 x 17408).
-    static constexpr int CW = 64, GROUPS = BN / CW, FOLD_WARPS = 4 * GROUPS, LW = GATED ? 8 : BN == 256 ? 16 : BN == 192 ? 32 : 64;
+    // share of the registers for their sums (a register split) and loads of 8 (gate/up with
+    // loads of 16: 330 us against 287 at 2048 x 5120 x 2 x 17408).
+    static constexpr int CW = 64, GROUPS = BN / CW, FOLD_WARPS = 4 * GROUPS, LW = BN == 256 ? 8 : BN == 192 ? 32 : 64;
     static constexpr int OUT_BYTES = GATED ? 2 * GROUPS * 128 * 4 : FOLD_WARPS * STAGING;   // row maxima, or output staging
     static constexpr bool REG_SPLIT = BN == 256;
     static constexpr int THREADS = 128 + 32 * FOLD_WARPS, REGS = 65536 / THREADS / 8 * 8, REGS_FOLD = 104, REGS_OTHER = 64;
@@ -156,10 +159,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
 #pragma unroll
             for (int j = 0; j < C::CW / 2; ++j) acc[j] = 0;
             for (int kb0 = 0; kb0 < kbs && ok; kb0 += C::SC_KB) {
-                if (!mbar_wait(&sc_full[slot], sph, abort_flag, p.err, DEV_TIMEOUT_CONV)) {
-                    ok = false;
-                    break;
-                }
+                ok &= mbar_wait(&sc_full[slot], sph, abort_flag, p.err, DEV_TIMEOUT_CONV);
                 const float* scr = sc + slot * C::SC_KB * C::SC_PITCH;
 #pragma unroll
                 for (int k = 0; k < C::SC_KB; ++k) {
@@ -167,10 +167,8 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
                     const float sx = scr[k * C::SC_PITCH + row];
                     const float s0 = sx * scr[k * C::SC_PITCH + 128 + blk];
                     const float s1 = C::GATED ? sx * scr[k * C::SC_PITCH + 129] : s0;
-                    if (!mbar_wait(&done[st], ph, abort_flag, p.err, DEV_TIMEOUT_ACC)) {
-                        ok = false;
-                        break;
-                    }
+                    // (after a time-out the sums mean nothing; the loop ends with this group)
+                    ok &= mbar_wait(&done[st], ph, abort_flag, p.err, DEV_TIMEOUT_ACC);
                     tc_fence_after();
                     const int buf = k & (C::NBUF - 1);
                     const uint32_t a0 = lane_addr + (uint32_t)(buf * C::BUF_COLS);
