@@ -855,6 +855,9 @@ qmm_status qmm_dbg_wait_timeout(unsigned timeout_us, cudaStream_t stream) {
 
 // ---------------------------------------------------------------- norm with an 8-bit output
 
+// Most rows, columns or K: tile counts and tile ends stay within 32 bits.
+constexpr int kMostRows = 0x7FFFFFFF - 511;
+
 static bool is_dtype(qmm_dtype t) { return t == QMM_F32 || t == QMM_BF16; }
 
 static qmm_status add_rmsnorm(const char* who, bool q81, const void* X, qmm_dtype xdt, int64_t ldx, const void* R,
@@ -862,8 +865,8 @@ static qmm_status add_rmsnorm(const char* who, bool q81, const void* X, qmm_dtyp
                               float eps, int T, int D, void* Q, float* S, uint16_t* Yd, uint16_t* Ys, uint16_t* Y,
                               cudaStream_t stream) {
     const int unit = q81 ? 32 : 16;
-    if (T < 0 || D < unit || D % unit || D > rmsnorm8_max_width())
-        return fail(QMM_ERR_UNSUPPORTED_SHAPE, "%s: need T >= 0, D %% %d == 0, D <= %d (T=%d D=%d)", who, unit,
+    if (T < 0 || T > kMostRows || D < unit || D % unit || D > rmsnorm8_max_width())
+        return fail(QMM_ERR_UNSUPPORTED_SHAPE, "%s: need 0 <= T <= 2^31 - 512, D %% %d == 0, D <= %d (T=%d D=%d)", who, unit,
                     rmsnorm8_max_width(), T, D);
     if (!is_dtype(xdt) || !is_dtype(gdt) || (R && !is_dtype(rdt))) return fail(QMM_ERR_INVALID_ARG, "%s: bad type", who);
     if (!(eps >= 0.0f)) return fail(QMM_ERR_INVALID_ARG, "%s: eps must not be negative", who);
@@ -943,9 +946,9 @@ static qmm_status run_fp8a8(const char* who, DeviceState* d, Fp8a8Params& p, boo
 
 qmm_status qmm_fp8a8_blk128(const uint8_t* Xq, const float* Xs, int M, int K, int N, const uint8_t* W, const float* S,
                             void* Y, qmm_dtype ydt, cudaStream_t stream) {
-    if (M < 0 || K < 16 || K % 16 || N < 1)
-        return fail(QMM_ERR_UNSUPPORTED_SHAPE, "qmm_fp8a8_blk128: need M >= 0, K %% 16 == 0, N >= 1 (M=%d K=%d N=%d)", M,
-                    K, N);
+    if (M < 0 || K < 16 || K % 16 || N < 1 || M > kMostRows || K > kMostRows || N > kMostRows)
+        return fail(QMM_ERR_UNSUPPORTED_SHAPE,
+                    "qmm_fp8a8_blk128: need M >= 0, K %% 16 == 0, N >= 1, each <= 2^31 - 512 (M=%d K=%d N=%d)", M, K, N);
     if (!is_dtype(ydt)) return fail(QMM_ERR_INVALID_ARG, "qmm_fp8a8_blk128: bad output type");
     if (!W || !S || (M > 0 && (!Xq || !Xs || !Y))) return fail(QMM_ERR_INVALID_ARG, "qmm_fp8a8_blk128: null pointer");
     if (!aligned16(Xq) || !aligned16(Xs) || !aligned16(W) || !aligned16(S) || !aligned16(Y))
@@ -968,9 +971,10 @@ qmm_status qmm_fp8a8_blk128(const uint8_t* Xq, const float* Xs, int M, int K, in
 
 qmm_status qmm_fp8a8_swiglu_blk128(const uint8_t* Xq, const float* Xs, int M, int K, int F, const uint8_t* Wgu,
                                    const float* Sgu, uint8_t* Hq, float* Hs, cudaStream_t stream) {
-    if (M < 0 || K < 16 || K % 16 || F < 128 || F % 128)
+    if (M < 0 || K < 16 || K % 16 || F < 128 || F % 128 || M > kMostRows || K > kMostRows || F > kMostRows / 2)
         return fail(QMM_ERR_UNSUPPORTED_SHAPE,
-                    "qmm_fp8a8_swiglu_blk128: need M >= 0, K %% 16 == 0, F %% 128 == 0 (M=%d K=%d F=%d)", M, K, F);
+                    "qmm_fp8a8_swiglu_blk128: need M >= 0, K %% 16 == 0, F %% 128 == 0, M, K and 2F <= 2^31 - 512 "
+                    "(M=%d K=%d F=%d)", M, K, F);
     if (!Wgu || !Sgu || (M > 0 && (!Xq || !Xs || !Hq || !Hs)))
         return fail(QMM_ERR_INVALID_ARG, "qmm_fp8a8_swiglu_blk128: null pointer");
     if (!aligned16(Xq) || !aligned16(Xs) || !aligned16(Wgu) || !aligned16(Sgu) || !aligned16(Hq) || !aligned16(Hs))

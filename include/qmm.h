@@ -146,8 +146,8 @@ qmm_status qmm_q8_0_q8_1(const int8_t *Xq, const uint16_t *Xd, int M, int K, int
  *   X [T] rows of ldx elements, R / Rout (both NULL: no residual) of ldr / ldro,
  *   G [D]; each fp32 or bf16 (rdt is the type of R and Rout).  Rout may be R (or
  *   X, where type and pitch are equal): the sum in place.  fp32 arithmetic.
- * Shapes: T >= 0, D % 16 == 0 (_q8_1: D % 32 == 0), D <= 16384; pitches at least D
- * and multiples of 8.
+ * Shapes: 0 <= T <= 2^31 - 512, D % 16 == 0 (_q8_1: D % 32 == 0), D <= 16384; pitches
+ * at least D and multiples of 8.
  */
 qmm_status qmm_add_rmsnorm_fp8(const void *X, qmm_dtype xdt, int64_t ldx, const void *R, int64_t ldr, void *Rout,
                                int64_t ldro, qmm_dtype rdt, const void *G, qmm_dtype gdt, float eps, int T, int D,
@@ -165,7 +165,7 @@ qmm_status qmm_add_rmsnorm_q8_1(const void *X, qmm_dtype xdt, int64_t ldx, const
  *   qmm_fp8_blk128; the last block of either dimension may be partly filled);
  *   Y [M][N] fp32 (QMM_F32) or bf16 rounded to nearest even (QMM_BF16).
  * Products exact, block sums and their scaled sum in fp32.
- * Shapes: M >= 0, K % 16 == 0, N >= 1.
+ * Shapes: M >= 0, K % 16 == 0, N >= 1, none above 2^31 - 512.
  *
  * qmm_fp8a8_swiglu_blk128 -- the first half of a gated feed-forward: gate and up
  * products, SwiGLU and the rounding of H to FP8 in one kernel:
@@ -174,7 +174,7 @@ qmm_status qmm_add_rmsnorm_q8_1(const void *X, qmm_dtype xdt, int64_t ldx, const
  *   Wgu [2F][K] E4M3 (gate rows first), Sgu [2F/128][ceil(K/128)] fp32;
  *   Hq [M][F] E4M3 bytes, Hs [M][F/128] fp32: the activation operand of the down
  *   product (qmm_fp8a8_blk128 with K = F).
- * Shapes: M >= 0, K % 16 == 0, F % 128 == 0.
+ * Shapes: M >= 0, K % 16 == 0, F % 128 == 0; M, K and 2F at most 2^31 - 512.
  */
 qmm_status qmm_fp8a8_blk128(const uint8_t *Xq, const float *Xs, int M, int K, int N, const uint8_t *W, const float *S,
                             void *Y, qmm_dtype ydt, cudaStream_t stream);

@@ -73,3 +73,13 @@ def test_products(L):
         args[i] = P(264)
         assert g(*args) == INVALID
     assert b"qmm_fp8a8_swiglu_blk128" in L.qmm_last_error()
+
+
+def test_sizes_whose_tiles_pass_32_bits(L):
+    top = 2 ** 31 - 511
+    assert L.qmm_add_rmsnorm_fp8(*norm_args(T=top), A, A, None, None) == SHAPE
+    assert L.qmm_fp8a8_blk128(A, A, top, 256, 256, A, A, A, 1, None) == SHAPE
+    assert L.qmm_fp8a8_blk128(A, A, 1, 2 ** 31 - 16, 1, A, A, A, 1, None) == SHAPE
+    assert L.qmm_fp8a8_blk128(A, A, 1, 16, top, A, A, A, 1, None) == SHAPE
+    assert L.qmm_fp8a8_swiglu_blk128(A, A, top, 256, 256, A, A, A, A, None) == SHAPE
+    assert L.qmm_fp8a8_swiglu_blk128(A, A, 1, 16, 2 ** 30, A, A, A, A, None) == SHAPE
