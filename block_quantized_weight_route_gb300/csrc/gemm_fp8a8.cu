@@ -27,7 +27,7 @@ double pair_time(long tiles, long pairs, int i, int kbs) {
 //   narrow kernel, 128 weight rows x tn tokens, K over cs CTAs
 //   pair kernel, 256 tokens x bn columns, one pair per two SMs
 // Measured at 5120 x 5120: 128 tokens narrow 128/3 10.5 us, pair 13.9; 300 tokens narrow
-// 128/1 16.8, pair (192 columns) 20.9; 600 tokens 31 and 24; 1 token narrow 16/6 6.7,
+// 128/1 16.8, pair (192 columns) 18.7; 600 tokens 32.9 and 21.5; 1 token narrow 16/6 6.5,
 // 16/3 7.5, 16/7 (more CTAs than fit at once) 11.3; at 2000 x 1000, 128 tokens 32/4 6.4, 128/8 8.5.
 Fp8a8Plan one_launch(int M, int kbs, int cols, bool gated, int sms, int dev, double* time) {
     Fp8a8Plan best{};
