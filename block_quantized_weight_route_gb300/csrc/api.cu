@@ -244,10 +244,10 @@ qmm_status qmm_w4a16_ws(const uint16_t* X, int M, int K, int N, const uint8_t* W
     DeviceState* d = nullptr;
     st = device_state(&d);
     if (st != QMM_OK) return st;
-    // sh.rows x sh.bn tiles; clusters of cn CTAs share the activation rows
+    // sh.rows x sh.bn tiles, by one CTA or (narrow tiles) a pair
     const TileShape sh = w4_dense_shape(M, N, d->sms);
     const int n_tiles = (N + sh.bn - 1) / sh.bn;
-    const int cn = cluster_for(n_tiles);
+    const int cn = sh.bn == 128 ? pair_ctas(n_tiles) : 1;
     CUtensorMap ta, tb;
     if ((st = make_tmap(&ta, X, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, K, M, (uint64_t)K * 2, 64, sh.rows / cn,
                         CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK)
@@ -291,7 +291,7 @@ qmm_status qmm_fp8_blk128_ws(const uint16_t* X, int M, int K, int N, const uint8
     DeviceState* d = nullptr;
     st = device_state(&d);
     if (st != QMM_OK) return st;
-    const int cn = cluster_for(N / 128);
+    const int cn = pair_ctas(N / 128);
     CUtensorMap ta, tb;
     const int bm = fp8_tile_rows();
     if ((st = make_tmap(&ta, X, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, K, M, (uint64_t)K * 2, 64, bm / cn,
@@ -438,8 +438,7 @@ qmm_status moe_route_permute(const float* logits, int T, int E, int k, int32_t* 
 }
 
 // Gate/up + SwiGLU + q8_1 over permuted rows Xp [P][D], grouped by the 256-row
-// tile list: 256 token rows x (64 gate + 64 up weight rows) per tile, clusters
-// of CTAs sharing the token rows.  Writes Hq (f16 codes), Hd, Hs, Hd32.
+// tile list: 256 token rows x (64 gate + 64 up weight rows) per tile.  Writes Hq (f16 codes), Hd, Hs, Hd32.
 // Pointer-table form of the expert weights (moe_expert_table_build): E tensor
 // maps of the gate/up codes, E of the down indices, then the E gate/up scale and
 // E down scale pointers.
@@ -468,7 +467,7 @@ static qmm_status run_gate_up(DeviceState* d, const uint16_t* Xp, int P, int D, 
     const TileShape sh = w4_gate_up_shape();
     const int hstep = sh.bn / 2;
     if (F % hstep) return fail(QMM_ERR_UNSUPPORTED_SHAPE, "expert stage: F %% %d != 0 (F=%d)", hstep, F);
-    const int gu_cn = gate_up_cluster(F / hstep);
+    const int gu_cn = pair_ctas(F / hstep);
     CUtensorMap ta, tb;
     if ((st = make_tmap(&ta, Xp, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, D, P, (uint64_t)D * 2, 64, sh.rows / gu_cn,
                         CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK)

@@ -14,7 +14,7 @@
 // operands swapped (FP8 fold, gate/up), one M=128 (weight rows), N=256 (token
 // rows) MMA per K step, the accumulator transposed.  Operands are
 // K-major in the canonical 128-byte-swizzled layout.  Dense problems whose last
-// wave of tiles would leave half the clusters idle split those tiles along K
+// wave of tiles would leave half the SMs idle split those tiles along K
 // (fp32 partials in the caller's workspace, added in split order by
 // split_reduce_kernel).
 //
@@ -38,21 +38,16 @@
 
 namespace qmm {
 
-// CTA-pair (cta_group::2) GEMMs wherever a launch forms clusters of 2.
+// CTA-pair (cta_group::2) GEMMs wherever the column tiles pair up.
 #ifndef QMM_PAIR
 #define QMM_PAIR 0
-#endif
-
-// Short tiles (at most 128 live rows of 256) load half the activation tile.
-#ifndef QMM_HALF_A
-#define QMM_HALF_A 1
 #endif
 
 enum class BMode { W4, FP8 };
 enum class Epi { STORE, SWIGLU_Q81, FOLD_FP8 };
 
 template <BMode B_, Epi E_, int BN_, int CONV_WARPS_, int EPI_WARPS_, int TSTAGES_, int CSTAGES_, bool GROUPED_,
-          int CLUSTER_N_ = 1, int MSUB_ = 1, bool PAIR_ = false, bool SWAP_ = false>
+          int MSUB_ = 1, bool PAIR_ = false, bool SWAP_ = false>
 struct GemmCfg {
     static constexpr BMode B = B_;
     // Operands swapped (FP8 fold, gate/up): the converted weight tile is the
@@ -91,7 +86,7 @@ struct GemmCfg {
     // half of each operand from each CTA's shared memory, which halves the
     // shared-memory operand traffic per FLOP against a one-CTA M = 128 MMA.
     static constexpr bool PAIR = PAIR_;
-    static_assert(!PAIR || (CLUSTER_N_ == 2 && MSUB_ == 1), "CTA pair: a cluster of 2, one 128-row tile per CTA");
+    static_assert(!PAIR || MSUB_ == 1, "CTA pair: one 128-row tile per CTA");
     // accumulator columns per row sub-tile, and rows of the tile a work item covers
     static constexpr int ACC_N = PAIR_ ? 2 * BN_ : BN_;
     static constexpr int TILE_M = PAIR_ ? 256 : 128 * MSUB_;
@@ -99,11 +94,12 @@ struct GemmCfg {
     // issues MSUB MMAs (one per 128-row sub-tile) against the same B operand,
     // which divides the conversion work per FLOP by MSUB.
     static constexpr int MSUB = MSUB_;
-    // CTAs of a cluster work on the same activation rows and consecutive column
-    // tiles; each loads 1/CLUSTER_N of the activation tile and multicasts it to
-    // all, so the activations cross L2 once per cluster instead of once per CTA.
-    static constexpr int CLUSTER_N = CLUSTER_N_;
-    static constexpr int A_SLICE_ROWS = PAIR_ ? 128 : 128 * MSUB_ / CLUSTER_N_;
+    // CTAs of a cluster, on consecutive column tiles.  Only the pair forms clusters:
+    // every CTA loads its own activation rows.  (The two CTAs of a cluster sharing
+    // them by multicast copies was no faster: each stage is then refilled only when
+    // both have read it.  4096 x 4096 x 4096 W4 113 us without, 115 with;
+    // 5268 x 2048 x 5120 W4 105 and 107, 2048 x 5120 x 5120 FP8 110 and 111.)
+    static constexpr int CLUSTER_N = PAIR_ ? 2 : 1;
     static constexpr Epi EPI = E_;
     static constexpr bool GROUPED = GROUPED_;
     static constexpr int BM = 128 * MSUB_, BN = BN_, BK = 64, UMMA_K = 16;
@@ -180,7 +176,6 @@ struct GemmCfg {
     static_assert(MSUB == 1 || MSUB == 2, "row sub-tiles");
     static_assert(MSUB == 1 || !FOLD || EPI_WARPS == 16, "two-sub-tile folds need 16 fold warps (registers)");
     static_assert(NBUF >= 1, "TMEM columns");
-    static_assert(CLUSTER_N == 1 || CLUSTER_N == 2 || CLUSTER_N == 4, "cluster size");
     static_assert((EPI_WARPS == 4 && CONV_WARPS == 8) || (EPI_WARPS == 8 && CONV_WARPS == 4) ||
                       (EPI_WARPS == 16 && (CONV_WARPS == 2 || CONV_WARPS == 4 || CONV_WARPS == 8)) || WIDE16,
                   "warp layout");
@@ -610,9 +605,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::MAXNREG)
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::TSTAGES; ++i) {
             mbar_init(&full_t[i], 1);
-            // released by the MMA commit of every CTA of the cluster (each read the multicast
-            // tile), or (pair) by the pair's one MMA commit
-            mbar_init(&empty_t[i], C::PAIR ? 1 : C::CLUSTER_N);
+            mbar_init(&empty_t[i], 1);   // the MMA commit (pair: the pair's one)
         }
         // pair: the MMA issuer (even CTA) waits on its own full_c, which its converters
         // arrive on and, once per stage, the odd CTA's relay thread; and on its own
@@ -646,7 +639,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::MAXNREG)
     }
     tc_fence_before();
     __syncthreads();
-    if constexpr (C::CLUSTER_N > 1) cluster_sync();   // peers' barriers are initialised before any multicast
+    if constexpr (C::CLUSTER_N > 1) cluster_sync();   // the peer's barriers are initialised before anything signals them
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
@@ -1075,27 +1068,11 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::MAXNREG)
                         // different stages and kinds overlap.
                         const int l0 = (s % C::TMA_GROUPS) * 4;
                         uint8_t* st = tstage + s * C::TSTAGE_BYTES;
-                        // A tile of at most 128 live rows reads only the first 128-row slice of
-                        // the activation tile: the CTA that would load the second slice skips
-                        // it, and every CTA of the cluster expects that many bytes less.
-                        constexpr bool kHalfA = QMM_HALF_A && !C::PAIR && C::CLUSTER_N == 2 && C::MSUB == 2;
-                        const bool half_a = kHalfA && ti.rows <= 128;
-                        if (lane == l0)
-                            mbar_arrive_expect_tx(&full_t[s], C::TSTAGE_BYTES - (half_a ? C::A_SLICE_ROWS * 128 : 0));
+                        if (lane == l0) mbar_arrive_expect_tx(&full_t[s], C::TSTAGE_BYTES);
                         __syncwarp();
                         if (lane == l0) {
-                            if constexpr (C::PAIR) {
-                                // this CTA's 128 rows of the pair's 256-row tile
-                                tma_load_2d(st, &tmA, &full_t[s], kb * C::BK, ti.row0);
-                            } else if constexpr (C::CLUSTER_N > 1) {
-                                // this CTA's slice of the activation tile, written into every CTA of the cluster
-                                if (!(half_a && crank == 1))
-                                    tma_load_2d_multicast(st + crank * C::A_SLICE_ROWS * 128, &tmA, &full_t[s], kb * C::BK,
-                                                      ti.row0 + crank * C::A_SLICE_ROWS,
-                                                      (uint16_t)((1u << C::CLUSTER_N) - 1));
-                            } else {
-                                tma_load_2d(st, &tmA, &full_t[s], kb * C::BK, ti.row0);
-                            }
+                            // the activation tile (pair: this CTA's 128 rows of its 256)
+                            tma_load_2d(st, &tmA, &full_t[s], kb * C::BK, ti.row0);
                         } else if (lane == l0 + 1 || lane == l0 + 2) {
                             uint8_t* bdst = st + C::A_RAW_BYTES;
                             const int kx = kb * C::B_ROW_BYTES;
@@ -1220,10 +1197,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::MAXNREG)
                                 }
                             }
                             tc_commit(&empty_c[cs]);
-                            if constexpr (C::CLUSTER_N > 1)
-                                tc_commit_multicast(&empty_t[ts], (uint16_t)((1u << C::CLUSTER_N) - 1));
-                            else
-                                tc_commit(&empty_t[ts]);
+                            tc_commit(&empty_t[ts]);
                         }
                         if (++ts == C::TSTAGES) ts = 0;
                         if (++cs == C::CSTAGES) {
@@ -1409,8 +1383,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::MAXNREG)
     }
 
     __syncthreads();
-    // No CTA leaves while a peer may still multicast into its shared memory or
-    // signal its barriers.
+    // No CTA leaves while its peer may still signal its barriers or read its operands.
     if constexpr (C::CLUSTER_N > 1) cluster_sync();
     if (warp == 1) {
         tc_fence_after();

@@ -50,11 +50,10 @@ struct GemmParams {
 };
 
 // Launchers (return a cudaError_t from the launch).  Each takes two encoded
-// tensor maps: tmA for the activation operand (box rows 128 / cn: each CTA of a
-// cluster of cn loads that slice and multicasts it), tmB for the raw weight
-// codes; cn must divide p.n_tiles (cluster_for picks it).
-int cluster_for(int n_tiles);
-int gate_up_cluster(int n_tiles);   // the same choice for the gate/up GEMM
+// tensor maps: tmA for the activation operand (box rows: the tile's / cn), tmB for
+// the raw weight codes; cn, the CTAs that compute a tile (pair_ctas), must divide
+// p.n_tiles.
+int pair_ctas(int n_tiles);   // 2 in the CTA-pair build where the column tiles pair up, else 1
 cudaError_t launch_w4a16_dense(const CUtensorMap& tmA, const CUtensorMap& tmB, const GemmParams& p, int cn,
                                cudaStream_t s);
 cudaError_t launch_w4_gate_up_swiglu(const CUtensorMap& tmA, const CUtensorMap& tmB, const GemmParams& p, int cn,
@@ -65,7 +64,7 @@ struct TileShape {
 };
 TileShape w4_dense_shape(int M, int N, int sms);   // the launch picks the kernel by n_step (128 or 256)
 TileShape w4_gate_up_shape();
-// token rows of one FP8 tile (the activation box height before the cluster split)
+// token rows of one FP8 tile (the activation box height before a pair's split)
 int fp8_tile_rows();
 cudaError_t launch_fp8_blk128(const CUtensorMap& tmA, const CUtensorMap& tmB, const GemmParams& p, int cn,
                               cudaStream_t s);
