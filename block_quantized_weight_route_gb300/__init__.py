@@ -103,6 +103,12 @@ def lib() -> ctypes.CDLL:
         L.qmm_fp8a8_blk128.argtypes = [P, P, i32, i32, i32, P, P, P, i32, P]
         L.qmm_fp8a8_swiglu_blk128.restype = i32
         L.qmm_fp8a8_swiglu_blk128.argtypes = [P, P, i32, i32, i32, P, P, P, P, P]
+        L.qmm_dbg_fp8a8_plan.restype = i32
+        L.qmm_dbg_fp8a8_plan.argtypes = [i32, i32, i32, i32, P]
+        L.qmm_dbg_fp8a8_blk128.restype = i32
+        L.qmm_dbg_fp8a8_blk128.argtypes = [P, P, i32, i32, i32, P, P, P, i32, P, P]
+        L.qmm_dbg_fp8a8_swiglu_blk128.restype = i32
+        L.qmm_dbg_fp8a8_swiglu_blk128.argtypes = [P, P, i32, i32, i32, P, P, P, P, P, P]
         L.qmm_dbg_wait_timeout.restype = i32
         L.qmm_dbg_wait_timeout.argtypes = [ctypes.c_uint, P]
         _lib = L
@@ -567,6 +573,51 @@ def qmm_dbg_combine(Yslot, row, w):
     st = lib().qmm_dbg_combine(_ptr(Yslot), P, _ptr(row), _ptr(w), T, k, D, _ptr(Y), _stream(dev))
     _check("qmm_dbg_combine", st)
     return Y
+
+
+QMM_FP8A8_PLAN_FIELDS = 9
+
+
+def qmm_dbg_fp8a8_plan(M: int, K: int, N: int, gated: bool = False) -> tuple:
+    """The tiling that an FP8 x FP8 product of this shape takes: two (pair, bn, tn, cs)
+    and the column where the second launch begins (N: there is none)."""
+    arr = (ctypes.c_int * QMM_FP8A8_PLAN_FIELDS)()
+    _check("qmm_dbg_fp8a8_plan", lib().qmm_dbg_fp8a8_plan(M, K, N, int(gated), ctypes.cast(arr, ctypes.c_void_p)))
+    return tuple(arr[:4]), tuple(arr[4:8]), arr[8]
+
+
+def _plan_array(plan):
+    first, second, split = plan
+    return (ctypes.c_int * QMM_FP8A8_PLAN_FIELDS)(*first, *second, split)
+
+
+def qmm_dbg_fp8a8_blk128(Xq, Xs, W, S, plan, out_dtype=torch.bfloat16, Y=None):
+    """qmm_fp8a8_blk128 by a given tiling (as qmm_dbg_fp8a8_plan returns it)."""
+    M, K = Xq.shape
+    N = W.shape[0]
+    _need_operands(Xq, Xs, W, S, M, K, N, (N + 127) // 128, "W", "S")
+    if out_dtype not in _DTYPE:
+        raise TypeError("out_dtype must be float32 or bfloat16")
+    if Y is None:
+        Y = torch.empty((M, N), dtype=out_dtype, device=Xq.device)
+    _need(Y, "Y", (out_dtype,), (M, N))
+    _check("qmm_dbg_fp8a8_blk128",
+           lib().qmm_dbg_fp8a8_blk128(_ptr(Xq), _ptr(Xs), M, K, N, _ptr(W), _ptr(S), _ptr(Y), _DTYPE[out_dtype],
+                                      ctypes.cast(_plan_array(plan), ctypes.c_void_p), _stream(Xq.device)))
+    return Y
+
+
+def qmm_dbg_fp8a8_swiglu_blk128(Xq, Xs, Wgu, Sgu, plan):
+    """qmm_fp8a8_swiglu_blk128 by a given tiling."""
+    M, K = Xq.shape
+    F = Wgu.shape[0] // 2
+    _need_operands(Xq, Xs, Wgu, Sgu, M, K, 2 * F, 2 * F // 128, "Wgu", "Sgu")
+    Hq = torch.empty((M, F), dtype=torch.float8_e4m3fn, device=Xq.device)
+    Hs = torch.empty((M, F // 128), dtype=torch.float32, device=Xq.device)
+    _check("qmm_dbg_fp8a8_swiglu_blk128",
+           lib().qmm_dbg_fp8a8_swiglu_blk128(_ptr(Xq), _ptr(Xs), M, K, F, _ptr(Wgu), _ptr(Sgu), _ptr(Hq), _ptr(Hs),
+                                             ctypes.cast(_plan_array(plan), ctypes.c_void_p), _stream(Xq.device)))
+    return Hq, Hs
 
 
 def qmm_dbg_wait_timeout(timeout_us: int, device=None) -> None:

@@ -919,8 +919,8 @@ qmm_status qmm_add_rmsnorm_q8_1(const void* X, qmm_dtype xdt, int64_t ldx, const
 
 // ---------------------------------------------------------------- FP8 x FP8 products
 
-static qmm_status run_fp8a8(const char* who, DeviceState* d, Fp8a8Params& p, bool gated, cudaStream_t stream) {
-    const Fp8a8Plans plans = fp8a8_plan(p.M, p.K, p.N, gated, d->sms, d->index);
+static qmm_status run_fp8a8(const char* who, DeviceState* d, Fp8a8Params& p, bool gated, const Fp8a8Plans& plans,
+                            cudaStream_t stream) {
     p.err = d->err;
     for (int part = 0; part < (plans.split < p.N ? 2 : 1); ++part) {
         const Fp8a8Plan& pl = part ? plans.second : plans.first;
@@ -943,15 +943,24 @@ static qmm_status run_fp8a8(const char* who, DeviceState* d, Fp8a8Params& p, boo
     return QMM_OK;
 }
 
-qmm_status qmm_fp8a8_blk128(const uint8_t* Xq, const float* Xs, int M, int K, int N, const uint8_t* W, const float* S,
-                            void* Y, qmm_dtype ydt, cudaStream_t stream) {
+// qmm_dbg_fp8a8_plan's fields
+static Fp8a8Plans plans_of(const int* f) {
+    auto one = [](const int* g) { return Fp8a8Plan{g[0] != 0, g[1], g[2], g[3]}; };
+    return Fp8a8Plans{one(f), one(f + 4), f[8]};
+}
+
+// The two products, by the tiling of the rule or (fields) a given one.
+static qmm_status fp8a8_product(const char* who, const uint8_t* Xq, const float* Xs, int M, int K, int N, const uint8_t* W,
+                                const float* S, void* Y, qmm_dtype ydt, const int* fields, cudaStream_t stream) {
     if (M < 0 || K < 16 || K % 16 || N < 1 || M > kMostRows || K > kMostRows || N > kMostRows)
-        return fail(QMM_ERR_UNSUPPORTED_SHAPE,
-                    "qmm_fp8a8_blk128: need M >= 0, K %% 16 == 0, N >= 1, each <= 2^31 - 512 (M=%d K=%d N=%d)", M, K, N);
-    if (!is_dtype(ydt)) return fail(QMM_ERR_INVALID_ARG, "qmm_fp8a8_blk128: bad output type");
-    if (!W || !S || (M > 0 && (!Xq || !Xs || !Y))) return fail(QMM_ERR_INVALID_ARG, "qmm_fp8a8_blk128: null pointer");
+        return fail(QMM_ERR_UNSUPPORTED_SHAPE, "%s: need M >= 0, K %% 16 == 0, N >= 1, each <= 2^31 - 512 (M=%d K=%d N=%d)",
+                    who, M, K, N);
+    if (!is_dtype(ydt)) return fail(QMM_ERR_INVALID_ARG, "%s: bad output type", who);
+    if (!W || !S || (M > 0 && (!Xq || !Xs || !Y))) return fail(QMM_ERR_INVALID_ARG, "%s: null pointer", who);
     if (!aligned16(Xq) || !aligned16(Xs) || !aligned16(W) || !aligned16(S) || !aligned16(Y))
-        return fail(QMM_ERR_INVALID_ARG, "qmm_fp8a8_blk128: buffers must be 16-byte aligned");
+        return fail(QMM_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned", who);
+    if (fields && !fp8a8_plans_fit(plans_of(fields), M, K, N, false))
+        return fail(QMM_ERR_INVALID_ARG, "%s: no such tiling of this shape", who);
     DeviceState* d = nullptr;
     qmm_status st = device_state(&d);
     if (st != QMM_OK || M == 0) return st;
@@ -965,19 +974,19 @@ qmm_status qmm_fp8a8_blk128(const uint8_t* Xq, const float* Xs, int M, int K, in
     p.N = N;
     p.Y = Y;
     p.y_bf16 = ydt == QMM_BF16;
-    return run_fp8a8("qmm_fp8a8_blk128 launch", d, p, false, stream);
+    return run_fp8a8(who, d, p, false, fields ? plans_of(fields) : fp8a8_plan(M, K, N, false, d->sms, d->index), stream);
 }
 
-qmm_status qmm_fp8a8_swiglu_blk128(const uint8_t* Xq, const float* Xs, int M, int K, int F, const uint8_t* Wgu,
-                                   const float* Sgu, uint8_t* Hq, float* Hs, cudaStream_t stream) {
+static qmm_status fp8a8_swiglu(const char* who, const uint8_t* Xq, const float* Xs, int M, int K, int F, const uint8_t* Wgu,
+                               const float* Sgu, uint8_t* Hq, float* Hs, const int* fields, cudaStream_t stream) {
     if (M < 0 || K < 16 || K % 16 || F < 128 || F % 128 || M > kMostRows || K > kMostRows || F > kMostRows / 2)
         return fail(QMM_ERR_UNSUPPORTED_SHAPE,
-                    "qmm_fp8a8_swiglu_blk128: need M >= 0, K %% 16 == 0, F %% 128 == 0, M, K and 2F <= 2^31 - 512 "
-                    "(M=%d K=%d F=%d)", M, K, F);
-    if (!Wgu || !Sgu || (M > 0 && (!Xq || !Xs || !Hq || !Hs)))
-        return fail(QMM_ERR_INVALID_ARG, "qmm_fp8a8_swiglu_blk128: null pointer");
+                    "%s: need M >= 0, K %% 16 == 0, F %% 128 == 0, M, K and 2F <= 2^31 - 512 (M=%d K=%d F=%d)", who, M, K, F);
+    if (!Wgu || !Sgu || (M > 0 && (!Xq || !Xs || !Hq || !Hs))) return fail(QMM_ERR_INVALID_ARG, "%s: null pointer", who);
     if (!aligned16(Xq) || !aligned16(Xs) || !aligned16(Wgu) || !aligned16(Sgu) || !aligned16(Hq) || !aligned16(Hs))
-        return fail(QMM_ERR_INVALID_ARG, "qmm_fp8a8_swiglu_blk128: buffers must be 16-byte aligned");
+        return fail(QMM_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned", who);
+    if (fields && !fp8a8_plans_fit(plans_of(fields), M, K, F, true))
+        return fail(QMM_ERR_INVALID_ARG, "%s: no such tiling of this shape", who);
     DeviceState* d = nullptr;
     qmm_status st = device_state(&d);
     if (st != QMM_OK || M == 0) return st;
@@ -991,7 +1000,43 @@ qmm_status qmm_fp8a8_swiglu_blk128(const uint8_t* Xq, const float* Xs, int M, in
     p.N = F;
     p.Hq = Hq;
     p.Hs = Hs;
-    return run_fp8a8("qmm_fp8a8_swiglu_blk128 launch", d, p, true, stream);
+    return run_fp8a8(who, d, p, true, fields ? plans_of(fields) : fp8a8_plan(M, K, F, true, d->sms, d->index), stream);
+}
+
+qmm_status qmm_fp8a8_blk128(const uint8_t* Xq, const float* Xs, int M, int K, int N, const uint8_t* W, const float* S,
+                            void* Y, qmm_dtype ydt, cudaStream_t stream) {
+    return fp8a8_product("qmm_fp8a8_blk128", Xq, Xs, M, K, N, W, S, Y, ydt, nullptr, stream);
+}
+
+qmm_status qmm_fp8a8_swiglu_blk128(const uint8_t* Xq, const float* Xs, int M, int K, int F, const uint8_t* Wgu,
+                                   const float* Sgu, uint8_t* Hq, float* Hs, cudaStream_t stream) {
+    return fp8a8_swiglu("qmm_fp8a8_swiglu_blk128", Xq, Xs, M, K, F, Wgu, Sgu, Hq, Hs, nullptr, stream);
+}
+
+qmm_status qmm_dbg_fp8a8_plan(int M, int K, int N, int gated, int* plan) {
+    if (!plan) return fail(QMM_ERR_INVALID_ARG, "qmm_dbg_fp8a8_plan: null pointer");
+    if (M < 1 || K < 16 || K % 16 || N < 1 || M > kMostRows || K > kMostRows || N > kMostRows / 2 || (gated && N % 128))
+        return fail(QMM_ERR_UNSUPPORTED_SHAPE, "qmm_dbg_fp8a8_plan: no such product (M=%d K=%d N=%d)", M, K, N);
+    DeviceState* d = nullptr;
+    const qmm_status st = device_state(&d);
+    if (st != QMM_OK) return st;
+    const Fp8a8Plans r = fp8a8_plan(M, K, N, gated != 0, d->sms, d->index);
+    const int f[QMM_FP8A8_PLAN_FIELDS] = {r.first.pair,  r.first.bn,  r.first.tn,  r.first.cs, r.second.pair,
+                                          r.second.bn,   r.second.tn, r.second.cs, r.split};
+    memcpy(plan, f, sizeof f);
+    return QMM_OK;
+}
+
+qmm_status qmm_dbg_fp8a8_blk128(const uint8_t* Xq, const float* Xs, int M, int K, int N, const uint8_t* W, const float* S,
+                                void* Y, qmm_dtype ydt, const int* plan, cudaStream_t stream) {
+    if (!plan) return fail(QMM_ERR_INVALID_ARG, "qmm_dbg_fp8a8_blk128: null pointer");
+    return fp8a8_product("qmm_dbg_fp8a8_blk128", Xq, Xs, M, K, N, W, S, Y, ydt, plan, stream);
+}
+
+qmm_status qmm_dbg_fp8a8_swiglu_blk128(const uint8_t* Xq, const float* Xs, int M, int K, int F, const uint8_t* Wgu,
+                                       const float* Sgu, uint8_t* Hq, float* Hs, const int* plan, cudaStream_t stream) {
+    if (!plan) return fail(QMM_ERR_INVALID_ARG, "qmm_dbg_fp8a8_swiglu_blk128: null pointer");
+    return fp8a8_swiglu("qmm_dbg_fp8a8_swiglu_blk128", Xq, Xs, M, K, F, Wgu, Sgu, Hq, Hs, plan, stream);
 }
 
 qmm_status qmm_profile_enable(int on) {

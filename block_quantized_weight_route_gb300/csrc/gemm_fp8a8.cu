@@ -103,4 +103,25 @@ Fp8a8Plans fp8a8_plan(int M, int K, int N, bool gated, int sms, int dev) {
     return r;
 }
 
+static bool plan_fits(const Fp8a8Plan& pl, int M, int kbs, int cols, bool gated) {
+    if (pl.pair) {
+        for (int i = 0; i < (gated ? 1 : 3); ++i)
+            if (pl.bn == kBn[i]) return true;
+        return false;
+    }
+    bool tile = false;
+    for (int tn : kTn) tile |= pl.tn == tn;
+    return tile && pl.cs >= 1 && pl.cs <= 8 && pl.cs <= kbs && (cols + 127) / 128 <= 65535 && (M + pl.tn - 1) / pl.tn <= 65535;
+}
+
+// Every CTA of a narrow tile's cluster has a K block, the grid is in range, and no tile of
+// the first launch reaches into the second's columns, which start at a weight block.
+bool fp8a8_plans_fit(const Fp8a8Plans& r, int M, int K, int N, bool gated) {
+    const int kbs = (K + 127) / 128;
+    if (r.split < 1 || r.split > N || !plan_fits(r.first, M, kbs, r.split, gated)) return false;
+    if (r.split == N) return true;
+    const int width = r.first.pair && !gated ? r.first.bn : 128;
+    return r.split % 128 == 0 && r.split % width == 0 && plan_fits(r.second, M, kbs, N - r.split, gated);
+}
+
 }  // namespace qmm

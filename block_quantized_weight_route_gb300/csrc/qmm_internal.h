@@ -163,6 +163,7 @@ struct Fp8a8Plans {
     int split;
 };
 Fp8a8Plans fp8a8_plan(int M, int K, int N, bool gated, int sms, int dev);
+bool fp8a8_plans_fit(const Fp8a8Plans& r, int M, int K, int N, bool gated);   // whether the kernels can run a given tiling
 int fp8a8_narrow_at_once(bool gated, int tn, int cs, int dev);   // clusters of cs CTAs that the device holds at once (0: error)
 cudaError_t launch_fp8a8_narrow(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, bool gated, int tn,
                                 int cs, int dev, cudaStream_t s);

@@ -328,6 +328,26 @@ qmm_status qmm_dbg_combine(const float *Yslot, int P, const int32_t *row, const 
                            cudaStream_t stream);
 
 /*
+ * qmm_dbg_fp8a8_* -- the tilings of the FP8 x FP8 products, so that each can be
+ * checked by itself: which kernel takes a shape follows from estimated times.
+ *   A tiling is QMM_FP8A8_PLAN_FIELDS ints: {pair, bn, tn, cs} of the launch over the
+ *   columns [0, split), the same of the launch over [split, N), and split (N: one
+ *   launch).  pair != 0: CTA pairs with tiles of 256 tokens x bn columns (128, 192 or
+ *   256; gate/up: 256, gate and up together); pair == 0: tiles of tn tokens (16, 32, 64
+ *   or 128) x 128 columns, K over clusters of cs CTAs (1 to 8, at most the K blocks).
+ * qmm_dbg_fp8a8_plan -- the tiling that qmm_fp8a8_blk128 (gated == 0) or
+ *   qmm_fp8a8_swiglu_blk128 (N = F) takes on the current device.
+ * qmm_dbg_fp8a8_blk128 / qmm_dbg_fp8a8_swiglu_blk128 -- the products by a given tiling.
+ */
+#define QMM_FP8A8_PLAN_FIELDS 9
+qmm_status qmm_dbg_fp8a8_plan(int M, int K, int N, int gated, int *plan);
+qmm_status qmm_dbg_fp8a8_blk128(const uint8_t *Xq, const float *Xs, int M, int K, int N, const uint8_t *W,
+                                const float *S, void *Y, qmm_dtype ydt, const int *plan, cudaStream_t stream);
+qmm_status qmm_dbg_fp8a8_swiglu_blk128(const uint8_t *Xq, const float *Xs, int M, int K, int F, const uint8_t *Wgu,
+                                       const float *Sgu, uint8_t *Hq, float *Hs, const int *plan,
+                                       cudaStream_t stream);
+
+/*
  * qmm_dbg_wait_timeout -- test hook for failure detection (no counterpart on
  * the pages).  Launches one warp that waits, with the same bounded mbarrier
  * wait every kernel of the library uses, on a barrier that nothing arrives on;
