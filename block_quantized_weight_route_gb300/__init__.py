@@ -124,9 +124,22 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _need(t: torch.Tensor, name: str, dtypes, shape=None) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+_current_device = torch._C._cuda_getDevice
+
+
+def _device(t: torch.Tensor, name: str) -> int:
+    """The index of t's device, which has to be the current one: the library launches
+    there, and takes its error word and its tilings from there."""
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0:
         raise TypeError(f"{name} must be a CUDA tensor")
+    if dev != _current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, but the current device is cuda:{_current_device()}")
+    return dev
+
+
+def _need(t: torch.Tensor, name: str, dtypes, shape=None) -> torch.Tensor:
+    _device(t, name)
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
     if not t.is_contiguous():
@@ -142,7 +155,10 @@ _U8 = (torch.uint8, torch.int8)
 
 
 def _stream(device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    s = torch.cuda.current_stream(device)
+    if s.device.index != _current_device():
+        raise ValueError(f"the call's device is {s.device}, but the current device is cuda:{_current_device()}")
+    return ctypes.c_void_p(s.cuda_stream)
 
 
 def qmm_check_status(device=None) -> None:
@@ -239,26 +255,25 @@ _F32 = (torch.float32,)
 _Tensor = torch.Tensor
 
 
-def _ok(t, dtypes, shape) -> bool:
-    """Whether _need would pass.  The calls below take a few microseconds on the GPU, so
-    what passes is checked in one expression; _need words the error of what does not."""
-    return isinstance(t, _Tensor) and t.is_cuda and t.dtype in dtypes and t.shape == shape and t.is_contiguous()
+def _ok(t, dtypes, shape, dev: int) -> bool:
+    """Whether _need would pass, given the current device.  The calls below take a few
+    microseconds on the GPU, so what passes is checked in one expression; _need words the
+    error of what does not."""
+    return isinstance(t, _Tensor) and t.get_device() == dev and t.dtype in dtypes and t.shape == shape and t.is_contiguous()
 
 
-def _raw_stream(device) -> int:
-    """The current stream's handle, without making a Stream object."""
-    return torch._C._cuda_getCurrentRawStream(device.index)
+# The current stream's handle of a device index, without making a Stream object.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _pitch(t: torch.Tensor, name: str, shape) -> int:
-    """The row pitch of a CUDA matrix in fp32 or bf16 whose rows are contiguous."""
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in _DTYPE and t.shape == shape and t.dim() == 2:
+def _pitch(t: torch.Tensor, name: str, shape, dev: int) -> int:
+    """The row pitch of a matrix in fp32 or bf16 on device dev whose rows are contiguous."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype in _DTYPE and t.shape == shape and t.dim() == 2:
         if t.is_contiguous():
             return shape[1]
         if t.stride(1) == 1:
             return t.stride(0)
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+    _device(t, name)
     if t.dtype not in _DTYPE:
         raise TypeError(f"{name} must have dtype in {tuple(_DTYPE)}, got {t.dtype}")
     if t.dim() != 2 or t.shape == shape:
@@ -267,29 +282,30 @@ def _pitch(t: torch.Tensor, name: str, shape) -> int:
 
 
 def _norm_args(X, G, R, eps, Rout, Y, bf16_out):
-    """Checked arguments that the two norms share: (X's shape, Rout, Y, the call's first 13 arguments)."""
+    """Checked arguments that the two norms share: (X's device and shape, Rout, Y, the call's first 13 arguments)."""
+    dev = _device(X, "X")
     shape = X.shape
-    ldx = _pitch(X, "X", shape)
+    ldx = _pitch(X, "X", shape, dev)
     T, D = shape
-    if not _ok(G, _DTYPE, (D,)):
+    if not _ok(G, _DTYPE, (D,), dev):
         _need(G, "G", _DTYPE, (D,))
     if Y is None:
         if bf16_out:
             Y = torch.empty((T, D), dtype=torch.bfloat16, device=X.device)
-    elif not _ok(Y, _BF16, shape):
+    elif not _ok(Y, _BF16, shape, dev):
         _need(Y, "Y", _BF16, shape)
     if R is None:
         if Rout is not None:
             raise ValueError("Rout without R")
-        return shape, None, Y, (X.data_ptr(), _DTYPE[X.dtype], ldx, None, 0, None, 0, 0, G.data_ptr(),
+        return dev, shape, None, Y, (X.data_ptr(), _DTYPE[X.dtype], ldx, None, 0, None, 0, 0, G.data_ptr(),
                                 _DTYPE[G.dtype], eps, T, D)
-    ldr = _pitch(R, "R", shape)
+    ldr = _pitch(R, "R", shape, dev)
     if Rout is None:
         Rout = torch.empty((T, D), dtype=R.dtype, device=X.device)
-    ldro = _pitch(Rout, "Rout", shape)
+    ldro = _pitch(Rout, "Rout", shape, dev)
     if Rout.dtype != R.dtype:
         raise TypeError("Rout must have R's dtype")
-    return shape, Rout, Y, (X.data_ptr(), _DTYPE[X.dtype], ldx, R.data_ptr(), ldr, Rout.data_ptr(), ldro,
+    return dev, shape, Rout, Y, (X.data_ptr(), _DTYPE[X.dtype], ldx, R.data_ptr(), ldr, Rout.data_ptr(), ldro,
                             _DTYPE[R.dtype], G.data_ptr(), _DTYPE[G.dtype], eps, T, D)
 
 
@@ -300,18 +316,18 @@ def qmm_add_rmsnorm_fp8(X, G, R=None, eps: float = 1e-6, Rout=None, Q=None, S=No
     G are fp32 or bf16; X, R and Rout may be row slices.  Rout=R adds in place.
     bf16_out (or Y given): the normalised rows in bf16 too.  Returns Q, S, R
     (Rout, or None) and Y (or None)."""
-    shape, Rout, Y, args = _norm_args(X, G, R, eps, Rout, Y, bf16_out)
+    dev, shape, Rout, Y, args = _norm_args(X, G, R, eps, Rout, Y, bf16_out)
     groups = (shape[0], (shape[1] + 127) // 128)
     if Q is None:
         Q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=X.device)
-    elif not _ok(Q, _F8, shape):
+    elif not _ok(Q, _F8, shape, dev):
         _need(Q, "Q", _F8, shape)
     if S is None:
         S = torch.empty(groups, dtype=torch.float32, device=X.device)
-    elif not _ok(S, _F32, groups):
+    elif not _ok(S, _F32, groups, dev):
         _need(S, "S", _F32, groups)
     st = lib().qmm_add_rmsnorm_fp8(*args, Q.data_ptr(), S.data_ptr(), None if Y is None else Y.data_ptr(),
-                                   _raw_stream(X.device))
+                                   _raw_stream(dev))
     if st:
         _check("qmm_add_rmsnorm_fp8", st)
     return {"Q": Q, "S": S, "R": Rout, "Y": Y}
@@ -320,12 +336,12 @@ def qmm_add_rmsnorm_fp8(X, G, R=None, eps: float = 1e-6, Rout=None, Q=None, S=No
 def qmm_add_rmsnorm_q8_1(X, G, R=None, eps: float = 1e-6, Rout=None, Y=None, bf16_out: bool = False) -> dict:
     """qmm_add_rmsnorm_fp8 with the rows as q8_1 blocks of 32 (what qmm_q8_0_q8_1
     takes): Yq int8 [T, D], Yd / Ys fp16 bits [T, D/32], R and Y as there."""
-    (T, D), Rout, Y, args = _norm_args(X, G, R, eps, Rout, Y, bf16_out)
+    dev, (T, D), Rout, Y, args = _norm_args(X, G, R, eps, Rout, Y, bf16_out)
     Yq = torch.empty((T, D), dtype=torch.int8, device=X.device)
     Yd = torch.empty((T, D // 32), dtype=torch.int16, device=X.device)
     Ys = torch.empty((T, D // 32), dtype=torch.int16, device=X.device)
     st = lib().qmm_add_rmsnorm_q8_1(*args, Yq.data_ptr(), Yd.data_ptr(), Ys.data_ptr(),
-                                    None if Y is None else Y.data_ptr(), _raw_stream(X.device))
+                                    None if Y is None else Y.data_ptr(), _raw_stream(dev))
     if st:
         _check("qmm_add_rmsnorm_q8_1", st)
     return {"Yq": Yq, "Yd": Yd, "Ys": Ys, "R": Rout, "Y": Y}
@@ -343,20 +359,21 @@ def _need_operands(Xq, Xs, W, S, M: int, K: int, rows: int, blocks: int, name_w:
 def qmm_fp8a8_blk128(Xq, Xs, W, S, out_dtype=torch.bfloat16, Y=None):
     """Y[M,N] = sum over 128-K blocks of Xs[m, kb] * S[n/128, kb] * e4m3(Xq) . e4m3(W)^T.
     Xq [M, K] and W [N, K] E4M3, Xs [M, ceil(K/128)] and S [ceil(N/128), ceil(K/128)] fp32."""
+    dev = _device(Xq, "Xq")
     M, K = Xq.shape
     N = W.shape[0]
     if out_dtype not in _DTYPE:
         raise TypeError("out_dtype must be float32 or bfloat16")
     kb = (K + 127) // 128
-    if not (_ok(Xq, _F8, Xq.shape) and _ok(Xs, _F32, (M, kb)) and _ok(W, _F8, (N, K)) and
-            _ok(S, _F32, ((N + 127) // 128, kb))):
+    if not (_ok(Xq, _F8, Xq.shape, dev) and _ok(Xs, _F32, (M, kb), dev) and _ok(W, _F8, (N, K), dev) and
+            _ok(S, _F32, ((N + 127) // 128, kb), dev)):
         _need_operands(Xq, Xs, W, S, M, K, N, (N + 127) // 128, "W", "S")
     if Y is None:
         Y = torch.empty((M, N), dtype=out_dtype, device=Xq.device)
-    elif not _ok(Y, (out_dtype,), (M, N)):
+    elif not _ok(Y, (out_dtype,), (M, N), dev):
         _need(Y, "Y", (out_dtype,), (M, N))
     st = lib().qmm_fp8a8_blk128(Xq.data_ptr(), Xs.data_ptr(), M, K, N, W.data_ptr(), S.data_ptr(), Y.data_ptr(),
-                                _DTYPE[out_dtype], _raw_stream(Xq.device))
+                                _DTYPE[out_dtype], _raw_stream(dev))
     if st:
         _check("qmm_fp8a8_blk128", st)
     return Y
@@ -366,22 +383,23 @@ def qmm_fp8a8_swiglu_blk128(Xq, Xs, Wgu, Sgu, Hq=None, Hs=None):
     """H = silu(X . Wg^T) * (X . Wu^T) as E4M3 codes Hq [M, F] with one fp32 scale per
     128 columns Hs [M, F/128].  Xq, Xs as in qmm_fp8a8_blk128; Wgu [2F, K] E4M3 (gate
     rows first), Sgu [2F/128, ceil(K/128)] fp32."""
+    dev = _device(Xq, "Xq")
     M, K = Xq.shape
     F = Wgu.shape[0] // 2
     kb = (K + 127) // 128
-    if not (_ok(Xq, _F8, Xq.shape) and _ok(Xs, _F32, (M, kb)) and _ok(Wgu, _F8, (2 * F, K)) and
-            _ok(Sgu, _F32, (2 * F // 128, kb))):
+    if not (_ok(Xq, _F8, Xq.shape, dev) and _ok(Xs, _F32, (M, kb), dev) and _ok(Wgu, _F8, (2 * F, K), dev) and
+            _ok(Sgu, _F32, (2 * F // 128, kb), dev)):
         _need_operands(Xq, Xs, Wgu, Sgu, M, K, 2 * F, 2 * F // 128, "Wgu", "Sgu")
     if Hq is None:
         Hq = torch.empty((M, F), dtype=torch.float8_e4m3fn, device=Xq.device)
-    elif not _ok(Hq, _F8, (M, F)):
+    elif not _ok(Hq, _F8, (M, F), dev):
         _need(Hq, "Hq", _F8, (M, F))
     if Hs is None:
         Hs = torch.empty((M, F // 128), dtype=torch.float32, device=Xq.device)
-    elif not _ok(Hs, _F32, (M, F // 128)):
+    elif not _ok(Hs, _F32, (M, F // 128), dev):
         _need(Hs, "Hs", _F32, (M, F // 128))
     st = lib().qmm_fp8a8_swiglu_blk128(Xq.data_ptr(), Xs.data_ptr(), M, K, F, Wgu.data_ptr(), Sgu.data_ptr(),
-                                       Hq.data_ptr(), Hs.data_ptr(), _raw_stream(Xq.device))
+                                       Hq.data_ptr(), Hs.data_ptr(), _raw_stream(dev))
     if st:
         _check("qmm_fp8a8_swiglu_blk128", st)
     return Hq, Hs
@@ -403,9 +421,8 @@ def moe_route_permute(logits, k: int, ws=None) -> dict:
                offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
                src=torch.empty(T * k, dtype=torch.int32, device=dev),
                row=torch.empty((T, k), dtype=torch.int32, device=dev))
-    need = moe_route_workspace_size(T, E, k)
     if ws is None:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        ws = torch.empty(max(moe_route_workspace_size(T, E, k), 256), dtype=torch.uint8, device=dev)
     _need(ws, "ws", _U8)
     st = lib().moe_route_permute(_ptr(logits), T, E, k, _ptr(out["ids"]), _ptr(out["w"]), _ptr(out["counts"]),
                                  _ptr(out["offsets"]), _ptr(out["src"]), _ptr(out["row"]), _ptr(ws), ws.numel(),
