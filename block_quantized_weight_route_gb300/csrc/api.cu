@@ -51,7 +51,6 @@ struct DeviceState {
     uint32_t* err = nullptr;
 };
 
-constexpr int kMaxDevices = 64;
 DeviceState g_dev[kMaxDevices];
 std::mutex g_mu;
 EncodeTiledFn g_encode = nullptr;

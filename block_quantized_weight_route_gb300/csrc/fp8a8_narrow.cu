@@ -425,11 +425,11 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     }
 }
 
-// One-time set-up on device `dev` (the current one, below 64).
+// One-time set-up on device `dev` (the current one).
 template <class C>
 cudaError_t prepare(int dev) {
-    static bool ready[64] = {};
-    if (!ready[dev]) {
+    static PerDevice ready;
+    if (!ready.get(dev)) {
         cudaError_t e = cudaFuncSetAttribute(fp8a8_narrow_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
         if constexpr (C::REG_SPLIT) {
@@ -440,7 +440,7 @@ cudaError_t prepare(int dev) {
             if (e != cudaSuccess) return e;
             if (fa.numRegs != C::REGS) return cudaErrorInvalidConfiguration;
         }
-        ready[dev] = true;
+        ready.set(dev, 1);
     }
     return cudaSuccess;
 }
@@ -471,8 +471,8 @@ namespace {
 
 template <class C>
 int clusters_at_once(int cs, int dev) {
-    static int at_once[64][9] = {};
-    if (at_once[dev][cs] == 0) {
+    static PerDevice at_once[9];   // by cs
+    if (at_once[cs].get(dev) == 0) {
         if (prepare<C>(dev) != cudaSuccess) return 0;
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
@@ -489,9 +489,9 @@ int clusters_at_once(int cs, int dev) {
         if (cudaOccupancyMaxActiveClusters(&n, fp8a8_narrow_kernel<C>, &cfg) != cudaSuccess || n < 1) return 0;
         // (the query counts one CTA per SM for a kernel that allocates TMEM; two whose shared
         // memory, registers and TMEM fit do run side by side)
-        at_once[dev][cs] = n * C::PER_SM;
+        at_once[cs].set(dev, n * C::PER_SM);
     }
-    return at_once[dev][cs];
+    return at_once[cs].get(dev);
 }
 
 // f(configuration) for the kernel of tn tokens a tile

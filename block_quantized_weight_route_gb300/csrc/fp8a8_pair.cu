@@ -381,9 +381,10 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
 
 template <class C>
 cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, int sms, int dev, cudaStream_t s) {
-    static int most[64] = {};   // pairs that fit the device at once
+    static PerDevice most;   // pairs that fit the device at once
     cudaError_t e;
-    if (most[dev] == 0) {
+    int at_once = most.get(dev);
+    if (at_once == 0) {
         e = cudaFuncSetAttribute(fp8a8_pair_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
         if constexpr (C::REG_SPLIT) {
@@ -407,16 +408,15 @@ cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Para
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (most[dev] == 0) {
+    if (at_once == 0) {
         cfg.gridDim = dim3(2 * (sms / 2), 1, 1);
-        int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, fp8a8_pair_kernel<C>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&at_once, fp8a8_pair_kernel<C>, &cfg);
         if (e != cudaSuccess) return e;
-        if (n < 1) return cudaErrorInvalidConfiguration;
-        most[dev] = n;
+        if (at_once < 1) return cudaErrorInvalidConfiguration;
+        most.set(dev, at_once);
     }
     const long tiles = (long)p.m_tiles * p.n_tiles;
-    cfg.gridDim = dim3(2 * (unsigned)(tiles < most[dev] ? tiles : most[dev]), 1, 1);
+    cfg.gridDim = dim3(2 * (unsigned)(tiles < at_once ? tiles : at_once), 1, 1);
     return cudaLaunchKernelEx(&cfg, fp8a8_pair_kernel<C>, tx, tw, p);
 }
 

@@ -1418,8 +1418,8 @@ cudaError_t launch_qgemm(const CUtensorMap& tmA, const CUtensorMap& tmB, GemmPar
     }
     int dev = 0;
     cudaGetDevice(&dev);
-    static int max_clusters[64] = {};
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    static PerDevice max_clusters;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1431,7 +1431,8 @@ cudaError_t launch_qgemm(const CUtensorMap& tmA, const CUtensorMap& tmB, GemmPar
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (max_clusters[dev] == 0) {
+    int clusters = max_clusters.get(dev);
+    if (clusters == 0) {
         int sms = 0;
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         int n = sms / C::CLUSTER_N;
@@ -1440,9 +1441,8 @@ cudaError_t launch_qgemm(const CUtensorMap& tmA, const CUtensorMap& tmB, GemmPar
             int q = 0;
             if (cudaOccupancyMaxActiveClusters(&q, qgemm_kernel<C>, &cfg) == cudaSuccess && q > 0) n = q;
         }
-        max_clusters[dev] = n;
+        max_clusters.set(dev, clusters = n);
     }
-    int clusters = max_clusters[dev];
     p.split_S = 1;
     if constexpr (!C::GROUPED) {
         // Dense: when the last wave of tiles fills at most half the clusters, split

@@ -6,6 +6,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "device_cache.h"
+
 namespace qmm {
 
 // Parameters of one launch of the block-quantised GEMM kernel family.
