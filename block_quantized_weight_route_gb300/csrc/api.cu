@@ -918,8 +918,21 @@ qmm_status qmm_add_rmsnorm_q8_1(const void* X, qmm_dtype xdt, int64_t ldx, const
 
 // ---------------------------------------------------------------- FP8 x FP8 products
 
-static qmm_status run_fp8a8(const char* who, DeviceState* d, Fp8a8Params& p, bool gated, const Fp8a8Plans& plans,
+// qmm_dbg_fp8a8_plan's fields
+static Fp8a8Plans plans_of(const int* f) {
+    auto one = [](const int* g) { return Fp8a8Plan{g[0] != 0, g[1], g[2], g[3]}; };
+    return Fp8a8Plans{one(f), one(f + 4), f[8]};
+}
+
+static qmm_status run_fp8a8(const char* who, DeviceState* d, Fp8a8Params& p, bool gated, const int* fields,
                             cudaStream_t stream) {
+    Fp8a8Plans plans;
+    if (fields) {
+        plans = plans_of(fields);
+    } else {
+        const cudaError_t e = fp8a8_plan(p.M, p.K, p.N, gated, d->sms, d->index, &plans);
+        if (e != cudaSuccess) return cuda_fail(e, who);
+    }
     p.err = d->err;
     for (int part = 0; part < (plans.split < p.N ? 2 : 1); ++part) {
         const Fp8a8Plan& pl = part ? plans.second : plans.first;
@@ -940,12 +953,6 @@ static qmm_status run_fp8a8(const char* who, DeviceState* d, Fp8a8Params& p, boo
         if (e != cudaSuccess) return cuda_fail(e, who);
     }
     return QMM_OK;
-}
-
-// qmm_dbg_fp8a8_plan's fields
-static Fp8a8Plans plans_of(const int* f) {
-    auto one = [](const int* g) { return Fp8a8Plan{g[0] != 0, g[1], g[2], g[3]}; };
-    return Fp8a8Plans{one(f), one(f + 4), f[8]};
 }
 
 // The two products, by the tiling of the rule or (fields) a given one.
@@ -973,7 +980,7 @@ static qmm_status fp8a8_product(const char* who, const uint8_t* Xq, const float*
     p.N = N;
     p.Y = Y;
     p.y_bf16 = ydt == QMM_BF16;
-    return run_fp8a8(who, d, p, false, fields ? plans_of(fields) : fp8a8_plan(M, K, N, false, d->sms, d->index), stream);
+    return run_fp8a8(who, d, p, false, fields, stream);
 }
 
 static qmm_status fp8a8_swiglu(const char* who, const uint8_t* Xq, const float* Xs, int M, int K, int F, const uint8_t* Wgu,
@@ -999,7 +1006,7 @@ static qmm_status fp8a8_swiglu(const char* who, const uint8_t* Xq, const float* 
     p.N = F;
     p.Hq = Hq;
     p.Hs = Hs;
-    return run_fp8a8(who, d, p, true, fields ? plans_of(fields) : fp8a8_plan(M, K, F, true, d->sms, d->index), stream);
+    return run_fp8a8(who, d, p, true, fields, stream);
 }
 
 qmm_status qmm_fp8a8_blk128(const uint8_t* Xq, const float* Xs, int M, int K, int N, const uint8_t* W, const float* S,
@@ -1019,7 +1026,9 @@ qmm_status qmm_dbg_fp8a8_plan(int M, int K, int N, int gated, int* plan) {
     DeviceState* d = nullptr;
     const qmm_status st = device_state(&d);
     if (st != QMM_OK) return st;
-    const Fp8a8Plans r = fp8a8_plan(M, K, N, gated != 0, d->sms, d->index);
+    Fp8a8Plans r;
+    const cudaError_t e = fp8a8_plan(M, K, N, gated != 0, d->sms, d->index, &r);
+    if (e != cudaSuccess) return cuda_fail(e, "qmm_dbg_fp8a8_plan");
     const int f[QMM_FP8A8_PLAN_FIELDS] = {r.first.pair,  r.first.bn,  r.first.tn,  r.first.cs, r.second.pair,
                                           r.second.bn,   r.second.tn, r.second.cs, r.split};
     memcpy(plan, f, sizeof f);

@@ -44,7 +44,8 @@ struct NarrowCfg {
     static constexpr int FOLD_WARPS = TOKENS_M ? 16 : 4 * MATS * TG, THREADS = 128 + 32 * FOLD_WARPS;
     // 64 sums a thread (tokens on the M side, gate and up): more registers for the fold warps
     static constexpr bool REG_SPLIT = TOKENS_M && GATED;
-    static constexpr int REGS = 96, REGS_FOLD = 104, REGS_OTHER = 64;
+    static constexpr int REGS_EVEN = 65536 / (THREADS * PER_SM) / 8 * 8, REGS = REGS_EVEN < 255 ? REGS_EVEN : 255;
+    static constexpr int REGS_FOLD = 104, REGS_OTHER = 64;
     static_assert(!REG_SPLIT || REGS_FOLD * 32 * FOLD_WARPS + REGS_OTHER * 128 == REGS * THREADS, "register shares = launch registers");
     static constexpr int COPIES = MATS + 1;
     static_assert(COPIES * STAGES <= 32, "a lane per copy");
@@ -221,7 +222,7 @@ __device__ __forceinline__ void fold_tokens_m(const Fp8a8Params& p, int warp, in
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, C::PER_SM)
+__global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
     fp8a8_narrow_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, Fp8a8Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stage = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -470,10 +471,11 @@ cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Para
 namespace {
 
 template <class C>
-int clusters_at_once(int cs, int dev) {
+cudaError_t clusters_at_once(int cs, int dev, int* clusters) {
     static PerDevice at_once[9];   // by cs
     if (at_once[cs].get(dev) == 0) {
-        if (prepare<C>(dev) != cudaSuccess) return 0;
+        cudaError_t e = prepare<C>(dev);
+        if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -486,12 +488,14 @@ int clusters_at_once(int cs, int dev) {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, fp8a8_narrow_kernel<C>, &cfg) != cudaSuccess || n < 1) return 0;
+        e = cudaOccupancyMaxActiveClusters(&n, fp8a8_narrow_kernel<C>, &cfg);
+        if (e != cudaSuccess) return e;
         // (the query counts one CTA per SM for a kernel that allocates TMEM; two whose shared
         // memory, registers and TMEM fit do run side by side)
         at_once[cs].set(dev, n * C::PER_SM);
     }
-    return at_once[cs].get(dev);
+    *clusters = at_once[cs].get(dev);
+    return cudaSuccess;
 }
 
 // f(configuration) for the kernel of tn tokens a tile
@@ -512,8 +516,8 @@ auto with_config(bool gated, int tn, F f) {
 }  // namespace
 
 // (A cluster's CTAs are on SMs of one group of SMs, so fewer fit than slots / cs.)
-int fp8a8_narrow_at_once(bool gated, int tn, int cs, int dev) {
-    return with_config(gated, tn, [&](auto c) { return clusters_at_once<decltype(c)>(cs, dev); });
+cudaError_t fp8a8_narrow_at_once(bool gated, int tn, int cs, int dev, int* clusters) {
+    return with_config(gated, tn, [&](auto c) { return clusters_at_once<decltype(c)>(cs, dev, clusters); });
 }
 
 cudaError_t launch_fp8a8_narrow(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, bool gated, int tn,

@@ -29,21 +29,24 @@ double pair_time(long tiles, long pairs, int i, int kbs) {
 // Measured at 5120 x 5120: 128 tokens narrow 128/3 10.5 us, pair 13.9; 300 tokens narrow
 // 128/1 16.8, pair (192 columns) 18.7; 600 tokens 32.9 and 21.5; 1 token narrow 16/6 6.5,
 // 16/3 7.5, 16/7 (more CTAs than fit at once) 11.3; at 2000 x 1000, 128 tokens 32/4 6.4, 128/8 8.5.
-Fp8a8Plan one_launch(int M, int kbs, int cols, bool gated, int sms, int dev, double* time) {
-    Fp8a8Plan best{};
+// (A tiling that cannot be asked about is an error, not one tiling less.)
+cudaError_t one_launch(int M, int kbs, int cols, bool gated, int sms, int dev, Fp8a8Plan* best, double* time) {
+    *best = Fp8a8Plan{};
     *time = 1e300;
     auto consider = [&](const Fp8a8Plan& pl, double t) {
         if (t < *time) {
             *time = t;
-            best = pl;
+            *best = pl;
         }
     };
     for (int i = 0; i < 4; ++i) {
         const long tiles = (long)((cols + 127) / 128) * ((M + kTn[i] - 1) / kTn[i]);
         if (tiles > 8L * sms) continue;   // the pair kernel's
         for (int cs = 1; cs <= 8 && cs <= kbs; ++cs) {
-            const int at_once = fp8a8_narrow_at_once(gated, kTn[i], cs, dev);
-            if (at_once < 1) continue;
+            int at_once = 0;
+            const cudaError_t e = fp8a8_narrow_at_once(gated, kTn[i], cs, dev, &at_once);
+            if (e != cudaSuccess) return e;
+            if (at_once < 1) continue;   // clusters of cs do not fit this device
             Fp8a8Plan pl{};
             pl.tn = kTn[i];
             pl.cs = cs;
@@ -61,7 +64,7 @@ Fp8a8Plan one_launch(int M, int kbs, int cols, bool gated, int sms, int dev, dou
         pl.bn = kBn[i];
         consider(pl, pair_time((long)((M + 255) / 256) * ((cols + width - 1) / width), sms / 2, i, kbs));
     }
-    return best;
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -69,7 +72,7 @@ Fp8a8Plan one_launch(int M, int kbs, int cols, bool gated, int sms, int dev, dou
 // One launch, or the columns of the whole waves of widest pair tiles in one and the rest
 // in a second with a plan of its own, where that takes less by more than the second
 // launch costs (2048 x 5120 x 5120: 152 tiles in two waves and 256 columns left).
-Fp8a8Plans fp8a8_plan(int M, int K, int N, bool gated, int sms, int dev) {
+cudaError_t fp8a8_plan(int M, int K, int N, bool gated, int sms, int dev, Fp8a8Plans* plans) {
     // (a model's calls come in the same few shapes: the last ones' plans are kept)
     struct Known {
         int M, K, N, gated, dev;
@@ -77,11 +80,15 @@ Fp8a8Plans fp8a8_plan(int M, int K, int N, bool gated, int sms, int dev) {
     };
     static thread_local Known known[16] = {};
     Known& slot = known[((unsigned)M * 2654435761u ^ (unsigned)K * 40503u ^ (unsigned)N * 9973u ^ (unsigned)gated) >> 7 & 15u];
-    if (slot.M == M && slot.K == K && slot.N == N && slot.gated == gated && slot.dev == dev) return slot.plans;
+    if (slot.M == M && slot.K == K && slot.N == N && slot.gated == gated && slot.dev == dev) {
+        *plans = slot.plans;
+        return cudaSuccess;
+    }
     const int kbs = (K + 127) / 128;
     Fp8a8Plans r{};
     double least;
-    r.first = one_launch(M, kbs, N, gated, sms, dev, &least);
+    cudaError_t e = one_launch(M, kbs, N, gated, sms, dev, &r.first, &least);
+    if (e != cudaSuccess) return e;
     r.split = N;
     const long mt = (M + 255) / 256, pairs = sms / 2;
     const int width = gated ? 128 : kBn[0];
@@ -89,7 +96,9 @@ Fp8a8Plans fp8a8_plan(int M, int K, int N, bool gated, int sms, int dev) {
     const long whole = waves * pairs / mt * width;
     if (waves >= 1 && whole > 0 && whole < N) {
         double rest;
-        const Fp8a8Plan second = one_launch(M, kbs, N - (int)whole, gated, sms, dev, &rest);
+        Fp8a8Plan second;
+        e = one_launch(M, kbs, N - (int)whole, gated, sms, dev, &second, &rest);
+        if (e != cudaSuccess) return e;
         const double t = pair_time(mt * (whole / width), pairs, 0, kbs) + rest + kSecondLaunch;
         if (t < 0.97 * least) {
             r.first = Fp8a8Plan{};
@@ -100,7 +109,8 @@ Fp8a8Plans fp8a8_plan(int M, int K, int N, bool gated, int sms, int dev) {
         }
     }
     slot = Known{M, K, N, gated, dev, r};
-    return r;
+    *plans = r;
+    return cudaSuccess;
 }
 
 static bool plan_fits(const Fp8a8Plan& pl, int M, int kbs, int cols, bool gated) {

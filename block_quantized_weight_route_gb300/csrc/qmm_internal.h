@@ -164,9 +164,10 @@ struct Fp8a8Plans {
     Fp8a8Plan first, second;
     int split;
 };
-Fp8a8Plans fp8a8_plan(int M, int K, int N, bool gated, int sms, int dev);
+cudaError_t fp8a8_plan(int M, int K, int N, bool gated, int sms, int dev, Fp8a8Plans* plans);
 bool fp8a8_plans_fit(const Fp8a8Plans& r, int M, int K, int N, bool gated);   // whether the kernels can run a given tiling
-int fp8a8_narrow_at_once(bool gated, int tn, int cs, int dev);   // clusters of cs CTAs that the device holds at once (0: error)
+// clusters of cs CTAs that the device holds at once (0: none)
+cudaError_t fp8a8_narrow_at_once(bool gated, int tn, int cs, int dev, int* clusters);
 cudaError_t launch_fp8a8_narrow(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, bool gated, int tn,
                                 int cs, int dev, cudaStream_t s);
 cudaError_t launch_fp8a8_pair(const CUtensorMap& tx, const CUtensorMap& tw, Fp8a8Params p, bool gated, int bn, int sms,
