@@ -57,6 +57,13 @@ cudaError_t one_launch(int M, int kbs, int cols, bool gated, int sms, int dev, F
                              traffic_time(tiles, kbs, kTn[i] + (gated ? 256 : 128)));
         }
     }
+    // Up to 16 tokens (the narrowest tile) the pair kernel takes only what the narrow one
+    // cannot.  Its constants were fitted to waves of full tiles and leave out its start, so
+    // that with K <= 640 the estimate favours it where it takes 3.1 us for 2.5 (1 x 16 x 128)
+    // to 5.3 for 3.7 (1 x 400 x 5120); of 496 such shapes the narrow kernel was faster in 495, by
+    // 14% in the mean.  With several hundred tokens the estimate is right (600 x 16 x 256:
+    // 16-token tiles 34% slower).
+    if (M <= kTn[0] && *time < 1e300) return cudaSuccess;
     for (int i = 0; i < (gated ? 1 : 3); ++i) {
         const int width = gated ? 128 : kBn[i];
         Fp8a8Plan pl{};
@@ -94,7 +101,7 @@ cudaError_t fp8a8_plan(int M, int K, int N, bool gated, int sms, int dev, Fp8a8P
     const int width = gated ? 128 : kBn[0];
     const long waves = mt * ((N + width - 1) / width) / pairs;
     const long whole = waves * pairs / mt * width;
-    if (waves >= 1 && whole > 0 && whole < N) {
+    if (M > kTn[0] && waves >= 1 && whole > 0 && whole < N) {
         double rest;
         Fp8a8Plan second;
         e = one_launch(M, kbs, N - (int)whole, gated, sms, dev, &second, &rest);

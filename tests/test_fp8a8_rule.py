@@ -84,3 +84,12 @@ def test_the_workloads_sizes(rule, M, K, N, gated, want):
     e, pl = plan(rule, M, K, N, gated)
     assert e == 0 and pl[0] == want
     assert pl[2] == (4864 if (M, N) == (2048, 5120) else N)
+
+
+@pytest.mark.parametrize("M", [1, 2, 5, 16])
+@pytest.mark.parametrize("K", [16, 128, 256, 400, 640, 1024, 5120])
+@pytest.mark.parametrize("N", [1, 128, 768, 2048, 5120, 17408])
+def test_up_to_16_tokens_take_the_narrow_kernel(rule, M, K, N):
+    """Faster there than the kernel of 256 tokens a tile, by up to 28% with small K."""
+    e, pl = plan(rule, M, K, N)
+    assert e == 0 and pl[0][0] == 0 and pl[0][2] == 16 and pl[2] == N, pl
