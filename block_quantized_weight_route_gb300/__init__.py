@@ -266,6 +266,13 @@ def _ok(t, dtypes, shape, dev: int) -> bool:
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
+def _aligned(t: torch.Tensor) -> torch.Tensor:
+    """t, or a copy of it that starts at a multiple of 16 bytes, as the library asks of
+    every buffer.  Row slices of codes do by themselves; a row of scales can be as short as
+    4 bytes.  (Callers look at the addresses first, which they need anyway.)"""
+    return t if t.data_ptr() & 15 == 0 else t.clone()
+
+
 def _pitch(t: torch.Tensor, name: str, shape, dev: int) -> int:
     """The row pitch of a matrix in fp32 or bf16 on device dev whose rows are contiguous."""
     if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype in _DTYPE and t.shape == shape and t.dim() == 2:
@@ -313,7 +320,7 @@ def qmm_add_rmsnorm_fp8(X, G, R=None, eps: float = 1e-6, Rout=None, Q=None, S=No
                         bf16_out: bool = False) -> dict:
     """RMS norm of X [T, D], or of the stored sum Rout = X + R, times G [D], as E4M3
     codes Q [T, D] with one fp32 scale per 128 columns S [T, ceil(D/128)].  X, R and
-    G are fp32 or bf16; X, R and Rout may be row slices.  Rout=R adds in place.
+    G are fp32 or bf16; X, R, Rout, Q and S may be row slices.  Rout=R adds in place.
     bf16_out (or Y given): the normalised rows in bf16 too.  Returns Q, S, R
     (Rout, or None) and Y (or None)."""
     dev, shape, Rout, Y, args = _norm_args(X, G, R, eps, Rout, Y, bf16_out)
@@ -326,10 +333,14 @@ def qmm_add_rmsnorm_fp8(X, G, R=None, eps: float = 1e-6, Rout=None, Q=None, S=No
         S = torch.empty(groups, dtype=torch.float32, device=X.device)
     elif not _ok(S, _F32, groups, dev):
         _need(S, "S", _F32, groups)
-    st = lib().qmm_add_rmsnorm_fp8(*args, Q.data_ptr(), S.data_ptr(), None if Y is None else Y.data_ptr(),
-                                   _raw_stream(dev))
+    s = S.data_ptr()
+    scales = _aligned(S) if s & 15 else None
+    st = lib().qmm_add_rmsnorm_fp8(*args, Q.data_ptr(), s if scales is None else scales.data_ptr(),
+                                   None if Y is None else Y.data_ptr(), _raw_stream(dev))
     if st:
         _check("qmm_add_rmsnorm_fp8", st)
+    if scales is not None:
+        S.copy_(scales)
     return {"Q": Q, "S": S, "R": Rout, "Y": Y}
 
 
@@ -358,7 +369,8 @@ def _need_operands(Xq, Xs, W, S, M: int, K: int, rows: int, blocks: int, name_w:
 
 def qmm_fp8a8_blk128(Xq, Xs, W, S, out_dtype=torch.bfloat16, Y=None):
     """Y[M,N] = sum over 128-K blocks of Xs[m, kb] * S[n/128, kb] * e4m3(Xq) . e4m3(W)^T.
-    Xq [M, K] and W [N, K] E4M3, Xs [M, ceil(K/128)] and S [ceil(N/128), ceil(K/128)] fp32."""
+    Xq [M, K] and W [N, K] E4M3, Xs [M, ceil(K/128)] and S [ceil(N/128), ceil(K/128)] fp32.
+    Slices of a batch's tokens do: scales that start off a multiple of 16 bytes are copied first."""
     dev = _device(Xq, "Xq")
     M, K = Xq.shape
     N = W.shape[0]
@@ -372,7 +384,11 @@ def qmm_fp8a8_blk128(Xq, Xs, W, S, out_dtype=torch.bfloat16, Y=None):
         Y = torch.empty((M, N), dtype=out_dtype, device=Xq.device)
     elif not _ok(Y, (out_dtype,), (M, N), dev):
         _need(Y, "Y", (out_dtype,), (M, N))
-    st = lib().qmm_fp8a8_blk128(Xq.data_ptr(), Xs.data_ptr(), M, K, N, W.data_ptr(), S.data_ptr(), Y.data_ptr(),
+    xs, s = Xs.data_ptr(), S.data_ptr()
+    if (xs | s) & 15:
+        Xs, S = _aligned(Xs), _aligned(S)
+        xs, s = Xs.data_ptr(), S.data_ptr()
+    st = lib().qmm_fp8a8_blk128(Xq.data_ptr(), xs, M, K, N, W.data_ptr(), s, Y.data_ptr(),
                                 _DTYPE[out_dtype], _raw_stream(dev))
     if st:
         _check("qmm_fp8a8_blk128", st)
@@ -381,8 +397,8 @@ def qmm_fp8a8_blk128(Xq, Xs, W, S, out_dtype=torch.bfloat16, Y=None):
 
 def qmm_fp8a8_swiglu_blk128(Xq, Xs, Wgu, Sgu, Hq=None, Hs=None):
     """H = silu(X . Wg^T) * (X . Wu^T) as E4M3 codes Hq [M, F] with one fp32 scale per
-    128 columns Hs [M, F/128].  Xq, Xs as in qmm_fp8a8_blk128; Wgu [2F, K] E4M3 (gate
-    rows first), Sgu [2F/128, ceil(K/128)] fp32."""
+    128 columns Hs [M, F/128].  Xq, Xs as in qmm_fp8a8_blk128, slices too; Wgu [2F, K] E4M3
+    (gate rows first), Sgu [2F/128, ceil(K/128)] fp32."""
     dev = _device(Xq, "Xq")
     M, K = Xq.shape
     F = Wgu.shape[0] // 2
@@ -398,10 +414,15 @@ def qmm_fp8a8_swiglu_blk128(Xq, Xs, Wgu, Sgu, Hq=None, Hs=None):
         Hs = torch.empty((M, F // 128), dtype=torch.float32, device=Xq.device)
     elif not _ok(Hs, _F32, (M, F // 128), dev):
         _need(Hs, "Hs", _F32, (M, F // 128))
-    st = lib().qmm_fp8a8_swiglu_blk128(Xq.data_ptr(), Xs.data_ptr(), M, K, F, Wgu.data_ptr(), Sgu.data_ptr(),
-                                       Hq.data_ptr(), Hs.data_ptr(), _raw_stream(dev))
+    xs, s, hs, scales = Xs.data_ptr(), Sgu.data_ptr(), Hs.data_ptr(), None
+    if (xs | s | hs) & 15:
+        Xs, Sgu, scales = _aligned(Xs), _aligned(Sgu), _aligned(Hs)
+        xs, s, hs = Xs.data_ptr(), Sgu.data_ptr(), scales.data_ptr()
+    st = lib().qmm_fp8a8_swiglu_blk128(Xq.data_ptr(), xs, M, K, F, Wgu.data_ptr(), s, Hq.data_ptr(), hs, _raw_stream(dev))
     if st:
         _check("qmm_fp8a8_swiglu_blk128", st)
+    if scales is not None and scales is not Hs:
+        Hs.copy_(scales)
     return Hq, Hs
 
 
