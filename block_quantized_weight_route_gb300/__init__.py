@@ -124,7 +124,7 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-_current_device = torch._C._cuda_getDevice
+_current_device = getattr(torch._C, "_cuda_getDevice", None)   # (None: a torch without CUDA, which has no CUDA tensors)
 
 
 def _device(t: torch.Tensor, name: str) -> int:
@@ -162,7 +162,8 @@ def _stream(device) -> ctypes.c_void_p:
 
 
 def qmm_check_status(device=None) -> None:
-    """Synchronise the current stream and raise if a kernel wait timed out."""
+    """Synchronise the current stream (of the current device, which `device` may name)
+    and raise if a kernel wait timed out."""
     _check("qmm_check_status", lib().qmm_check_status(_stream(device)))
 
 
@@ -263,7 +264,7 @@ def _ok(t, dtypes, shape, dev: int) -> bool:
 
 
 # The current stream's handle of a device index, without making a Stream object.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _aligned(t: torch.Tensor) -> torch.Tensor:

@@ -4,6 +4,10 @@ without storage, on devices that need not be there).
 The library launches on the current device, with the tilings and the error word of that
 device: with operands elsewhere it would hand one GPU the addresses of another.
 """
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
@@ -86,3 +90,17 @@ def test_a_stream_of_another_device(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream)
     with pytest.raises(ValueError, match="current device is cuda:0"):
         q._stream(torch.device("cuda", 1))
+
+
+def test_import_with_a_torch_without_cuda():
+    """The package is imported (to build, to ask for sizes) where torch has no CUDA."""
+    program = ("import torch\n"
+               "for n in ('_cuda_getDevice', '_cuda_getCurrentRawStream'):\n"
+               "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+               "import block_quantized_weight_route_gb300 as q\n"
+               "try: q.qmm_fp8a8_blk128(torch.zeros(1, 16), None, None, None)\n"
+               "except TypeError as e: assert 'CUDA tensor' in str(e)\n"
+               "else: raise AssertionError\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", program], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
