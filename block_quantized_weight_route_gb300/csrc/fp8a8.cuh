@@ -1,5 +1,5 @@
-// Pieces shared by the FP8 x FP8 kernels: the E4M3 MMA, pair copies, packed fp32
-// arithmetic, output stores and the SwiGLU.
+// Pieces shared by the FP8 x FP8 kernels: the E4M3 MMA, pair copies, TMEM loads, the
+// SwiGLU and the output stores.  (Packed fp32 arithmetic: quant8.cuh.)
 #pragma once
 #include "ptx.cuh"
 #include "qmm_internal.h"
@@ -27,7 +27,7 @@ __device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t a_desc,
 // this thread's TMEM reads (complete at tcgen05.wait::ld, ordered by
 // tcgen05.fence::before_thread_sync).  No shared or global memory is handed over,
 // so the release is at CTA scope: a cluster-scope release took about 1200 cycles
-// per hand-over (2048 x 5120 x 5120: 128 us with it, 70 us without).
+// per hand-over (it made the kernel 1.8 times as slow at 2048 x 5120 x 5120).
 // crank: this CTA's rank; the even CTA arrives without the detour over the cluster.
 __device__ __forceinline__ void mbar_arrive_even(uint64_t* bar, int crank) {
     asm volatile(
@@ -213,8 +213,8 @@ __device__ __forceinline__ void flush_ragged(const Fp8a8Params& p, const uint8_t
 
 // A warp's 32 rows x 64 columns (lane = row, `v` its 64 consecutive outputs, two per element) to Y
 // at (row0, col), through the warp's staging, so that a store instruction writes runs of 128
-// bytes.  Runs of 32 (with 2 KB of staging) took 46 us instead of 35 at 5268 x 1024 x 5120,
-// single elements in ragged rows 262 instead of 50 at 5268 x 1024 x 5119 (there a run's two
+// bytes.  Runs of 32 (with 2 KB of staging) took 46 us instead of 34 at 5268 x 1024 x 5120,
+// single elements in ragged rows 262 instead of 49 at 5268 x 1024 x 5119 (there a run's two
 // ends are sectors written in part).  Ragged rows are copied UNROLL at a time, what the
 // kernel's registers allow.
 template <bool BF16, bool RAGGED, int UNROLL>

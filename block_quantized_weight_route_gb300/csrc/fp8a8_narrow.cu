@@ -16,10 +16,10 @@
 // swapped, every fold thread reads every token's scale from shared memory, 512 cycles a
 // K block for 128 tokens; with a token per lane it reads one.
 // What bounds it: with a few tokens the weights' way from HBM once it flows (gate/up of one
-// token, 178 MB: 29 us, 6.1 TB/s = 0.90 of a plain copy) and, for a single small matrix, the
-// launch and the cluster's sum (5120 x 5120, 26 MB: 6.6 us, 4.0 TB/s); at 128 tokens a tile
-// shared memory (32 KB written and read a K block, 0.27 of the 0.30 us it takes; 300 x 5120 x
-// 5120: 17.2 us).
+// token, 178 MB: 28.4 us, 6.3 TB/s = 0.93 of a plain copy; of 64 33.4 us, of 100 34.4) and, for a
+// single small matrix, the launch and the cluster's sum (5120 x 5120, 26 MB: 7.2 us,
+// 3.6 TB/s; 6.0 where the weights are in L2); at 128 tokens a tile shared memory (32 KB
+// written and read a K block, 0.27 of the 0.30 us it takes; 300 x 5120 x 5120: 16.7 us).
 #include "fp8a8.cuh"
 
 namespace qmm {
@@ -32,7 +32,7 @@ struct NarrowCfg {
     static constexpr int W_BYTES = MATS * 128 * 128, X_BYTES = TN * 128, STAGE_BYTES = W_BYTES + X_BYTES;
     // Two CTAs on an SM where a stage (and a fold thread) is small: one's start and end run beside the other's
     // stream, and a product of few tiles is split over more CTAs (one token, 5120 x 5120:
-    // 6.7 us over 240 CTAs, 7.5 over 120, 7.9 with one CTA of twice the stages)
+    // 7.2 us over 240 CTAs, 8.0 over 120; one CTA with twice the stages 5% slower still)
     static constexpr int PER_SM = TN * MATS <= 32 ? 2 : 1;
     static constexpr int STAGES = (PER_SM == 2 ? 106496 : 196608) / STAGE_BYTES;
     static constexpr int ACC_COLS = TN * MATS;
@@ -491,7 +491,8 @@ cudaError_t clusters_at_once(int cs, int dev, int* clusters) {
         e = cudaOccupancyMaxActiveClusters(&n, fp8a8_narrow_kernel<C>, &cfg);
         if (e != cudaSuccess) return e;
         // (the query counts one CTA per SM for a kernel that allocates TMEM; two whose shared
-        // memory, registers and TMEM fit do run side by side)
+        // memory, registers and TMEM fit do run side by side: one token, 5120 x 5120, takes 7.2 us
+        // over 240 CTAs, and 12.9 over 280, where a second wave begins)
         at_once[cs].set(dev, n * C::PER_SM);
     }
     *clusters = at_once[cs].get(dev);

@@ -19,9 +19,9 @@
 // buffer's MMA (512 cycles at BN = 256), so the length of the fold's path counts, not its
 // throughput.  BN = 128 has four buffers and is bound by shared memory (48 KB written and
 // read a K block, 470 cycles).  Per K block: 0.42 us at BN = 256, 0.375 at 192, 0.245 at 128.
-// Measured: 2048 x 5120 x 5120 48.5 us (2.21 PFLOP/s; the last 256 columns in the narrow
-// kernel), 5268 x 17408 x 5120 348 us (2.70 PFLOP/s; 399 us in a row of calls that meets the
-// power limit), gate/up 2048 x 5120 x 2 x 17408 286 us (2.56 PFLOP/s; 309 in a row).
+// Measured: 2048 x 5120 x 5120 49 us (2.19 PFLOP/s; the last 256 columns in the narrow
+// kernel), 5268 x 17408 x 5120 354 us (2.65 PFLOP/s; 390 us in a row of calls that meets the
+// power limit), gate/up 2048 x 5120 x 2 x 17408 290 us (2.52 PFLOP/s; 310 in a row).
 // Next to that way the fold's instructions count: 112 a K block and fold warp (gate/up 137),
 // 32 of them the packed FMAs; a spill in the K loop costs 20 to 40%.
 // Not kept: three buffers of 160 columns with 20 fold warps, halves of the tile with MMAs
@@ -49,7 +49,7 @@ struct PairCfg {
     static constexpr int NBUF = BN <= 128 ? 4 : 2, BUF_COLS = 512 / NBUF;
     // Ring of scales: slots of SC_KB K blocks, which is also how many the fold loop unrolls: the
     // loop's end moves sums between registers (131 instructions a K block unrolled by four,
-    // 112 by eight; 362 and 348 us at 5268 x 17408 x 5120).  Gate/up unrolled by eight spills.
+    // 112 by eight; 4% slower at 5268 x 17408 x 5120).  Gate/up unrolled by eight spills.
     static constexpr int SC_KB = GATED ? 4 : 8, SC_SLOTS = 16 / SC_KB;
     static constexpr int SC_PITCH = 128 + 4;                      // per K block: the rows' scales, the two blocks'
     static constexpr int SC_FLOATS = SC_SLOTS * SC_KB * SC_PITCH;
@@ -57,7 +57,7 @@ struct PairCfg {
     // where the registers hold them (8 fold warps: all 64 columns at once, 37 us against 45
     // with loads of 32 at 256 x 17408 x 5120; 12 warps: 32); 16 warps need more than an even
     // share of the registers for their sums (a register split) and loads of 8 (gate/up with
-    // loads of 16: 330 us against 287 at 2048 x 5120 x 2 x 17408).
+    // loads of 16: 15% slower at 2048 x 5120 x 2 x 17408).
     static constexpr int CW = 64, GROUPS = BN / CW, FOLD_WARPS = 4 * GROUPS, LW = BN == 256 ? 8 : BN == 192 ? 32 : 64;
     static constexpr int OUT_BYTES = GATED ? 2 * GROUPS * 128 * 4 : FOLD_WARPS * STAGING;   // row maxima, or output staging
     static constexpr bool REG_SPLIT = BN == 256;

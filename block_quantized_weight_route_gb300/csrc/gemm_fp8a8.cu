@@ -26,9 +26,11 @@ double pair_time(long tiles, long pairs, int i, int kbs) {
 // for the operands' way through L2, which tells tilings of equal waves apart:
 //   narrow kernel, 128 weight rows x tn tokens, K over cs CTAs
 //   pair kernel, 256 tokens x bn columns, one pair per two SMs
-// Measured at 5120 x 5120: 128 tokens narrow 128/3 10.5 us, pair 13.9; 300 tokens narrow
-// 128/1 16.8, pair (192 columns) 18.7; 600 tokens 32.9 and 21.5; 1 token narrow 16/6 6.5,
-// 16/3 7.5, 16/7 (more CTAs than fit at once) 11.3; at 2000 x 1000, 128 tokens 32/4 6.4, 128/8 8.5.
+// Measured at 5120 x 5120: 128 tokens narrow 128/3 11.1 us, pair (128 columns) 13.4; 300 tokens
+// narrow 128/1 16.7, pair (192) 18.6; 600 tokens 32.4 and (256) 21.4; 1 token narrow 16/6 7.2,
+// 16/3 8.0, 16/7 (more CTAs than fit at once) 12.9; at K = 2000, N = 1000, 128 tokens 32/4 6.2,
+// 128/8 7.1, pair (128) 7.9; gate/up at 5120 x 17408, 100 tokens narrow 128/1 34.4, 64/1 61, pair 42;
+// 300 tokens 94, 147 and 80.
 // (A tiling that cannot be asked about is an error, not one tiling less.)
 cudaError_t one_launch(int M, int kbs, int cols, bool gated, int sms, int dev, Fp8a8Plan* best, double* time) {
     *best = Fp8a8Plan{};

@@ -9,8 +9,8 @@
 // takes one row, or, for rows of at most 1024 values, each warp one.  16 (or 4)
 // consecutive lanes hold one group, whose maximum is a few shuffles.
 // Measured: 21504 x 2560, fp32 rows and residual, bf16 rows out beside the codes (830 MB)
-// 118 us = 7.0 TB/s; all bf16 56 us = 6.9 TB/s; 2048 x 5120 bf16 (74 MB) 14.0 us = 5.3 TB/s;
-// 5268 x 2048, fp32 rows, bf16 residual, q8_1 (98 MB) 17.6 us = 5.6 TB/s; one row 2.2 us,
+// 118 us = 7.0 TB/s; all bf16 56 us = 7.0 TB/s; 2048 x 5120 bf16 (74 MB) 13.7 us = 5.4 TB/s;
+// 5268 x 2048, fp32 rows, bf16 residual, q8_1 (98 MB) 17.4 us = 5.7 TB/s; one row 2 us,
 // the launch.  Not kept: a persistent grid that loads the next row ahead (slower).
 #include "qmm_internal.h"
 #include "quant8.cuh"

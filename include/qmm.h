@@ -141,7 +141,11 @@ qmm_status qmm_q8_0_q8_1(const int8_t *Xq, const uint16_t *Xd, int M, int K, int
  *          Q = E4M3(y / S), to nearest even;  Q [T][D], S [T][ceil(D/128)] fp32;
  *   _q8_1: per 32 columns: d = max|y| / 127, Yq = round-half-away(y / d) in
  *          [-127, 127], Yd = fp16(d), Ys = fp16(d * sum Yq);  Yq [T][D], Yd / Ys [T][D/32].
- *   A group of zeros has scale 0 and codes 0; a NaN in a row makes its Q NaN.
+ *   A quotient y / S is a product with S's reciprocal, within 3 ulp: a code differs from a
+ *   division's where the quotient lies that close to a rounding boundary.
+ *   A group of zeros has scale 0 and codes 0.  A NaN in a row makes its Q NaN (_q8_1, whose
+ *   codes have no NaN: its Yd and Ys); an infinity does so for its group and leaves the rest
+ *   of the row 0.  A finite row whose sum of squares passes fp32's range comes out as zeros.
  *   Y (or NULL): the rows y as well, bf16 (RNE) [T][D], for a product that takes bf16.
  *   X [T] rows of ldx elements, R / Rout (both NULL: no residual) of ldr / ldro,
  *   G [D]; each fp32 or bf16 (rdt is the type of R and Rout).  Rout may be R (or

@@ -69,3 +69,20 @@ def test_nothing_beside_the_rows(q, D):
             assert bool((w[:T, D:] == 7).all()) and bool((w[T] == 7).all())
         assert bool((Q[T] == 7).all()) and bool((S[T] == 7).all())
         assert torch.equal(wide["X"][:T, :D], X) and torch.equal(wide["R"][:T, :D], R)
+
+
+def test_q8_1_nan_and_infinity_show_in_the_scales(q):
+    """int8 has no NaN: a block that a NaN or an infinity reaches has a NaN d and s."""
+    X = t.rows(5, 6, 384, BF16).contiguous()
+    G = torch.ones(384, device="cuda")
+    clean = q.qmm_add_rmsnorm_q8_1(X, G)
+    Z = X.clone()
+    Z[1, 200] = float("nan")
+    Z[4, 7] = float("inf")
+    out = q.qmm_add_rmsnorm_q8_1(Z, G, bf16_out=True)
+    d, s = (out[k].view(torch.float16) for k in ("Yd", "Ys"))
+    assert torch.isnan(d[1]).all() and torch.isnan(s[1]).all() and torch.isnan(out["Y"][1]).all()
+    # inf / inf in its own block; v / inf = 0 in the others
+    assert torch.isnan(d[4, 0]) and torch.isnan(s[4, 0]) and not d[4, 1:].any() and not out["Yq"][4, 32:].any()
+    for r in (0, 2, 3, 5):
+        assert all(torch.equal(out[k][r], clean[k][r]) for k in ("Yq", "Yd", "Ys"))
