@@ -103,6 +103,18 @@ def lib() -> ctypes.CDLL:
         L.qmm_fp8a8_blk128.argtypes = [P, P, i32, i32, i32, P, P, P, i32, P]
         L.qmm_fp8a8_swiglu_blk128.restype = i32
         L.qmm_fp8a8_swiglu_blk128.argtypes = [P, P, i32, i32, i32, P, P, P, P, P]
+        L.qmm_fp8a8_epilogue_blk128.restype = i32
+        L.qmm_fp8a8_epilogue_blk128.argtypes = [P, P, i32, i32, i32, P, P, P, i32, i32, P, i64, i32, P, i32, P]
+        L.moe_route_scored.restype = i32
+        L.moe_route_scored.argtypes = [P, i32, i64, P, P, i32, i32, i32, i32, i32, i32, i32, i32, f32, P, P, P]
+        L.moe_expert_stage_fp8_workspace_size.restype = sz
+        L.moe_expert_stage_fp8_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+        L.moe_expert_stage_fp8_workspace_layout.restype = i32
+        L.moe_expert_stage_fp8_workspace_layout.argtypes = [i32, i32, i32, i32, i32, P]
+        L.moe_expert_stage_fp8.restype = i32
+        L.moe_expert_stage_fp8.argtypes = [P, P, P, P, i32, i32, i32, i32, i32, P, P, P, P, P, i64, i32, P, i32, P, sz, P]
+        L.qmm_dbg_fp8a8_epilogue_blk128.restype = i32
+        L.qmm_dbg_fp8a8_epilogue_blk128.argtypes = [P, P, i32, i32, i32, P, P, P, i32, i32, P, i64, i32, P, i32, P, P]
         L.qmm_dbg_fp8a8_plan.restype = i32
         L.qmm_dbg_fp8a8_plan.argtypes = [i32, i32, i32, i32, P]
         L.qmm_dbg_fp8a8_blk128.restype = i32
@@ -427,6 +439,169 @@ def qmm_fp8a8_swiglu_blk128(Xq, Xs, Wgu, Sgu, Hq=None, Hs=None):
     return Hq, Hs
 
 
+QMM_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def _epilogue_args(Xq, Xs, W, S, bias, act, R, out_dtype, Y, dev):
+    """Checked arguments of the product with an epilogue: (Y, the call's arguments up to the stream)."""
+    M, K = Xq.shape
+    N = W.shape[0]
+    if out_dtype not in _DTYPE:
+        raise TypeError("out_dtype must be float32 or bfloat16")
+    if act not in QMM_ACTS:
+        raise ValueError(f"act must be one of {tuple(QMM_ACTS)}, got {act!r}")
+    kb = (K + 127) // 128
+    if not (_ok(Xq, _F8, Xq.shape, dev) and _ok(Xs, _F32, (M, kb), dev) and _ok(W, _F8, (N, K), dev) and
+            _ok(S, _F32, ((N + 127) // 128, kb), dev)):
+        _need_operands(Xq, Xs, W, S, M, K, N, (N + 127) // 128, "W", "S")
+    b, bdt = None, 0
+    if bias is not None:
+        if not _ok(bias, _DTYPE, (N,), dev):
+            _need(bias, "bias", tuple(_DTYPE), (N,))
+        bias = _aligned(bias)
+        b, bdt = bias.data_ptr(), _DTYPE[bias.dtype]
+    r, ldr, rdt = None, 0, 0
+    if R is not None:
+        ldr = _pitch(R, "R", (M, N), dev)
+        r, rdt = R.data_ptr(), _DTYPE[R.dtype]
+        if r & 15 and R is not Y:
+            R = R.contiguous().clone()
+            r, ldr = R.data_ptr(), N
+    if Y is None:
+        Y = torch.empty((M, N), dtype=out_dtype, device=Xq.device)
+    elif not _ok(Y, (out_dtype,), (M, N), dev):
+        _need(Y, "Y", (out_dtype,), (M, N))
+    Xs, S = _aligned(Xs), _aligned(S)
+    # (the tensors behind copies are kept until the call is made)
+    return Y, (bias, Xs, S, R), (Xq.data_ptr(), Xs.data_ptr(), M, K, N, W.data_ptr(), S.data_ptr(), b, bdt, QMM_ACTS[act], r, ldr,
+                              rdt, Y.data_ptr(), _DTYPE[out_dtype])
+
+
+def qmm_fp8a8_epilogue_blk128(Xq, Xs, W, S, bias=None, act: str = "none", R=None, out_dtype=torch.bfloat16, Y=None):
+    """Y[M,N] = act(P + bias) + R, P the product of qmm_fp8a8_blk128 (its arguments as there).
+    bias [N] and R [M, N] fp32 or bf16; R may be a row slice, or Y itself (the residual in
+    place); act: "none", "relu", "silu", "gelu" (erf) or "gelu_tanh"."""
+    dev = _device(Xq, "Xq")
+    Y, keep, args = _epilogue_args(Xq, Xs, W, S, bias, act, R, out_dtype, Y, dev)
+    st = lib().qmm_fp8a8_epilogue_blk128(*args, _raw_stream(dev))
+    if st:
+        _check("qmm_fp8a8_epilogue_blk128", st)
+    return Y
+
+
+QMM_SCORES = {"softmax": 0, "sigmoid": 1}
+_I32 = (torch.int32,)
+
+
+def moe_route_scored(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, groups_kept: int = 1,
+                     group_top: int = 2, renorm: bool = True, scale: float = 1.0, live=None, ids=None, w=None):
+    """Routing by scores: softmax or sigmoid of logits [T, E] (fp32 or bf16, row slices too), the k
+    largest of score + bias (bias [E] fp32) in the groups_kept best of `groups` groups (by the
+    sum of a group's group_top largest), weights the scores themselves, renormalised over
+    the k (renorm) and times scale.  live (int32, one element): tokens from it on are padding
+    and get ids -1, weights 0.  Returns (ids int32 [T, k], w fp32 [T, k])."""
+    dev = _device(logits, "logits")
+    T, E = logits.shape
+    ldl = _pitch(logits, "logits", (T, E), dev)
+    if score not in QMM_SCORES:
+        raise ValueError(f"score must be one of {tuple(QMM_SCORES)}, got {score!r}")
+    if bias is not None:
+        if not _ok(bias, _F32, (E,), dev):
+            _need(bias, "bias", _F32, (E,))
+        bias = _aligned(bias)
+    if live is not None:
+        _need(live, "live", _I32)
+        if live.numel() != 1:
+            raise ValueError("live must have one element")
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    elif not _ok(ids, _I32, (T, k), dev):
+        _need(ids, "ids", _I32, (T, k))
+    if w is None:
+        w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    elif not _ok(w, _F32, (T, k), dev):
+        _need(w, "w", _F32, (T, k))
+    if logits.data_ptr() & 15:
+        logits = logits.contiguous().clone()
+        ldl = E
+    at, copies = (ids.data_ptr(), w.data_ptr()), None
+    if (at[0] | at[1]) & 15:   # row slices: written to copies first
+        copies = _aligned(ids), _aligned(w)
+        at = copies[0].data_ptr(), copies[1].data_ptr()
+    st = lib().moe_route_scored(logits.data_ptr(), _DTYPE[logits.dtype], ldl, None if bias is None else bias.data_ptr(),
+                                None if live is None else live.data_ptr(), T, E, k, QMM_SCORES[score], groups, groups_kept,
+                                group_top, 1 if renorm else 0, scale, *at, _raw_stream(dev))
+    if st:
+        _check("moe_route_scored", st)
+    if copies is not None:
+        for out, copy in zip((ids, w), copies):
+            if copy is not out:
+                out.copy_(copy)
+    return ids, w
+
+
+def moe_expert_stage_fp8_workspace_size(T: int, D: int, F: int, E: int, k: int) -> int:
+    """(0 for a shape that the stage does not take.)"""
+    return int(lib().moe_expert_stage_fp8_workspace_size(T, D, F, E, k))
+
+
+MOE_FP8_WS_FIELDS = ("counts", "offsets", "src", "row", "chunk_counts", "tiles", "tile_count", "Xp", "Xps", "Hq", "Hs", "y",
+                     "total")
+
+
+def moe_expert_stage_fp8_workspace_layout(T: int, D: int, F: int, E: int, k: int) -> dict:
+    """Byte offsets of the workspace's regions (see workspace_view)."""
+    arr = (ctypes.c_size_t * len(MOE_FP8_WS_FIELDS))()
+    _check("moe_expert_stage_fp8_workspace_layout",
+           lib().moe_expert_stage_fp8_workspace_layout(T, D, F, E, k, ctypes.cast(arr, ctypes.c_void_p)))
+    return dict(zip(MOE_FP8_WS_FIELDS, [int(v) for v in arr]))
+
+
+def moe_expert_stage_fp8(Xq, Xs, ids, w, Wgu, Sgu, Wd, Sd, R=None, out_dtype=torch.bfloat16, Y=None, ws=None):
+    """The routed expert stage over FP8 weights: Y[t] = R[t] + sum_j w[t,j] * Wd[e] . fp8(silu(g) * u),
+    e = ids[t, j] (outside [0, E): nothing), g and u the gate and up rows of Wgu[e] times X[t].
+    Xq [T, D] E4M3 and Xs [T, ceil(D/128)] fp32 (as qmm_add_rmsnorm_fp8 gives them), ids int32 and
+    w fp32 [T, k] (as moe_route_scored gives them), Wgu [E, 2F, D] (gate rows first) with Sgu [E, 2F/128,
+    ceil(D/128)], Wd [E, D, F] with Sd [E, ceil(D/128), F/128], R [T, D] fp32 or bf16 (a row slice,
+    or Y itself).  ws: a uint8 tensor of moe_expert_stage_fp8_workspace_size bytes (default: allocated)."""
+    dev = _device(Xq, "Xq")
+    T, D = Xq.shape
+    k = ids.shape[1]
+    E, F2 = Wgu.shape[0], Wgu.shape[1]
+    F = F2 // 2
+    kb = (D + 127) // 128
+    if out_dtype not in _DTYPE:
+        raise TypeError("out_dtype must be float32 or bfloat16")
+    for t, name, dtypes, shape in ((Xq, "Xq", _F8, (T, D)), (Xs, "Xs", _F32, (T, kb)), (ids, "ids", _I32, (T, k)),
+                                   (w, "w", _F32, (T, k)), (Wgu, "Wgu", _F8, (E, 2 * F, D)),
+                                   (Sgu, "Sgu", _F32, (E, 2 * F // 128, kb)), (Wd, "Wd", _F8, (E, D, F)),
+                                   (Sd, "Sd", _F32, (E, kb, F // 128))):
+        if not _ok(t, dtypes, shape, dev):
+            _need(t, name, dtypes, shape)
+    r, ldr, rdt = None, 0, 0
+    if R is not None:
+        ldr = _pitch(R, "R", (T, D), dev)
+        r, rdt = R.data_ptr(), _DTYPE[R.dtype]
+        if (r & 15 or ldr & 3) and R is not Y:
+            R = R.contiguous().clone()
+            r, ldr = R.data_ptr(), D
+    if Y is None:
+        Y = torch.empty((T, D), dtype=out_dtype, device=Xq.device)
+    elif not _ok(Y, (out_dtype,), (T, D), dev):
+        _need(Y, "Y", (out_dtype,), (T, D))
+    if ws is None:
+        ws = torch.empty(max(moe_expert_stage_fp8_workspace_size(T, D, F, E, k), 256), dtype=torch.uint8, device=Xq.device)
+    elif not _ok(ws, _U8, (ws.numel(),), dev):
+        _need(ws, "ws", _U8, (ws.numel(),))
+    Xs, Sgu, Sd, ids, w = _aligned(Xs), _aligned(Sgu), _aligned(Sd), _aligned(ids), _aligned(w)
+    st = lib().moe_expert_stage_fp8(Xq.data_ptr(), Xs.data_ptr(), ids.data_ptr(), w.data_ptr(), T, D, F, E, k, Wgu.data_ptr(),
+                                    Sgu.data_ptr(), Wd.data_ptr(), Sd.data_ptr(), r, ldr, rdt, Y.data_ptr(),
+                                    _DTYPE[out_dtype], ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    if st:
+        _check("moe_expert_stage_fp8", st)
+    return Y
+
+
 def moe_route_workspace_size(T: int, E: int, k: int) -> int:
     return int(lib().moe_route_workspace_size(T, E, k))
 
@@ -643,6 +818,14 @@ def qmm_dbg_fp8a8_blk128(Xq, Xs, W, S, plan, out_dtype=torch.bfloat16, Y=None):
     _check("qmm_dbg_fp8a8_blk128",
            lib().qmm_dbg_fp8a8_blk128(_ptr(Xq), _ptr(Xs), M, K, N, _ptr(W), _ptr(S), _ptr(Y), _DTYPE[out_dtype],
                                       ctypes.cast(_plan_array(plan), ctypes.c_void_p), _stream(Xq.device)))
+    return Y
+
+
+def qmm_dbg_fp8a8_epilogue_blk128(Xq, Xs, W, S, plan, bias=None, act: str = "none", R=None, out_dtype=torch.bfloat16, Y=None):
+    """qmm_fp8a8_epilogue_blk128 by a given tiling."""
+    Y, keep, args = _epilogue_args(Xq, Xs, W, S, bias, act, R, out_dtype, Y, _device(Xq, "Xq"))
+    _check("qmm_dbg_fp8a8_epilogue_blk128",
+           lib().qmm_dbg_fp8a8_epilogue_blk128(*args, ctypes.cast(_plan_array(plan), ctypes.c_void_p), _stream(Xq.device)))
     return Y
 
 

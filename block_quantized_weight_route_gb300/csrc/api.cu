@@ -955,9 +955,20 @@ static qmm_status run_fp8a8(const char* who, DeviceState* d, Fp8a8Params& p, boo
     return QMM_OK;
 }
 
+// What the product's epilogue adds.
+struct Epilogue {
+    const void* bias;
+    qmm_dtype bdt;
+    qmm_act act;
+    const void* R;
+    int64_t ldr;
+    qmm_dtype rdt;
+};
+
 // The two products, by the tiling of the rule or (fields) a given one.
 static qmm_status fp8a8_product(const char* who, const uint8_t* Xq, const float* Xs, int M, int K, int N, const uint8_t* W,
-                                const float* S, void* Y, qmm_dtype ydt, const int* fields, cudaStream_t stream) {
+                                const float* S, const Epilogue* epi, void* Y, qmm_dtype ydt, const int* fields,
+                                cudaStream_t stream) {
     if (M < 0 || K < 16 || K % 16 || N < 1 || M > kMostRows || K > kMostRows || N > kMostRows)
         return fail(QMM_ERR_UNSUPPORTED_SHAPE, "%s: need M >= 0, K %% 16 == 0, N >= 1, each <= 2^31 - 512 (M=%d K=%d N=%d)",
                     who, M, K, N);
@@ -967,6 +978,16 @@ static qmm_status fp8a8_product(const char* who, const uint8_t* Xq, const float*
         return fail(QMM_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned", who);
     if (fields && !fp8a8_plans_fit(plans_of(fields), M, K, N, false))
         return fail(QMM_ERR_INVALID_ARG, "%s: no such tiling of this shape", who);
+    if (epi) {
+        if ((epi->bias && !is_dtype(epi->bdt)) || (epi->R && !is_dtype(epi->rdt)) || epi->act < QMM_ACT_NONE ||
+            epi->act > QMM_ACT_GELU_TANH)
+            return fail(QMM_ERR_INVALID_ARG, "%s: bad type or activation", who);
+        if (!aligned16(epi->bias) || !aligned16(epi->R))
+            return fail(QMM_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned", who);
+        if (epi->R && epi->ldr < N) return fail(QMM_ERR_INVALID_ARG, "%s: R's row pitch must be at least N", who);
+        if (epi->R && epi->R == Y && (epi->rdt != ydt || (M > 1 && epi->ldr != N)))
+            return fail(QMM_ERR_INVALID_ARG, "%s: in place, R must have Y's type and pitch", who);
+    }
     DeviceState* d = nullptr;
     qmm_status st = device_state(&d);
     if (st != QMM_OK || M == 0) return st;
@@ -980,6 +1001,16 @@ static qmm_status fp8a8_product(const char* who, const uint8_t* Xq, const float*
     p.N = N;
     p.Y = Y;
     p.y_bf16 = ydt == QMM_BF16;
+    if (epi && (epi->bias || epi->act != QMM_ACT_NONE || epi->R)) {   // (nothing to add: the plain product)
+        p.epilogue = true;
+        p.act = epi->act;
+        p.bias = epi->bias;
+        p.bias_bf16 = epi->bdt == QMM_BF16;
+        p.R = epi->R;
+        p.ldr = (long)epi->ldr;
+        p.r_bf16 = epi->rdt == QMM_BF16;
+        p.vec4 = N % 4 == 0 && (!epi->R || epi->ldr % 4 == 0);
+    }
     return run_fp8a8(who, d, p, false, fields, stream);
 }
 
@@ -1011,7 +1042,14 @@ static qmm_status fp8a8_swiglu(const char* who, const uint8_t* Xq, const float* 
 
 qmm_status qmm_fp8a8_blk128(const uint8_t* Xq, const float* Xs, int M, int K, int N, const uint8_t* W, const float* S,
                             void* Y, qmm_dtype ydt, cudaStream_t stream) {
-    return fp8a8_product("qmm_fp8a8_blk128", Xq, Xs, M, K, N, W, S, Y, ydt, nullptr, stream);
+    return fp8a8_product("qmm_fp8a8_blk128", Xq, Xs, M, K, N, W, S, nullptr, Y, ydt, nullptr, stream);
+}
+
+qmm_status qmm_fp8a8_epilogue_blk128(const uint8_t* Xq, const float* Xs, int M, int K, int N, const uint8_t* W,
+                                     const float* S, const void* bias, qmm_dtype bdt, qmm_act act, const void* R,
+                                     int64_t ldr, qmm_dtype rdt, void* Y, qmm_dtype ydt, cudaStream_t stream) {
+    const Epilogue epi{bias, bdt, act, R, ldr, rdt};
+    return fp8a8_product("qmm_fp8a8_epilogue_blk128", Xq, Xs, M, K, N, W, S, &epi, Y, ydt, nullptr, stream);
 }
 
 qmm_status qmm_fp8a8_swiglu_blk128(const uint8_t* Xq, const float* Xs, int M, int K, int F, const uint8_t* Wgu,
@@ -1038,13 +1076,194 @@ qmm_status qmm_dbg_fp8a8_plan(int M, int K, int N, int gated, int* plan) {
 qmm_status qmm_dbg_fp8a8_blk128(const uint8_t* Xq, const float* Xs, int M, int K, int N, const uint8_t* W, const float* S,
                                 void* Y, qmm_dtype ydt, const int* plan, cudaStream_t stream) {
     if (!plan) return fail(QMM_ERR_INVALID_ARG, "qmm_dbg_fp8a8_blk128: null pointer");
-    return fp8a8_product("qmm_dbg_fp8a8_blk128", Xq, Xs, M, K, N, W, S, Y, ydt, plan, stream);
+    return fp8a8_product("qmm_dbg_fp8a8_blk128", Xq, Xs, M, K, N, W, S, nullptr, Y, ydt, plan, stream);
+}
+
+qmm_status qmm_dbg_fp8a8_epilogue_blk128(const uint8_t* Xq, const float* Xs, int M, int K, int N, const uint8_t* W,
+                                         const float* S, const void* bias, qmm_dtype bdt, qmm_act act, const void* R,
+                                         int64_t ldr, qmm_dtype rdt, void* Y, qmm_dtype ydt, const int* plan,
+                                         cudaStream_t stream) {
+    if (!plan) return fail(QMM_ERR_INVALID_ARG, "qmm_dbg_fp8a8_epilogue_blk128: null pointer");
+    const Epilogue epi{bias, bdt, act, R, ldr, rdt};
+    return fp8a8_product("qmm_dbg_fp8a8_epilogue_blk128", Xq, Xs, M, K, N, W, S, &epi, Y, ydt, plan, stream);
 }
 
 qmm_status qmm_dbg_fp8a8_swiglu_blk128(const uint8_t* Xq, const float* Xs, int M, int K, int F, const uint8_t* Wgu,
                                        const float* Sgu, uint8_t* Hq, float* Hs, const int* plan, cudaStream_t stream) {
     if (!plan) return fail(QMM_ERR_INVALID_ARG, "qmm_dbg_fp8a8_swiglu_blk128: null pointer");
     return fp8a8_swiglu("qmm_dbg_fp8a8_swiglu_blk128", Xq, Xs, M, K, F, Wgu, Sgu, Hq, Hs, plan, stream);
+}
+
+// ---------------------------------------------------------------- FP8 mixture of experts
+
+qmm_status moe_route_scored(const void* logits, qmm_dtype ldt, int64_t ldl, const float* bias, const int32_t* live,
+                            int T, int E, int k, qmm_score score, int groups, int groups_kept, int group_top,
+                            int renorm, float scale, int32_t* ids, float* w, cudaStream_t stream) {
+    const char* who = "moe_route_scored";
+    if (T < 0 || T > kMostRows || E < 1 || E > 512 || k < 1 || k > 16 || k > E)
+        return fail(QMM_ERR_UNSUPPORTED_SHAPE, "%s: need 0 <= T <= 2^31 - 512, 1 <= E <= 512, 1 <= k <= 16, k <= E (T=%d E=%d k=%d)", who,
+                    T, E, k);
+    if (groups < 1 || groups > 32 || E % groups || groups_kept < 1 || groups_kept > groups || k > E / groups * groups_kept ||
+        (groups > 1 && (group_top < 1 || group_top > 2 || group_top > E / groups)))
+        return fail(QMM_ERR_UNSUPPORTED_SHAPE,
+                    "%s: need 1 <= groups <= 32, E %% groups == 0, 1 <= groups_kept <= groups, k <= E / groups * groups_kept, "
+                    "group_top 1 or 2 and at most E / groups (E=%d k=%d groups=%d groups_kept=%d group_top=%d)",
+                    who, E, k, groups, groups_kept, group_top);
+    if (!is_dtype(ldt) || (score != QMM_SCORE_SOFTMAX && score != QMM_SCORE_SIGMOID))
+        return fail(QMM_ERR_INVALID_ARG, "%s: bad type or score", who);
+    if (T > 0 && (!logits || !ids || !w)) return fail(QMM_ERR_INVALID_ARG, "%s: null pointer", who);
+    if (ldl < E) return fail(QMM_ERR_INVALID_ARG, "%s: the logits' row pitch must be at least E", who);
+    if (!aligned16(logits) || !aligned16(bias) || !aligned16(ids) || !aligned16(w) || (reinterpret_cast<uintptr_t>(live) & 3u))
+        return fail(QMM_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned (live: 4-byte)", who);
+    DeviceState* d = nullptr;
+    qmm_status st = device_state(&d);
+    if (st != QMM_OK || T == 0) return st;
+    ScoredParams p{};
+    p.logits = logits;
+    p.bias = bias;
+    p.live = live;
+    p.ldl = (long)ldl;
+    p.l_bf16 = ldt == QMM_BF16;
+    p.T = T;
+    p.E = E;
+    p.k = k;
+    p.sigmoid = score == QMM_SCORE_SIGMOID;
+    p.groups = groups;
+    p.groups_kept = groups_kept;
+    p.group_top = groups > 1 ? group_top : 1;
+    p.renorm = renorm != 0;
+    p.scale = scale;
+    p.ids = ids;
+    p.w = w;
+    const cudaError_t e = launch_route_scored(p, d->sms, stream);
+    return e == cudaSuccess ? QMM_OK : cuda_fail(e, who);
+}
+
+// Smallest tile of the expert stage's kernels: what bounds the tile list's room.
+constexpr int kMoeTile = 16;
+static int moe_max_tiles(long P, int E, int tile_rows) {
+    const long full = P / tile_rows + E;   // (every expert's last tile may be short)
+    return (int)(full < P ? full : P);
+}
+
+constexpr int kMoeMostWidth = 1 << 20;   // (column tiles are a dimension of the grid)
+static bool moe_fp8_shape(int T, int D, int F, int E, int k) {
+    return T >= 0 && D >= 16 && D % 16 == 0 && F >= 128 && F % 128 == 0 && E >= 1 && E <= kMoeMaxExperts && k >= 1 && k <= 16 &&
+           (long)T * k <= 4l << 20 && (long)E * 2 * F <= kMostRows && (long)E * D <= kMostRows && D <= kMoeMostWidth && F <= kMoeMostWidth;
+}
+
+// Workspace regions of the FP8 expert stage, in the order of the QMM_MOE_FP8_WS_FIELDS list.
+static void moe_fp8_layout(int T, int D, int F, int E, int k, size_t* off) {
+    const size_t P = (size_t)T * k, kbs = (size_t)(D + 127) / 128;
+    const size_t sz[QMM_MOE_FP8_WS_FIELDS - 1] = {(size_t)E * 4, (size_t)(E + 1) * 4, P * 4, P * 4,
+                                                  (P + kMoeChunk - 1) / kMoeChunk * E * 4,
+                                                  (size_t)moe_max_tiles((long)P, E, kMoeTile) * 16, 4, P * D, P * kbs * 4, P * F,
+                                                  P * (F / 128) * 4, P * D * 4};
+    size_t o = 0;
+    for (int i = 0; i < QMM_MOE_FP8_WS_FIELDS - 1; ++i) {
+        off[i] = o;
+        o = align_up(o + sz[i], 256);
+    }
+    off[QMM_MOE_FP8_WS_FIELDS - 1] = o;
+}
+
+static qmm_status check_moe_fp8_shape(const char* who, int T, int D, int F, int E, int k) {
+    if (moe_fp8_shape(T, D, F, E, k)) return QMM_OK;
+    return fail(QMM_ERR_UNSUPPORTED_SHAPE,
+                "%s: need T >= 0, D %% 16 == 0, F %% 128 == 0, 1 <= k <= 16, 1 <= E <= 512, D and F <= 2^20, T * k <= 2^22, E * 2F and E * D <= 2^31 - 512 "
+                "(T=%d D=%d F=%d E=%d k=%d)",
+                who, T, D, F, E, k);
+}
+
+size_t moe_expert_stage_fp8_workspace_size(int T, int D, int F, int E, int k) {
+    if (!moe_fp8_shape(T, D, F, E, k)) return 0;
+    size_t off[QMM_MOE_FP8_WS_FIELDS];
+    moe_fp8_layout(T, D, F, E, k, off);
+    return off[QMM_MOE_FP8_WS_FIELDS - 1];
+}
+
+qmm_status moe_expert_stage_fp8_workspace_layout(int T, int D, int F, int E, int k, size_t* offsets_out) {
+    if (!offsets_out) return fail(QMM_ERR_INVALID_ARG, "moe_expert_stage_fp8_workspace_layout: null pointer");
+    const qmm_status st = check_moe_fp8_shape("moe_expert_stage_fp8_workspace_layout", T, D, F, E, k);
+    if (st == QMM_OK) moe_fp8_layout(T, D, F, E, k, offsets_out);
+    return st;
+}
+
+qmm_status moe_expert_stage_fp8(const uint8_t* Xq, const float* Xs, const int32_t* ids, const float* w, int T, int D,
+                                int F, int E, int k, const uint8_t* Wgu, const float* Sgu, const uint8_t* Wd,
+                                const float* Sd, const void* R, int64_t ldr, qmm_dtype rdt, void* Y, qmm_dtype ydt,
+                                void* ws, size_t ws_bytes, cudaStream_t stream) {
+    const char* who = "moe_expert_stage_fp8";
+    qmm_status st = check_moe_fp8_shape(who, T, D, F, E, k);
+    if (st != QMM_OK) return st;
+    if (!is_dtype(ydt) || (R && !is_dtype(rdt))) return fail(QMM_ERR_INVALID_ARG, "%s: bad type", who);
+    if (!Wgu || !Sgu || !Wd || !Sd || (T > 0 && (!Xq || !Xs || !ids || !w || !Y || !ws)))
+        return fail(QMM_ERR_INVALID_ARG, "%s: null pointer", who);
+    if (!aligned16(Xq) || !aligned16(Xs) || !aligned16(ids) || !aligned16(w) || !aligned16(Wgu) || !aligned16(Sgu) || !aligned16(Wd) ||
+        !aligned16(Sd) || !aligned16(R) || !aligned16(Y) || (reinterpret_cast<uintptr_t>(ws) & 255u))
+        return fail(QMM_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned (workspace 256-byte aligned)", who);
+    if (R && (ldr < D || ldr % 4)) return fail(QMM_ERR_INVALID_ARG, "%s: R's row pitch must be at least D and a multiple of 4", who);
+    if (R && R == Y && (rdt != ydt || (T > 1 && ldr != D)))
+        return fail(QMM_ERR_INVALID_ARG, "%s: in place, R must have Y's type and pitch", who);
+    size_t off[QMM_MOE_FP8_WS_FIELDS];
+    moe_fp8_layout(T, D, F, E, k, off);
+    if (T > 0 && ws_bytes < off[QMM_MOE_FP8_WS_FIELDS - 1])
+        return fail(QMM_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", who, ws_bytes, off[QMM_MOE_FP8_WS_FIELDS - 1]);
+    DeviceState* d = nullptr;
+    st = device_state(&d);
+    if (st != QMM_OK || T == 0) return st;
+
+    MoePlan plan;
+    cudaError_t e = moe_plan(T, D, F, E, k, d->index, &plan);
+    if (e != cudaSuccess) return cuda_fail(e, who);
+    const int P = T * k;
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    auto at = [&](int i) { return static_cast<void*>(base + off[i]); };
+    MoeGroups g{};
+    g.counts = static_cast<int32_t*>(at(0));
+    g.offsets = static_cast<int32_t*>(at(1));
+    g.src = static_cast<int32_t*>(at(2));
+    g.row = static_cast<int32_t*>(at(3));
+    g.chunk_counts = static_cast<int32_t*>(at(4));
+    g.tiles = static_cast<int4*>(at(5));
+    g.num_tiles = static_cast<int*>(at(6));
+    g.tile_rows = plan.tn;
+    g.max_tiles = moe_max_tiles(P, E, plan.tn);
+    uint8_t* Xp = static_cast<uint8_t*>(at(7));
+    float* Xps = static_cast<float*>(at(8));
+    uint8_t* Hq = static_cast<uint8_t*>(at(9));
+    float* Hs = static_cast<float*>(at(10));
+    float* Yslot = static_cast<float*>(at(11));
+    if ((e = launch_moe_group(ids, P, E, k, g, d->index, stream)) != cudaSuccess) return cuda_fail(e, "moe_expert_stage_fp8: grouping");
+    if ((e = launch_moe_gather(Xq, Xs, P, D, g, E, Xp, Xps, d->sms, stream)) != cudaSuccess)
+        return cuda_fail(e, "moe_expert_stage_fp8: gather");
+    for (int gated = 1; gated >= 0; --gated) {
+        Fp8a8Params p{};
+        p.Xq = gated ? Xp : Hq;
+        p.Xs = gated ? Xps : Hs;
+        p.W = gated ? Wgu : Wd;
+        p.S = gated ? Sgu : Sd;
+        p.M = P;
+        p.K = gated ? D : F;
+        p.N = gated ? F : D;
+        p.Y = Yslot;
+        p.Hq = Hq;
+        p.Hs = Hs;
+        p.err = d->err;
+        p.n_end = p.N;
+        p.tiles = g.tiles;
+        p.num_tiles = g.num_tiles;
+        p.max_tiles = g.max_tiles;
+        CUtensorMap tx, tw;
+        if ((st = make_tmap(&tx, p.Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, P, p.K, 128, plan.tn, CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK ||
+            (st = make_tmap(&tw, p.W, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, (uint64_t)E * p.N * (gated ? 2 : 1), p.K, 128, 128,
+                            CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK)
+            return st;
+        e = launch_fp8a8_narrow(tx, tw, p, gated, plan.tn, gated ? plan.cs_gate_up : plan.cs_down, d->index, stream);
+        if (e != cudaSuccess) return cuda_fail(e, gated ? "moe_expert_stage_fp8: gate/up" : "moe_expert_stage_fp8: down");
+    }
+    e = launch_moe_combine(Yslot, g.row, w, T, k, D, R, rdt == QMM_BF16, (long)ldr, Y, ydt == QMM_BF16, stream);
+    return e == cudaSuccess ? QMM_OK : cuda_fail(e, "moe_expert_stage_fp8: combine");
 }
 
 qmm_status qmm_profile_enable(int on) {

@@ -120,6 +120,40 @@ __device__ __forceinline__ float swiglu(float g, float u) {
     return __fdividef(g < 0.0f ? g * t : g, 1.0f + t) * u;
 }
 
+// The activations of the product's epilogue (qmm_act's order).  With t = exp(-|z|) <= 1, v times the logistic
+// function of z is v / (1 + t), or v t / (1 + t) for negative z: nothing overflows, and the fast
+// exponential's error falls with t.  The normal distribution's tail comes from erfc, where 1 + erf would cancel.
+__device__ __forceinline__ float activate(float v, int act) {
+    if (act == 0) return v;
+    if (act == 1) return max_nan(v, 0.0f);
+    if (act == 3) return 0.5f * v * erfcf(-0.70710678f * v);
+    const float z = act == 2 ? v : 1.5957691216f * v * fmaf(0.044715f * v, v, 1.0f);   // 2 sqrt(2 / pi) (v + 0.044715 v^3)
+    const float t = __expf(-fabsf(z));
+    return __fdividef(z < 0.0f ? v * t : v, 1.0f + t);
+}
+
+// act(y + bias) + R of row m, columns n .. n + 3 (what is past the end stays as it is).
+__device__ __forceinline__ float4 epilogue4(const Fp8a8Params& p, long m, int n, float4 y) {
+    float4 b = make_float4(0.f, 0.f, 0.f, 0.f), r = b;
+    if (p.vec4) {
+        if (n >= p.N) return y;
+        if (p.bias) b = load4(p.bias, p.bias_bf16, n);
+        if (p.R) r = load4(p.R, p.r_bf16, m * p.ldr + n);
+        return make_float4(activate(y.x + b.x, p.act) + r.x, activate(y.y + b.y, p.act) + r.y, activate(y.z + b.z, p.act) + r.z,
+                           activate(y.w + b.w, p.act) + r.w);
+    }
+    float v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (n + j < p.N) {
+            if (p.bias) v[j] += load1(p.bias, p.bias_bf16, n + j);
+            v[j] = activate(v[j], p.act);
+            if (p.R) v[j] += load1(p.R, p.r_bf16, m * p.ldr + n + j);
+        }
+    }
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+
 // The column, inside the tile, of a fold thread's column i, for column group cq:
 // consecutive columns, or (gated) half of them gate, then the same columns of up.
 template <class C>
@@ -229,6 +263,74 @@ __device__ __forceinline__ void store_columns(const Fp8a8Params& p, uint8_t* stg
         __syncwarp();
         if constexpr (RAGGED) flush_ragged<BF16, UNROLL>(p, stg, lane, row0, col + c);
         else flush_aligned(p, stg, lane, row0, col + c, BF16 ? 2 : 4);
+    }
+}
+
+// store_columns with the epilogue: 32 columns at a time as fp32 through the staging (32 rows x 128 bytes),
+// then, coalesced, the bias, the activation and the residual's rows, and the rounding.
+// VEC: eight lanes a row, four columns each, a row's eight residual loads in flight before
+// the first store (R may be Y, so the compiler would not move them past it).  Else a column a lane, a
+// row at a time.
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void store_epilogue(const Fp8a8Params& p, uint8_t* stg, int lane, long row0, int col0,
+                                               const uint64_t* v) {
+#pragma unroll
+    for (int c0 = 0; c0 < 64; c0 += 32) {
+        __syncwarp();
+        stage16<false>(stg, lane, 0, v + c0 / 2);
+        stage16<false>(stg, lane, 4, v + c0 / 2 + 8);
+        __syncwarp();
+        const int col = col0 + c0;
+        if constexpr (VEC) {
+            const int c = lane % 8, n = col + 4 * c;
+            if (n < p.N) {
+                float4 b = make_float4(0.f, 0.f, 0.f, 0.f), r[8];
+                if (p.bias) b = load4(p.bias, p.bias_bf16, n);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const long m = row0 + i * 4 + lane / 8;
+                    r[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (p.R && m < p.M) r[i] = load4(p.R, p.r_bf16, m * p.ldr + n);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int q = i * 4 + lane / 8;
+                    const long m = row0 + q;
+                    if (m < p.M) {
+                        const float4 y = *reinterpret_cast<const float4*>(stg + (q * 8 + (c ^ (q & 7))) * 16);
+                        const float o[4] = {activate(y.x + b.x, p.act) + r[i].x, activate(y.y + b.y, p.act) + r[i].y,
+                                            activate(y.z + b.z, p.act) + r[i].z, activate(y.w + b.w, p.act) + r[i].w};
+                        if constexpr (BF16) {
+                            const __nv_bfloat162 lo = __floats2bfloat162_rn(o[0], o[1]), hi = __floats2bfloat162_rn(o[2], o[3]);
+                            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.Y) + m * p.N + n) =
+                                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                        } else {
+                            *reinterpret_cast<float4*>(static_cast<float*>(p.Y) + m * p.N + n) = make_float4(o[0], o[1], o[2], o[3]);
+                        }
+                    }
+                }
+            }
+        } else {
+            const int n = col + lane, rows = p.M - row0 < 32 ? (int)(p.M - row0) : 32;
+            if (n < p.N) {
+                const float b = p.bias ? load1(p.bias, p.bias_bf16, n) : 0.0f;
+                for (int q0 = 0; q0 < rows; q0 += 8) {
+                    float r[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) r[i] = p.R && q0 + i < rows ? load1(p.R, p.r_bf16, (row0 + q0 + i) * p.ldr + n) : 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int q = q0 + i;
+                        if (q < rows) {
+                            const float y = reinterpret_cast<const float*>(stg + (q * 8 + ((lane / 4) ^ (q & 7))) * 16)[lane % 4];
+                            const float o = activate(y + b, p.act) + r[i];
+                            if constexpr (BF16) static_cast<__nv_bfloat16*>(p.Y)[(row0 + q) * p.N + n] = __float2bfloat16_rn(o);
+                            else static_cast<float*>(p.Y)[(row0 + q) * p.N + n] = o;
+                        }
+                    }
+                }
+            }
+        }
     }
 }
 

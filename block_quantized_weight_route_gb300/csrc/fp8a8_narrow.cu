@@ -2,6 +2,9 @@
 //
 //   y[m][n] = sum_kb Xs[m][kb] S[n/128][kb] P_kb[m][n],   P_kb = sum_{k in kb} Xq[m][k] W[n][k]
 //   GATED: h = silu(y gate) * y up, rounded to E4M3 per 128 columns of a token
+//   EPI: y = act(y + bias[n]) + R[m][n], in the cluster's sum
+//   GROUPED: rows grouped by expert (a list of tiles {expert, first row, rows} on the device),
+//            each tile against its expert's weights
 //
 // With few tokens the weights' bytes are the work, so the operands are swapped: a CTA
 // streams 128 weight rows (GATED: 128 gate and 128 up rows) through the M side of
@@ -25,10 +28,10 @@
 namespace qmm {
 namespace {
 
-template <int TN_, bool GATED_>
+template <int TN_, bool GATED_, bool EPI_ = false, bool GROUPED_ = false>
 struct NarrowCfg {
     static constexpr int TN = TN_, MATS = GATED_ ? 2 : 1;
-    static constexpr bool GATED = GATED_, TOKENS_M = TN == 128;
+    static constexpr bool GATED = GATED_, EPI = EPI_, GROUPED = GROUPED_, TOKENS_M = TN == 128;
     static constexpr int W_BYTES = MATS * 128 * 128, X_BYTES = TN * 128, STAGE_BYTES = W_BYTES + X_BYTES;
     // Two CTAs on an SM where a stage (and a fold thread) is small: one's start and end run beside the other's
     // stream, and a product of few tiles is split over more CTAs (one token, 5120 x 5120:
@@ -257,10 +260,13 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
         tma_prefetch_desc(&tmW);
     }
     const int cs = (int)gridDim.x, rank = (int)blockIdx.x;   // one cluster per row of the grid
-    const int n0 = p.n_first + (int)blockIdx.y * 128, m0 = (int)blockIdx.z * C::TN;
+    const int n0 = p.n_first + (int)blockIdx.y * 128;
+    int m0 = (int)blockIdx.z * C::TN, m_end = p.M;
+    int w0 = n0;            // first weight row
+    long blk0 = n0 / 128;   // and weight block
     const int kbs = (p.K + 127) / 128;
     const int kb0 = (int)((long)rank * kbs / cs), kb1 = (int)((long)(rank + 1) * kbs / cs);
-    if (warp == 0) {
+    if (!C::GROUPED && warp == 0) {
         // The first stages' weights on their way to L2 while the kernel before may still run
         // (only a hint: whatever that kernel writes, the copies below read after it)
         const int kb = kb0 + lane / C::MATS, m = lane % C::MATS;
@@ -272,6 +278,18 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
     tc_fence_after();
     wait_prerequisites();
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    if constexpr (C::GROUPED) {
+        if ((int)blockIdx.z >= *p.num_tiles) {   // (the grid covers the most tiles that there can be; the same in the whole cluster)
+            __syncthreads();
+            if (warp == 1) tmem_dealloc(tmem_base, C::TMEM_COLS);
+            return;
+        }
+        const int4 tile = p.tiles[blockIdx.z];
+        m0 = tile.y;
+        m_end = tile.y + tile.z;
+        w0 += tile.x * p.N * C::MATS;
+        blk0 += (long)tile.x * ((p.N + 127) / 128) * C::MATS;
+    }
 
     if (warp >= 4) {
         if constexpr (C::REG_SPLIT) setmaxnreg_inc<C::REGS_FOLD>();
@@ -292,7 +310,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
                 if (c == 0) mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
                 __syncwarp();
                 uint8_t* dst = stage + s * C::STAGE_BYTES + c * 128 * 128;
-                if (c >= 0 && c < C::MATS) tma_load_2d(dst, &tmW, &full[s], kb * 128, c * p.N + n0);
+                if (c >= 0 && c < C::MATS) tma_load_2d(dst, &tmW, &full[s], kb * 128, c * p.N + w0);
                 else if (c == C::MATS) tma_load_2d(dst, &tmX, &full[s], kb * 128, m0);
                 __syncwarp();
                 ++issued;
@@ -352,13 +370,13 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
             // ------------------------------------------------------------ scales
             int slot = 0;
             uint32_t sph = 0;
-            const long b0 = n0 / 128, b1 = (p.N + n0) / 128;   // weight blocks (gated: gate, up)
+            const long b0 = blk0, b1 = blk0 + p.N / 128;   // weight blocks (gated: gate, up)
             for (int kb = kb0; kb < kb1; kb += C::SC_KB) {
                 if (!mbar_wait(&sc_empty[slot], sph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_CONV_EMPTY)) break;
                 float* dst = sc + slot * C::SC_KB * C::SC_PITCH;
                 for (int i = lane; i < C::SC_KB * C::TN; i += 32) {
                     const int k = i / C::TN, r = i % C::TN;
-                    const bool in = kb + k < kb1 && m0 + r < p.M;
+                    const bool in = kb + k < kb1 && m0 + r < m_end;
                     cp_async4(dst + k * C::SC_PITCH + r, in ? p.Xs + (long)(m0 + r) * kbs + kb + k : p.Xs, in);
                 }
                 if (lane < C::MATS * C::SC_KB) {
@@ -378,11 +396,12 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
 
     __syncthreads();
     cluster_sync();   // every CTA's sums are in its shared memory
-    for (int t = rank + cs * warp; t < C::TN && m0 + t < p.M; t += cs * (C::THREADS / 32)) {
+    for (int t = rank + cs * warp; t < C::TN && m0 + t < m_end; t += cs * (C::THREADS / 32)) {
         const long m = (long)m0 + t;
         const uint32_t a = smem_u32(sums + t * 128 + (C::TOKENS_M ? lane ^ (t & 31) : lane) * 4);
-        const float4 y = cluster_sum(a, cs);
+        float4 y = cluster_sum(a, cs);
         const int n = n0 + lane * 4;
+        if constexpr (C::EPI) y = epilogue4(p, m, n, y);
         if constexpr (!C::GATED) {
             const float v[4] = {y.x, y.y, y.z, y.w};
             if (p.y_bf16) {
@@ -457,7 +476,7 @@ cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Para
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1] = overlap_attribute();
-    cfg.gridDim = dim3(cs, (p.n_end - p.n_first + 127) / 128, (p.M + C::TN - 1) / C::TN);
+    cfg.gridDim = dim3(cs, (p.n_end - p.n_first + 127) / 128, C::GROUPED ? p.max_tiles : (p.M + C::TN - 1) / C::TN);
     cfg.blockDim = dim3(C::THREADS, 1, 1);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;
@@ -500,30 +519,29 @@ cudaError_t clusters_at_once(int cs, int dev, int* clusters) {
 }
 
 // f(configuration) for the kernel of tn tokens a tile
-template <class F>
-auto with_config(bool gated, int tn, F f) {
-    if (gated) {
-        if (tn == 16) return f(NarrowCfg<16, true>{});
-        if (tn == 32) return f(NarrowCfg<32, true>{});
-        if (tn == 64) return f(NarrowCfg<64, true>{});
-        return f(NarrowCfg<128, true>{});
-    }
-    if (tn == 16) return f(NarrowCfg<16, false>{});
-    if (tn == 32) return f(NarrowCfg<32, false>{});
-    if (tn == 64) return f(NarrowCfg<64, false>{});
-    return f(NarrowCfg<128, false>{});
+template <bool GATED, bool EPI, bool GROUPED, class F>
+auto with_tile(int tn, F f) {
+    if (tn == 16) return f(NarrowCfg<16, GATED, EPI, GROUPED>{});
+    if (tn == 32) return f(NarrowCfg<32, GATED, EPI, GROUPED>{});
+    if (tn == 64) return f(NarrowCfg<64, GATED, EPI, GROUPED>{});
+    return f(NarrowCfg<128, GATED, EPI, GROUPED>{});
 }
 
 }  // namespace
 
-// (A cluster's CTAs are on SMs of one group of SMs, so fewer fit than slots / cs.)
+// (A cluster's CTAs are on SMs of one group of SMs, so fewer fit than slots / cs.  The epilogue
+// and the grouped form change nothing in what a CTA holds.)
 cudaError_t fp8a8_narrow_at_once(bool gated, int tn, int cs, int dev, int* clusters) {
-    return with_config(gated, tn, [&](auto c) { return clusters_at_once<decltype(c)>(cs, dev, clusters); });
+    auto f = [&](auto c) { return clusters_at_once<decltype(c)>(cs, dev, clusters); };
+    return gated ? with_tile<true, false, false>(tn, f) : with_tile<false, false, false>(tn, f);
 }
 
 cudaError_t launch_fp8a8_narrow(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, bool gated, int tn,
                                 int cs, int dev, cudaStream_t s) {
-    return with_config(gated, tn, [&](auto c) { return launch<decltype(c)>(tx, tw, p, cs, dev, s); });
+    auto f = [&](auto c) { return launch<decltype(c)>(tx, tw, p, cs, dev, s); };
+    if (p.tiles) return gated ? with_tile<true, false, true>(tn, f) : with_tile<false, false, true>(tn, f);
+    if (p.epilogue) return with_tile<false, true, false>(tn, f);
+    return gated ? with_tile<true, false, false>(tn, f) : with_tile<false, false, false>(tn, f);
 }
 
 }  // namespace qmm

@@ -38,10 +38,11 @@ namespace {
 
 // RAGGED: Y's row pitch is no multiple of 16 bytes.  BF16: Y is bf16, not fp32.  (One kernel with
 // all four ways to store makes the fold spill.)
-template <int BN_, bool GATED_, bool BF16_ = true, bool RAGGED_ = false>
+// EPI: y = act(y + bias) + R before the rounding; RAGGED is then Y's or R's pitch no multiple of 4 elements.
+template <int BN_, bool GATED_, bool BF16_ = true, bool RAGGED_ = false, bool EPI_ = false>
 struct PairCfg {
     static constexpr int BN = BN_;
-    static constexpr bool GATED = GATED_, RAGGED = RAGGED_, BF16 = BF16_;
+    static constexpr bool GATED = GATED_, RAGGED = RAGGED_, BF16 = BF16_, EPI = EPI_;
     static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / 2 * 128, STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGING = 4096;   // of a fold warp, for its outputs
     // 160 KB of operands (256 columns to a product: 128 KB beside the 64 KB of staging, as fast)
@@ -208,7 +209,8 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
             const PairTile ti = pair_tile<C>(p, te, crank);
             if constexpr (!C::GATED) {
                 uint8_t* stg = outs + (warp - 4) * C::STAGING;
-                store_columns<C::BF16, C::RAGGED, C::BN == 256 ? 4 : 8>(p, stg, lane, (long)ti.m0 + q * 32, ti.n0 + fold_col<C>(cq, 0), acc);
+                if constexpr (C::EPI) store_epilogue<C::BF16, !C::RAGGED>(p, stg, lane, (long)ti.m0 + q * 32, ti.n0 + fold_col<C>(cq, 0), acc);
+                else store_columns<C::BF16, C::RAGGED, C::BN == 256 ? 4 : 8>(p, stg, lane, (long)ti.m0 + q * 32, ti.n0 + fold_col<C>(cq, 0), acc);
             } else {
                 // the first half of acc: gate columns; the second half: the same columns of up
                 constexpr int HP = C::CW / 4;   // pairs
@@ -422,6 +424,13 @@ cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Para
 
 template <int BN>
 cudaError_t launch_product(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, int sms, int dev, cudaStream_t s) {
+    if (p.epilogue) {
+        if (p.y_bf16)
+            return p.vec4 ? launch<PairCfg<BN, false, true, false, true>>(tx, tw, p, sms, dev, s)
+                          : launch<PairCfg<BN, false, true, true, true>>(tx, tw, p, sms, dev, s);
+        return p.vec4 ? launch<PairCfg<BN, false, false, false, true>>(tx, tw, p, sms, dev, s)
+                      : launch<PairCfg<BN, false, false, true, true>>(tx, tw, p, sms, dev, s);
+    }
     const bool ragged = (long)p.N * (p.y_bf16 ? 2 : 4) % 16 != 0;
     if (p.y_bf16)
         return ragged ? launch<PairCfg<BN, false, true, true>>(tx, tw, p, sms, dev, s)

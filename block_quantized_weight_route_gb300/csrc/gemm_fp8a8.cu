@@ -1,4 +1,6 @@
 // FP8 x FP8 products with block scales: which kernel takes which shape.
+#include <cmath>
+
 #include "qmm_internal.h"
 
 namespace qmm {
@@ -119,6 +121,55 @@ cudaError_t fp8a8_plan(int M, int K, int N, bool gated, int sms, int dev, Fp8a8P
     }
     slot = Known{M, K, N, gated, dev, r};
     *plans = r;
+    return cudaSuccess;
+}
+
+// The expert stage: the tile's tokens with the least estimated time of both products (the narrow
+// kernel's constants above), for tokens that choose their experts evenly: the host does not
+// know the rows of an expert.
+cudaError_t moe_plan(int T, int D, int F, int E, int k, int dev, MoePlan* plan) {
+    struct Known {
+        int T, D, F, E, k, dev;
+        MoePlan plan;
+    };
+    static thread_local Known known[8] = {};
+    Known& slot = known[((unsigned)T * 2654435761u ^ (unsigned)D * 40503u ^ (unsigned)F * 9973u ^ (unsigned)(E * 31 + k)) >> 7 & 7u];
+    if (slot.T == T && slot.D == D && slot.F == F && slot.E == E && slot.k == k && slot.dev == dev) {
+        *plan = slot.plan;
+        return cudaSuccess;
+    }
+    const double experts = E * (1.0 - std::pow(1.0 - (k < E ? (double)k / E : 1.0), T)), rows = (double)T * k / experts;
+    double least = 1e300;
+    MoePlan best{128, 1, 1};
+    for (int i = 0; i < 4; ++i) {
+        if ((long)T * k / kTn[i] + E > 65535) continue;   // (the tiles are a dimension of the grid)
+        const double fill = rows / kTn[i], entries = experts * (fill < 0.5 ? 1.0 : fill + 0.5);
+        MoePlan pl{kTn[i], 1, 1};
+        double total = 0.0;
+        for (int gated = 0; gated < 2; ++gated) {
+            const int kbs = gated ? (D + 127) / 128 : F / 128, columns = gated ? F / 128 : (D + 127) / 128;
+            double t_best = 1e300;
+            for (int cs = 1; cs <= 8 && cs <= kbs; ++cs) {
+                int at_once = 0;
+                const cudaError_t e = fp8a8_narrow_at_once(gated, kTn[i], cs, dev, &at_once);
+                if (e != cudaSuccess) return e;
+                if (at_once < 1) continue;
+                const double tiles = entries * columns, waves = tiles < at_once ? 1.0 : tiles / at_once;
+                const double t = waves * (2.0 + 0.1 * cs + 0.011 * kTn[i] * (gated ? 2 : 1) + (kbs + cs - 1) / cs * kNarrowKb[gated][i]);
+                if (t < t_best) {
+                    t_best = t;
+                    (gated ? pl.cs_gate_up : pl.cs_down) = cs;
+                }
+            }
+            total += t_best;
+        }
+        if (total < least) {
+            least = total;
+            best = pl;
+        }
+    }
+    slot = Known{T, D, F, E, k, dev, best};
+    *plan = best;
     return cudaSuccess;
 }
 

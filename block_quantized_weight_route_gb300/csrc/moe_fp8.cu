@@ -1,0 +1,243 @@
+// Data movement of the FP8 expert stage: grouping of (token, expert) pairs by expert, the
+// gather of the tokens' rows, and the weighted combine.
+//
+// Grouping: pair q = t * k + j with expert ids[q] takes row offsets[e] + its rank among the
+// expert's pairs, in ascending q; pairs without an expert (ids[q] outside [0, E)) take none.
+// Ranks come from counts of fixed pieces (a warp's 32 pairs, then chunks of 2048), never from
+// atomic slot claims: the same rows every call, also where a token names an expert twice.
+#include "ptx.cuh"
+#include "qmm_internal.h"
+#include "quant8.cuh"
+
+namespace qmm {
+namespace {
+
+constexpr int kThreads = 1024, kPieces = kMoeChunk / 32;   // pieces of 32 pairs in a chunk
+
+// Pairs of each expert in each chunk.
+__global__ void __launch_bounds__(kThreads) moe_count_kernel(const int32_t* ids, int P, int E, int32_t* chunk_counts) {
+    __shared__ int32_t count[kMoeMaxExperts];
+    launch_dependents();
+    wait_prerequisites();
+    for (int e = threadIdx.x; e < E; e += kThreads) count[e] = 0;
+    __syncthreads();
+    const long q0 = (long)blockIdx.x * kMoeChunk;
+    for (int i = threadIdx.x; i < kMoeChunk; i += kThreads) {
+        const int e = q0 + i < P ? ids[q0 + i] : -1;
+        if ((unsigned)e < (unsigned)E) atomicAdd(&count[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kThreads) chunk_counts[(long)blockIdx.x * E + e] = count[e];
+}
+
+// Exclusive scan of one int a thread over the block.
+__device__ int block_scan(int v, int* total) {
+    __shared__ int warp_sums[kThreads / 32];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[wid] = x;
+    __syncthreads();
+    if (wid == 0) {
+        int s = warp_sums[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        warp_sums[lane] = s;
+    }
+    __syncthreads();
+    *total = warp_sums[kThreads / 32 - 1];
+    return (wid ? warp_sums[wid - 1] : 0) + x - v;
+}
+
+// One CTA a chunk: the rows of its pairs.  The first CTA writes what belongs to all of them:
+// counts, offsets and the tiles of `tile_rows` rows.
+__global__ void __launch_bounds__(kThreads) moe_rows_kernel(const int32_t* ids, int P, int E, int k, MoeGroups g) {
+    extern __shared__ uint16_t piece[];   // [kPieces][E]: pairs of the expert in a piece, then in the pieces before it
+    __shared__ int32_t first[kMoeMaxExperts];   // the chunk's first row of an expert
+    launch_dependents();
+    wait_prerequisites();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long q0 = (long)blockIdx.x * kMoeChunk;
+    const int n = (int)(P - q0 < kMoeChunk ? P - q0 : kMoeChunk), pieces = (n + 31) / 32;
+    for (int i = threadIdx.x; i < (pieces * E + 1) / 2; i += kThreads) reinterpret_cast<uint32_t*>(piece)[i] = 0;
+    __syncthreads();
+    int mine[kMoeChunk / kThreads], rank[kMoeChunk / kThreads];
+#pragma unroll
+    for (int r = 0; r < kMoeChunk / kThreads; ++r) {
+        const int i = r * kThreads + threadIdx.x;
+        int e = i < n ? ids[q0 + i] : -1;
+        if ((unsigned)e >= (unsigned)E) e = -1;
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        mine[r] = e;
+        rank[r] = __popc(same & ((1u << lane) - 1u));
+        if (e >= 0 && rank[r] == 0) piece[(r * (kThreads / 32) + warp) * E + e] = (uint16_t)__popc(same);
+    }
+    __syncthreads();
+    int total = 0, before = 0;   // the expert's pairs: all, and in earlier chunks
+    const int e = threadIdx.x;
+    if (e < E) {
+        int run = 0;
+        for (int i = 0; i < pieces; ++i) {
+            const int v = piece[i * E + e];
+            piece[i * E + e] = (uint16_t)run;
+            run += v;
+        }
+        total = run;
+        if (gridDim.x > 1) {
+            total = 0;
+#pragma unroll 8
+            for (int c = 0; c < (int)gridDim.x; ++c) {
+                const int v = g.chunk_counts[(long)c * E + e];
+                before += c < (int)blockIdx.x ? v : 0;
+                total += v;
+            }
+        }
+    }
+    int all;
+    const int offset = block_scan(total, &all);
+    if (e < E) first[e] = offset + before;
+    if (blockIdx.x == 0) {
+        const int tiles = (total + g.tile_rows - 1) / g.tile_rows;
+        int num;
+        const int t0 = block_scan(tiles, &num);
+        if (e < E) {
+            g.counts[e] = total;
+            g.offsets[e] = offset;
+            for (int i = 0; i < tiles; ++i)
+                if (t0 + i < g.max_tiles)
+                    g.tiles[t0 + i] = make_int4(e, offset + i * g.tile_rows, min(g.tile_rows, total - i * g.tile_rows), 0);
+        }
+        if (e == 0) {
+            g.offsets[E] = all;
+            *g.num_tiles = min(num, g.max_tiles);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kMoeChunk / kThreads; ++r) {
+        const int i = r * kThreads + threadIdx.x;
+        if (i < n) {
+            int at = -1;
+            if (mine[r] >= 0) {
+                at = first[mine[r]] + piece[(r * (kThreads / 32) + warp) * E + mine[r]] + rank[r];
+                g.src[at] = (int32_t)((q0 + i) / k);
+            }
+            g.row[q0 + i] = at;
+        }
+    }
+}
+
+// Xp[r] = Xq[src[r]] and its scales: a warp a row.
+__global__ void __launch_bounds__(256) moe_gather_kernel(const uint4* Xq, const float* Xs, const int32_t* src, const int32_t* rows,
+                                                         int vecs, int kbs, uint4* Xp, float* Xps) {
+    launch_dependents();
+    wait_prerequisites();
+    const int lane = threadIdx.x & 31, n = *rows;
+    for (long r = (blockIdx.x * (long)blockDim.x + threadIdx.x) >> 5; r < n; r += (long)gridDim.x * blockDim.x >> 5) {
+        const long t = src[r];
+        const uint4* in = Xq + t * vecs;
+        uint4* out = Xp + r * vecs;
+        int i = lane;
+        for (; i + 96 < vecs; i += 128) {   // four loads in flight a lane
+            const uint4 a = __ldg(in + i), b = __ldg(in + i + 32), c = __ldg(in + i + 64), d = __ldg(in + i + 96);
+            out[i] = a;
+            out[i + 32] = b;
+            out[i + 64] = c;
+            out[i + 96] = d;
+        }
+        for (; i < vecs; i += 32) out[i] = __ldg(in + i);
+        for (int j = lane; j < kbs; j += 32) Xps[r * kbs + j] = __ldg(Xs + t * kbs + j);
+    }
+}
+
+// Y[t] = R[t] + sum_j w[t][j] Yslot[row[t][j]], j ascending, in fp32; four columns a thread.
+template <int K>
+__global__ void __launch_bounds__(256) moe_combine_kernel(const float4* Yslot, const int32_t* row, const float* w, int k, int vecs,
+                                                          const void* R, int r_bf16, long ldr, void* Y, int y_bf16) {
+    launch_dependents();
+    wait_prerequisites();
+    const long t = blockIdx.x;
+    int rr[K];
+    float ww[K];
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        rr[j] = j < k ? __ldg(row + t * k + j) : -1;
+        ww[j] = j < k ? __ldg(w + t * k + j) : 0.0f;
+    }
+    for (int i = threadIdx.x; i < vecs; i += 256) {
+        float4 v[K];
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            if (rr[j] >= 0) v[j] = __ldcs(Yslot + (long)rr[j] * vecs + i);
+        float4 a = R ? load4(R, r_bf16, t * ldr + i * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            if (rr[j] >= 0) {
+                a.x = fmaf(ww[j], v[j].x, a.x);
+                a.y = fmaf(ww[j], v[j].y, a.y);
+                a.z = fmaf(ww[j], v[j].z, a.z);
+                a.w = fmaf(ww[j], v[j].w, a.w);
+            }
+        }
+        store4(Y, y_bf16, (t * vecs + i) * 4, a);
+    }
+}
+
+template <class A>
+struct Same {   // (an argument converts to the kernel's type)
+    using type = A;
+};
+template <class... A>
+cudaError_t launch(void (*kernel)(A...), unsigned grid, unsigned block, size_t smem, cudaStream_t s, typename Same<A>::type... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1] = {overlap_attribute()};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(block, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_group(const int32_t* ids, int P, int E, int k, const MoeGroups& g, int dev, cudaStream_t s) {
+    static PerDevice ready;
+    if (!ready.get(dev)) {
+        const cudaError_t e = cudaFuncSetAttribute(moe_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   kPieces * kMoeMaxExperts * 2);
+        if (e != cudaSuccess) return e;
+        ready.set(dev, 1);
+    }
+    const int chunks = (P + kMoeChunk - 1) / kMoeChunk;
+    if (chunks > 1) {
+        const cudaError_t e = launch(moe_count_kernel, chunks, kThreads, 0, s, ids, P, E, g.chunk_counts);
+        if (e != cudaSuccess) return e;
+    }
+    const int pieces = P < kMoeChunk ? (P + 31) / 32 : kPieces;
+    return launch(moe_rows_kernel, chunks, kThreads, ((size_t)pieces * E * 2 + 3) / 4 * 4, s, ids, P, E, k, g);
+}
+
+cudaError_t launch_moe_gather(const uint8_t* Xq, const float* Xs, int P, int D, const MoeGroups& g, int E, uint8_t* Xp, float* Xps,
+                              int sms, cudaStream_t s) {
+    const long ctas = ((long)P + 7) / 8, most = (long)sms * 8;
+    return launch(moe_gather_kernel, (unsigned)(ctas < most ? ctas : most), 256, 0, s, reinterpret_cast<const uint4*>(Xq), Xs, g.src,
+                  g.offsets + E, D / 16, (D + 127) / 128, reinterpret_cast<uint4*>(Xp), Xps);
+}
+
+cudaError_t launch_moe_combine(const float* Yslot, const int32_t* row, const float* w, int T, int k, int D, const void* R, int r_bf16,
+                               long ldr, void* Y, int y_bf16, cudaStream_t s) {
+    const auto kernel = k <= 2 ? moe_combine_kernel<2> : k <= 4 ? moe_combine_kernel<4> : k <= 8 ? moe_combine_kernel<8> : moe_combine_kernel<16>;
+    return launch(kernel, T, 256, 0, s, reinterpret_cast<const float4*>(Yslot), row, w, k, D / 4, R, r_bf16, ldr, Y, y_bf16);
+}
+
+}  // namespace qmm

@@ -151,6 +151,18 @@ struct Fp8a8Params {
     uint32_t* err;       // device error word
     int n_first, n_end;  // the launch's columns (n_first a multiple of 128)
     int m_tiles, n_tiles;
+    // y = act(y + bias[n]) + R[m][n]
+    bool epilogue;
+    int act;             // a qmm_act
+    const void* bias;    // [N], or null
+    const void* R;       // [M][ldr], or null; may be Y
+    long ldr;
+    int bias_bf16, r_bf16;
+    bool vec4;           // N and ldr are multiples of 4
+    // rows grouped by expert: W [E][N or 2N][K], S alike, M all rows
+    const int4* tiles;   // {expert, first row, rows, 0}; null: not grouped
+    const int* num_tiles;   // on the device
+    int max_tiles;       // room in `tiles`
 };
 // Which kernel takes a product: the pair kernel (many tokens) with its tile's columns,
 // or the narrow kernel (few) with its tile's tokens and the CTAs that share its K blocks.
@@ -165,6 +177,12 @@ struct Fp8a8Plans {
     int split;
 };
 cudaError_t fp8a8_plan(int M, int K, int N, bool gated, int sms, int dev, Fp8a8Plans* plans);
+// The expert stage's tiles: tokens of a tile, and the CTAs that share the K blocks of one in
+// the gate/up and in the down product.
+struct MoePlan {
+    int tn, cs_gate_up, cs_down;
+};
+cudaError_t moe_plan(int T, int D, int F, int E, int k, int dev, MoePlan* plan);
 bool fp8a8_plans_fit(const Fp8a8Plans& r, int M, int K, int N, bool gated);   // whether the kernels can run a given tiling
 // clusters of cs CTAs that the device holds at once (0: none)
 cudaError_t fp8a8_narrow_at_once(bool gated, int tn, int cs, int dev, int* clusters);
@@ -172,6 +190,42 @@ cudaError_t launch_fp8a8_narrow(const CUtensorMap& tx, const CUtensorMap& tw, co
                                 int cs, int dev, cudaStream_t s);
 cudaError_t launch_fp8a8_pair(const CUtensorMap& tx, const CUtensorMap& tw, Fp8a8Params p, bool gated, int bn, int sms,
                               int dev, cudaStream_t s);
+
+// Grouping of the FP8 expert stage (moe_fp8.cu).
+constexpr int kMoeChunk = 2048, kMoeMaxExperts = 512;   // pairs of a grouping chunk
+struct MoeGroups {
+    int32_t* counts;        // [E]
+    int32_t* offsets;       // [E + 1]
+    int32_t* src;           // [P] token of each row
+    int32_t* row;           // [P] row of each pair, -1 for one without an expert
+    int32_t* chunk_counts;  // [chunks][E] (scratch)
+    int4* tiles;            // {expert, first row, rows, 0}
+    int* num_tiles;
+    int tile_rows, max_tiles;
+};
+cudaError_t launch_moe_group(const int32_t* ids, int P, int E, int k, const MoeGroups& g, int dev, cudaStream_t s);
+cudaError_t launch_moe_gather(const uint8_t* Xq, const float* Xs, int P, int D, const MoeGroups& g, int E, uint8_t* Xp, float* Xps,
+                              int sms, cudaStream_t s);
+cudaError_t launch_moe_combine(const float* Yslot, const int32_t* row, const float* w, int T, int k, int D, const void* R, int r_bf16,
+                               long ldr, void* Y, int y_bf16, cudaStream_t s);
+
+// Routing by scores (route_scored.cu).
+struct ScoredParams {
+    const void* logits;  // [T][ldl] fp32 or bf16
+    const float* bias;   // [E], or null
+    const int32_t* live; // tokens from *live on have no experts (null: all T are live)
+    long ldl;
+    int l_bf16, T, E, k;
+    int sigmoid;         // else softmax
+    int groups, groups_kept, group_top;
+    int group_size;      // E / groups, and 2^20 / group_size rounded up (set by the launcher)
+    unsigned group_inv;
+    int renorm;
+    float scale;
+    int32_t* ids;        // [T][k]
+    float* w;            // [T][k]
+};
+cudaError_t launch_route_scored(ScoredParams p, int sms, cudaStream_t s);
 
 // Set the calling thread's message returned by qmm_last_error().
 void set_last_error(const char* msg);

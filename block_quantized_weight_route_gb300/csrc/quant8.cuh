@@ -42,6 +42,26 @@ __device__ __forceinline__ float max_nan_abs(float a, float b, float c) {
     return r;
 }
 
+// Four consecutive elements of an fp32 or bf16 array, i a multiple of 4; and one.
+__device__ __forceinline__ float4 load4(const void* a, int bf16, long i) {
+    if (!bf16) return *reinterpret_cast<const float4*>(static_cast<const float*>(a) + i);
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a) + i);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                       __uint_as_float(w.y & 0xffff0000u));
+}
+__device__ __forceinline__ float load1(const void* a, int bf16, long i) {
+    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a)[i]) : static_cast<const float*>(a)[i];
+}
+__device__ __forceinline__ void store4(void* a, int bf16, long i, float4 v) {
+    if (bf16) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a) + i) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    } else {
+        *reinterpret_cast<float4*>(static_cast<float*>(a) + i) = v;
+    }
+}
+
 // Two fp32 values in one 64-bit register, and packed arithmetic on them.
 __device__ __forceinline__ uint64_t pack2u(uint32_t a, uint32_t b) {
     uint64_t r;

@@ -186,6 +186,96 @@ qmm_status qmm_fp8a8_swiglu_blk128(const uint8_t *Xq, const float *Xs, int M, in
                                    const float *Sgu, uint8_t *Hq, float *Hs, cudaStream_t stream);
 
 /*
+ * qmm_fp8a8_epilogue_blk128 -- qmm_fp8a8_blk128 with a bias, an activation and a residual
+ * in the kernel's epilogue:
+ *   Y[m,n] = act(P[m,n] + bias[n]) + R[m,n],  P the product's fp32 sum (as in qmm_fp8a8_blk128)
+ *   act: QMM_ACT_NONE v;  QMM_ACT_RELU max(v, 0);  QMM_ACT_SILU v / (1 + exp(-v));
+ *        QMM_ACT_GELU v/2 (1 + erf(v / sqrt 2));
+ *        QMM_ACT_GELU_TANH v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3)))
+ *   bias [N] fp32 or bf16, or NULL (bdt is then ignored);
+ *   R [M] rows of ldr elements, fp32 or bf16, or NULL (ldr and rdt are then ignored); R may be
+ *   Y (same type, ldr = N): the residual stream in place.  Other overlaps of R and Y are not allowed.
+ *   Y [M][N] fp32 or bf16 (RNE).  Everything between the product and Y is fp32.
+ * Shapes as qmm_fp8a8_blk128; ldr >= N.
+ */
+typedef enum {
+    QMM_ACT_NONE = 0,
+    QMM_ACT_RELU = 1,
+    QMM_ACT_SILU = 2,
+    QMM_ACT_GELU = 3,
+    QMM_ACT_GELU_TANH = 4
+} qmm_act;
+qmm_status qmm_fp8a8_epilogue_blk128(const uint8_t *Xq, const float *Xs, int M, int K, int N, const uint8_t *W,
+                                     const float *S, const void *bias, qmm_dtype bdt, qmm_act act, const void *R,
+                                     int64_t ldr, qmm_dtype rdt, void *Y, qmm_dtype ydt, cudaStream_t stream);
+
+/*
+ * moe_route_scored -- routing of T tokens to k of E experts by scores, for any
+ * expert stage that takes ids and weights (moe_expert_stage_fp8):
+ *   s = softmax(l) (QMM_SCORE_SOFTMAX) or 1 / (1 + exp(-l)) (QMM_SCORE_SIGMOID);
+ *   c = s + bias (the bias, for balance, steers the choice and is not in the weights);
+ *   groups > 1: the experts are `groups` runs of E / groups; a group's score is the sum of
+ *     its group_top largest c, and only the groups_kept groups of largest score take part;
+ *   ids[t] = the k largest c, descending; w[t][j] = scale * s[ids[t][j]], with renorm != 0
+ *     divided by the sum of the k chosen s first.
+ * The order is that of exact arithmetic (of 64 bits where 32 do not decide it); equal values go
+ * to the lower index, experts and groups alike.  Renormalised weights are ratios of the
+ * exact scores, also where those underflow.  fp32 arithmetic for the weights.
+ *   An expert whose logit is -inf or NaN is off, and counts nothing in a softmax; one whose
+ *   bias is -inf or NaN is not chosen.  A group with fewer than group_top experts left has score -inf.
+ *   Where fewer than k experts are left, the last places get id -1 and weight 0.  A
+ *   logit of +inf makes a softmax NaN: its weights, and with a bias or sums of a group
+ *   the choice too (ids -1).
+ *   live: device int32, or NULL: tokens t >= *live (a batch's padding) get ids -1 and weights
+ *   0, and their logits are not read.
+ *   logits [T] rows of ldl elements, fp32 or bf16; bias [E] fp32 or NULL;
+ *   ids [T][k] int32; w [T][k] fp32.
+ * Shapes: T >= 0, 1 <= E <= 512, 1 <= k <= 16, k <= E / groups * groups_kept,
+ * 1 <= groups <= 32, E % groups == 0, 1 <= groups_kept <= groups, group_top 1 or 2 and (groups > 1)
+ * at most E / groups; ldl >= E.  groups = 1: groups_kept must be 1, group_top is ignored.
+ */
+typedef enum { QMM_SCORE_SOFTMAX = 0, QMM_SCORE_SIGMOID = 1 } qmm_score;
+qmm_status moe_route_scored(const void *logits, qmm_dtype ldt, int64_t ldl, const float *bias, const int32_t *live,
+                            int T, int E, int k, qmm_score score, int groups, int groups_kept, int group_top,
+                            int renorm, float scale, int32_t *ids, float *w, cudaStream_t stream);
+
+/*
+ * moe_expert_stage_fp8 -- the routed expert stage over FP8 weights and activations, for
+ * prompts and for single tokens, with the experts and weights of any router:
+ *   for each token t and each j with e = ids[t][j]:
+ *     g, u = rows n and F + n of Wgu[e] times X[t] (as qmm_fp8a8_blk128);
+ *     h = g / (1 + exp(-g)) * u, per 128 columns Hs = max|h| / 448, Hq = E4M3(h / Hs);
+ *     y_tj = Wd[e] . H  (as qmm_fp8a8_blk128)
+ *   Y[t] = R[t] + sum_j w[t][j] * y_tj   (fp32, j ascending: the same bits every call)
+ *   A pair whose id is outside [0, E) (a router's -1) adds nothing, whatever its weight; a
+ *   token may name an expert more than once.
+ *   Xq [T][D] E4M3, Xs [T][ceil(D/128)] fp32 (as qmm_add_rmsnorm_fp8 writes them);
+ *   ids [T][k] int32; w [T][k] fp32;
+ *   Wgu [E][2F][D] E4M3 (gate rows first), Sgu [E][2F/128][ceil(D/128)] fp32;
+ *   Wd [E][D][F] E4M3, Sd [E][ceil(D/128)][F/128] fp32;
+ *   R [T] rows of ldr elements, fp32 or bf16, or NULL (ldr, rdt ignored); may be Y (same
+ *   type, ldr = D), other overlaps of R and Y are not allowed; Y [T][D] fp32 or bf16 (RNE).
+ *   ws: device scratch of at least moe_expert_stage_fp8_workspace_size(...) bytes, 256-byte
+ *   aligned; its regions are listed by moe_expert_stage_fp8_workspace_layout().  Calls that share it
+ *   (captured graphs too) must not overlap on the GPU.
+ * Shapes: T >= 0, D % 16 == 0, F % 128 == 0, 1 <= k <= 16, 1 <= E <= 512, D and F at most 2^20,
+ * T * k at most 2^22, E * 2F and E * D at most 2^31 - 512; ldr >= D and a multiple of 4.
+ */
+size_t moe_expert_stage_fp8_workspace_size(int T, int D, int F, int E, int k);
+qmm_status moe_expert_stage_fp8(const uint8_t *Xq, const float *Xs, const int32_t *ids, const float *w, int T, int D,
+                                int F, int E, int k, const uint8_t *Wgu, const float *Sgu, const uint8_t *Wd,
+                                const float *Sd, const void *R, int64_t ldr, qmm_dtype rdt, void *Y, qmm_dtype ydt,
+                                void *ws, size_t ws_bytes, cudaStream_t stream);
+/* Byte offsets of its workspace's regions, in this order (P = T * k pairs; a pair's row is
+ * its place among all pairs grouped by expert, in ascending order of t and j):
+ *   0 counts [E] i32 (pairs of an expert)   1 offsets [E+1] i32 (its first row)
+ *   2 src [P] i32 (a row's token)   3 row [P] i32 (a pair's row, -1: no expert)
+ *   4 chunk counts   5 tile list   6 its count   7 X rows [P][D] E4M3   8 their scales [P][ceil(D/128)]
+ *   9 Hq [P][F] E4M3   10 Hs [P][F/128] fp32   11 y [P][D] fp32   12 total size */
+#define QMM_MOE_FP8_WS_FIELDS 13
+qmm_status moe_expert_stage_fp8_workspace_layout(int T, int D, int F, int E, int k, size_t *offsets_out);
+
+/*
  * moe_route_permute -- top-k routing and per-expert grouping of T tokens.
  * For each token t: ids[t][0..k) are the k largest logits (descending; a tie
  * goes to the lower expert index) and w[t][j] = exp(l_j - l_max) / sum over the
@@ -341,7 +431,8 @@ qmm_status qmm_dbg_combine(const float *Yslot, int P, const int32_t *row, const 
  *   or 128) x 128 columns, K over clusters of cs CTAs (1 to 8, at most the K blocks).
  * qmm_dbg_fp8a8_plan -- the tiling that qmm_fp8a8_blk128 (gated == 0) or
  *   qmm_fp8a8_swiglu_blk128 (N = F) takes on the current device.
- * qmm_dbg_fp8a8_blk128 / qmm_dbg_fp8a8_swiglu_blk128 -- the products by a given tiling.
+ * qmm_dbg_fp8a8_blk128 / qmm_dbg_fp8a8_swiglu_blk128 / qmm_dbg_fp8a8_epilogue_blk128 -- the
+ *   products by a given tiling.
  */
 #define QMM_FP8A8_PLAN_FIELDS 9
 qmm_status qmm_dbg_fp8a8_plan(int M, int K, int N, int gated, int *plan);
@@ -350,6 +441,10 @@ qmm_status qmm_dbg_fp8a8_blk128(const uint8_t *Xq, const float *Xs, int M, int K
 qmm_status qmm_dbg_fp8a8_swiglu_blk128(const uint8_t *Xq, const float *Xs, int M, int K, int F, const uint8_t *Wgu,
                                        const float *Sgu, uint8_t *Hq, float *Hs, const int *plan,
                                        cudaStream_t stream);
+qmm_status qmm_dbg_fp8a8_epilogue_blk128(const uint8_t *Xq, const float *Xs, int M, int K, int N, const uint8_t *W,
+                                         const float *S, const void *bias, qmm_dtype bdt, qmm_act act, const void *R,
+                                         int64_t ldr, qmm_dtype rdt, void *Y, qmm_dtype ydt, const int *plan,
+                                         cudaStream_t stream);
 
 /*
  * qmm_dbg_wait_timeout -- test hook for failure detection (no counterpart on
