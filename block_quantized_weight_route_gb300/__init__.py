@@ -546,7 +546,7 @@ def moe_expert_stage_fp8_workspace_size(T: int, D: int, F: int, E: int, k: int) 
 
 
 MOE_FP8_WS_FIELDS = ("counts", "offsets", "src", "row", "chunk_counts", "tiles", "tile_count", "Xp", "Xps", "Hq", "Hs", "y",
-                     "total")
+                     "y_units", "total")
 
 
 def moe_expert_stage_fp8_workspace_layout(T: int, D: int, F: int, E: int, k: int) -> dict:

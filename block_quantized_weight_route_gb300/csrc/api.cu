@@ -1158,7 +1158,7 @@ static void moe_fp8_layout(int T, int D, int F, int E, int k, size_t* off) {
     const size_t sz[QMM_MOE_FP8_WS_FIELDS - 1] = {(size_t)E * 4, (size_t)(E + 1) * 4, P * 4, P * 4,
                                                   (P + kMoeChunk - 1) / kMoeChunk * E * 4,
                                                   (size_t)moe_max_tiles((long)P, E, kMoeTile) * 16, 4, P * D, P * kbs * 4, P * F,
-                                                  P * (F / 128) * 4, P * D * 4};
+                                                  P * (F / 128) * 4, P * D * 4, P * ((D + 63) / 64) * 4};
     size_t o = 0;
     for (int i = 0; i < QMM_MOE_FP8_WS_FIELDS - 1; ++i) {
         off[i] = o;
@@ -1233,7 +1233,11 @@ qmm_status moe_expert_stage_fp8(const uint8_t* Xq, const float* Xs, const int32_
     float* Xps = static_cast<float*>(at(8));
     uint8_t* Hq = static_cast<uint8_t*>(at(9));
     float* Hs = static_cast<float*>(at(10));
-    float* Yslot = static_cast<float*>(at(11));
+    void* y = at(11);
+    // For a bf16 output 11 bits of each expert's row do (half a step is 2^-11 of a term, beside
+    // the output's own 2^-8 of the sum), and are half the bytes: 173 MB in place of 345 written and read again for
+    // 5268 tokens of 2048 columns and 8 experts.
+    float* y_unit = plan.many && ydt == QMM_BF16 ? static_cast<float*>(at(12)) : nullptr;
     if ((e = launch_moe_group(ids, P, E, k, g, d->index, stream)) != cudaSuccess) return cuda_fail(e, "moe_expert_stage_fp8: grouping");
     if ((e = launch_moe_gather(Xq, Xs, P, D, g, E, Xp, Xps, d->sms, stream)) != cudaSuccess)
         return cuda_fail(e, "moe_expert_stage_fp8: gather");
@@ -1246,7 +1250,8 @@ qmm_status moe_expert_stage_fp8(const uint8_t* Xq, const float* Xs, const int32_
         p.M = P;
         p.K = gated ? D : F;
         p.N = gated ? F : D;
-        p.Y = Yslot;
+        p.Y = y;
+        p.y_unit = y_unit;
         p.Hq = Hq;
         p.Hs = Hs;
         p.err = d->err;
@@ -1259,10 +1264,11 @@ qmm_status moe_expert_stage_fp8(const uint8_t* Xq, const float* Xs, const int32_
             (st = make_tmap(&tw, p.W, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, (uint64_t)E * p.N * (gated ? 2 : 1), p.K, 128, 128,
                             CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK)
             return st;
-        e = launch_fp8a8_narrow(tx, tw, p, gated, plan.tn, gated ? plan.cs_gate_up : plan.cs_down, d->index, stream);
+        e = plan.many ? launch_fp8a8_experts(tx, tw, p, gated, d->sms, d->index, stream)
+                      : launch_fp8a8_narrow(tx, tw, p, gated, plan.tn, gated ? plan.cs_gate_up : plan.cs_down, d->index, stream);
         if (e != cudaSuccess) return cuda_fail(e, gated ? "moe_expert_stage_fp8: gate/up" : "moe_expert_stage_fp8: down");
     }
-    e = launch_moe_combine(Yslot, g.row, w, T, k, D, R, rdt == QMM_BF16, (long)ldr, Y, ydt == QMM_BF16, stream);
+    e = launch_moe_combine(y, y_unit, g.row, w, T, k, D, R, rdt == QMM_BF16, (long)ldr, Y, ydt == QMM_BF16, stream);
     return e == cudaSuccess ? QMM_OK : cuda_fail(e, "moe_expert_stage_fp8: combine");
 }
 

@@ -1,0 +1,418 @@
+// The FP8 expert stage's products, many rows an expert: rows grouped by expert against that
+// expert's weights, tile by tile of a list that the grouping wrote on the device.
+//
+//   y[m][n] = sum_kb Xs[m][kb] S[e][n/128][kb] P_kb[m][n],   P_kb = sum_{k in kb} Xq[m][k] W[e][n][k]
+//   GATED: h = silu(y gate) * y up, rounded to E4M3 per 128 columns of a row
+//   else: the rows y, as fp32 or (HALF) as fp16 with a power of two per 64 columns
+//
+// Persistent CTAs, each on one tile of 128 rows x 256 weight rows (GATED: 128 gate, 128 up) at a
+// time: M = 128, N = 256 MMAs of one CTA.  A block's scale differs by row, so each P_kb goes from
+// TMEM to fp32 sums in registers, two TMEM buffers apart from the MMA, as in the pair kernel.
+//   warp 0: TMA producer   warp 1: MMA issuer
+//   warps 2, 3: the scales of several K blocks at a time, by asynchronous copies into a ring
+//   warps 4..19: fold; warp w reads TMEM lanes 32 (w % 4) .. +31 (a row per lane), 64 columns
+// Tiles of 128 rows rather than a CTA pair's 256, because an expert's last tile is half empty in the
+// mean: 42144 rows of 128 experts fill 84% of such tiles and 64% of the pair's.
+#include "fp8a8.cuh"
+
+namespace qmm {
+namespace {
+
+template <bool GATED_, bool HALF_ = false>
+struct ExpertsCfg {
+    static constexpr bool GATED = GATED_, HALF = HALF_;
+    static constexpr int BN = 256, A_BYTES = 128 * 128, B_BYTES = BN * 128, STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int STAGING = 4096;   // of a fold warp, for its outputs
+    static constexpr int CW = 64, GROUPS = BN / CW, FOLD_WARPS = 4 * GROUPS, LW = 8;
+    static constexpr int OUT_BYTES = GATED ? 2 * GROUPS * 128 * 4 : FOLD_WARPS * STAGING;   // row maxima, or output staging
+    static constexpr int STAGES = GATED ? 4 : 3, NBUF = 2, BUF_COLS = 256;
+    static constexpr int SC_KB = 4, SC_SLOTS = 4, SC_PITCH = 128 + 4, SC_FLOATS = SC_SLOTS * SC_KB * SC_PITCH;
+    static constexpr int THREADS = 128 + 32 * FOLD_WARPS, REGS = 65536 / THREADS / 8 * 8, REGS_FOLD = 104, REGS_OTHER = 64;
+    static_assert(REGS_FOLD * 32 * FOLD_WARPS + REGS_OTHER * 128 == REGS * THREADS, "register shares = launch registers");
+    static constexpr int COPIES = 3;
+    static_assert(COPIES * STAGES <= 32, "a lane per copy");
+    static constexpr int BARS = 2 * STAGES + NBUF + 2 * SC_SLOTS + 3;
+    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + OUT_BYTES + SC_FLOATS * 4 + BARS * 8 + 64;
+    static_assert(SMEM <= 232448, "shared memory");
+    static_assert(NBUF <= STAGES, "a stage's MMA barrier completes again only after its accumulator was read");
+};
+
+// Tile t of the launch: rows [m0, m0 + rows) of expert e, columns from n0.
+struct ExpertTile {
+    int e, m0, rows, n0;
+};
+template <class C>
+__device__ __forceinline__ ExpertTile expert_tile(const Fp8a8Params& p, int t) {
+    const int entry = t / p.n_tiles;
+    const int4 v = __ldg(p.tiles + entry);
+    return ExpertTile{v.x, v.y, v.z, (t - entry * p.n_tiles) * (C::GATED ? 128 : C::BN)};
+}
+
+__device__ __forceinline__ uint32_t codes4(const GroupScale& gs, uint64_t a, uint64_t b) {
+    const float2 x = unpack2(a), y = unpack2(b);
+    return e4m3x4(gs(x.x), gs(x.y), gs(y.x), gs(y.y));
+}
+
+// A lane's 64 sums as fp16 in units of a power of two, which it returns: the largest finite
+// one comes to 2^14 .. 2^15, so that 11 bits are kept of all within 2^28 of it; NaN and infinities stay.
+__device__ __forceinline__ float halves(const uint64_t* v, uint32_t (&h)[32]) {
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const float2 f = unpack2(v[i]);
+        const float a = fabsf(f.x), b = fabsf(f.y);
+        top = fmaxf(top, fmaxf(a < INFINITY ? a : 0.0f, b < INFINITY ? b : 0.0f));
+    }
+    // 2^(14 - e) for a top of 2^e .. 2^(e + 1), at most 2^126
+    const int e = (int)(__float_as_uint(top) >> 23);   // biased
+    const int up = min(127 + 14 + 127 - e, 253);
+    const float f = __uint_as_float((uint32_t)up << 23);
+    const uint64_t f2 = pack2(f, f);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const float2 x = unpack2(mul2(v[i], f2));
+        const __half2 y = __floats2half2_rn(x.x, x.y);
+        h[i] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+    return __uint_as_float((uint32_t)(254 - up) << 23);
+}
+
+// A warp's 32 rows x 128 bytes of staging to Y: eight lanes a row.
+__device__ __forceinline__ void flush_rows(const Fp8a8Params& p, const uint8_t* stg, int lane, long row0, int rows, int col, int esz) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + lane / 8, c = lane % 8, n = col + c * (16 / esz);
+        const uint4 d = *reinterpret_cast<const uint4*>(stg + (r * 8 + (c ^ (r & 7))) * 16);
+        if (r < rows && n < p.N) *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.Y) + ((row0 + r) * p.N + n) * esz) = d;
+    }
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
+    fp8a8_experts_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, Fp8a8Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* stage = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* outs = stage + C::STAGES * C::STAGE_BYTES;
+    float* rowmax = reinterpret_cast<float*>(outs);              // gated: [tile parity][column group][128]
+    float* sc = reinterpret_cast<float*>(outs + C::OUT_BYTES);   // [slot][kb][128 rows, 2 weight blocks]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sc + C::SC_FLOATS);
+    uint64_t* full = bars;
+    uint64_t* done = full + C::STAGES;        // a stage's MMAs are complete: its operands are free, its P is in TMEM
+    uint64_t* acc_empty = done + C::STAGES;
+    uint64_t* sc_full = acc_empty + C::NBUF;
+    uint64_t* sc_empty = sc_full + C::SC_SLOTS;
+    uint64_t* drain = sc_empty + C::SC_SLOTS;
+    uint64_t* rm_full = drain + 1;            // gated: every fold warp's row maxima are in shared memory
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rm_full + 2);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&done[i], 1);
+        }
+        for (int i = 0; i < C::NBUF; ++i) mbar_init(&acc_empty[i], C::FOLD_WARPS);
+        for (int i = 0; i < C::SC_SLOTS; ++i) {
+            mbar_init(&sc_full[i], 64);
+            mbar_init(&sc_empty[i], C::FOLD_WARPS);
+        }
+        mbar_init(drain, 1);
+        mbar_init(&rm_full[0], C::FOLD_WARPS);
+        mbar_init(&rm_full[1], C::FOLD_WARPS);
+        *abort_flag = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmW);
+    }
+    if (warp == 1) tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    wait_prerequisites();
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    const int tiles = *p.num_tiles * p.n_tiles, kbs = (p.K + 127) / 128, step = (int)gridDim.x;
+
+    if (warp >= 4) {
+        setmaxnreg_inc<C::REGS_FOLD>();
+        // ------------------------------------------------------------ fold
+        const int q = warp & 3, cq = (warp - 4) >> 2, row = q * 32 + lane;
+        const uint32_t lane_addr = tmem_base + ((uint32_t)(q * 32) << 16);
+        int st = 0, slot = 0, parity = 0;
+        uint32_t ph = 0, sph = 0, rph = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < tiles && ok; t += step, parity ^= 1) {
+            const int blk = !C::GATED && cq * C::CW >= 128;   // which of the tile's two weight blocks
+            uint64_t acc[C::CW / 2];
+#pragma unroll
+            for (int j = 0; j < C::CW / 2; ++j) acc[j] = 0;
+            for (int kb0 = 0; kb0 < kbs && ok; kb0 += C::SC_KB) {
+                ok &= mbar_wait(&sc_full[slot], sph, abort_flag, p.err, DEV_TIMEOUT_CONV);
+                const float* scr = sc + slot * C::SC_KB * C::SC_PITCH;
+#pragma unroll
+                for (int k = 0; k < C::SC_KB; ++k) {
+                    if (kb0 + k >= kbs) break;
+                    const float sx = scr[k * C::SC_PITCH + row];
+                    const float s0 = sx * scr[k * C::SC_PITCH + 128 + blk];
+                    const float s1 = C::GATED ? sx * scr[k * C::SC_PITCH + 129] : s0;
+                    // (after a time-out the sums mean nothing; the loop ends with this group)
+                    ok &= mbar_wait(&done[st], ph, abort_flag, p.err, DEV_TIMEOUT_ACC);
+                    tc_fence_after();
+                    // (the buffer of the tile's K block kb: every tile starts with buffer 0)
+                    const int buf = k & (C::NBUF - 1);
+                    const uint32_t a0 = lane_addr + (uint32_t)(buf * C::BUF_COLS);
+#pragma unroll
+                    for (int x = 0; x < C::CW; x += C::LW) {
+                        uint32_t r[C::LW];
+                        tmem_ld(a0 + fold_col<C>(cq, x), r);
+                        tmem_ld_wait();
+                        if (x == C::CW - C::LW) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&acc_empty[buf]);
+                        }
+                        const float sf = x < C::CW / 2 ? s0 : s1;
+                        const uint64_t s2 = pack2(sf, sf);
+#pragma unroll
+                        for (int j = 0; j < C::LW / 2; ++j)
+                            acc[x / 2 + j] = fma2(pack2u(r[2 * j], r[2 * j + 1]), s2, acc[x / 2 + j]);
+                    }
+                    if (++st == C::STAGES) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sc_empty[slot]);
+                if (++slot == C::SC_SLOTS) {
+                    slot = 0;
+                    sph ^= 1u;
+                }
+            }
+            if (!ok) break;
+            int te = t;   // (the tile's place is worked out here, not kept in registers through its K blocks)
+            asm volatile("" : "+r"(te));
+            const ExpertTile ti = expert_tile<C>(p, te);
+            if constexpr (!C::GATED) {
+                uint8_t* stg = outs + (warp - 4) * C::STAGING;
+                const int rows = ti.rows - q * 32, col = ti.n0 + cq * C::CW;
+                const long row0 = (long)ti.m0 + q * 32;
+                if constexpr (C::HALF) {
+                    if (col + C::CW > p.N) {   // (the columns past the end, another expert's, have no say in the unit)
+#pragma unroll
+                        for (int j = 0; j < C::CW / 2; ++j)
+                            if (col + 2 * j >= p.N) acc[j] = 0;
+                    }
+                    uint32_t h[32];
+                    const float unit = halves(acc, h);
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        *reinterpret_cast<uint4*>(stg + (lane * 8 + (c ^ (lane & 7))) * 16) = make_uint4(h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]);
+                    if (lane < rows && col < p.N) p.y_unit[(row0 + lane) * ((p.N + 63) / 64) + col / 64] = unit;
+                    __syncwarp();
+                    flush_rows(p, stg, lane, row0, rows, col, 2);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 64; c += 32) {
+                        __syncwarp();
+                        stage16<false>(stg, lane, 0, acc + c / 2);
+                        stage16<false>(stg, lane, 4, acc + c / 2 + 8);
+                        __syncwarp();
+                        flush_rows(p, stg, lane, row0, rows, col + c, 4);
+                    }
+                }
+            } else {
+                // the first half of acc: gate columns; the second half: the same columns of up
+                constexpr int HP = C::CW / 4;   // pairs
+                float a = 0.f;
+#pragma unroll
+                for (int j = 0; j < HP; ++j) {
+                    const float2 g = unpack2(acc[j]), u = unpack2(acc[HP + j]);
+                    const float h0 = swiglu(g.x, u.x), h1 = swiglu(g.y, u.y);
+                    a = max_nan_abs(a, h0, h1);
+                    acc[j] = pack2(h0, h1);
+                }
+                float* rm = rowmax + parity * 512 + row;
+                rm[cq * 128] = a;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&rm_full[parity]);
+                if (!mbar_wait(&rm_full[parity], rph, abort_flag, p.err, DEV_TIMEOUT_ACC)) break;
+                rph ^= (uint32_t)parity;
+#pragma unroll
+                for (int i = 0; i < C::GROUPS; ++i) a = max_nan(a, rm[i * 128]);
+                const GroupScale gs = group_scale<448>(a);
+                if (row < ti.rows) {
+                    const long grow = (long)ti.m0 + row;
+                    uint4* dst = reinterpret_cast<uint4*>(p.Hq + grow * p.N + ti.n0 + cq * (C::CW / 2));
+#pragma unroll
+                    for (int j = 0; j < HP / 8; ++j) {
+                        const uint64_t* v = acc + 8 * j;
+                        dst[j] = make_uint4(codes4(gs, v[0], v[1]), codes4(gs, v[2], v[3]), codes4(gs, v[4], v[5]), codes4(gs, v[6], v[7]));
+                    }
+                    if (cq == 0) p.Hs[grow * (p.N / 128) + ti.n0 / 128] = gs.s;
+                }
+            }
+        }
+    } else {
+        setmaxnreg_dec<C::REGS_OTHER>();
+        if (warp == 0) {
+            // ------------------------------------------------------------ producer
+            int s = 0;
+            uint32_t ph = 0;
+            long issued = 0;
+            bool ok = true;
+            ExpertTile ti{};
+            if ((int)blockIdx.x < tiles) ti = expert_tile<C>(p, blockIdx.x);
+            for (int t = blockIdx.x; t < tiles && ok; t += step) {
+                // this lane's copy: rows of X, or one of the two blocks of weight rows
+                const int first = ti.e * p.N * (C::GATED ? 2 : 1) + ti.n0, second = first + (C::GATED ? p.N : 128), m0 = ti.m0;
+                if (t + step < tiles) ti = expert_tile<C>(p, t + step);   // (read a tile ahead)
+                for (int kb = 0; kb < kbs; ++kb) {
+                    const bool got = mbar_wait(&done[s], ph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_TMA_EMPTY);
+                    if (__any_sync(0xffffffffu, !got)) {
+                        ok = false;
+                        break;
+                    }
+                    // one copy at a time executes per thread: each copy of a stage on its own lane
+                    const int c = lane - s * C::COPIES;
+                    if (c == 0) mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
+                    __syncwarp();
+                    uint8_t* dst = stage + s * C::STAGE_BYTES + c * 128 * 128;
+                    if (c == 0) tma_load_2d(dst, &tmX, &full[s], kb * 128, m0);
+                    else if (c == 1 || c == 2) tma_load_2d(dst, &tmW, &full[s], kb * 128, c == 1 ? first : second);
+                    __syncwarp();
+                    ++issued;
+                    if (++s == C::STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (lane == 0) drain_ring(full, issued, C::STAGES, p.err);
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ MMA issuer
+            const uint32_t st0 = smem_u32(stage);
+            int s = 0;
+            uint32_t ph = 0, bph = 0;   // bph: a phase bit per buffer
+            bool ok = true;
+            for (int t = blockIdx.x; t < tiles && ok; t += step) {
+                for (int kb = 0; kb < kbs; ++kb) {
+                    const int buf = kb & (C::NBUF - 1);
+                    const bool got = mbar_wait(&full[s], ph, abort_flag, p.err, DEV_TIMEOUT_TMA_FULL) &&
+                                     mbar_wait(&acc_empty[buf], ((bph >> buf) & 1u) ^ 1u, abort_flag, p.err, DEV_TIMEOUT_ACC_EMPTY);
+                    if (__any_sync(0xffffffffu, !got)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = st0 + (uint32_t)(s * C::STAGE_BYTES);
+                    const uint64_t ad = smem_desc_sw128(sa), bd = smem_desc_sw128(sa + C::A_BYTES);
+                    const uint32_t d = tmem_base + (uint32_t)(buf * C::BUF_COLS);
+                    if (elect_one_sync()) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)   // 32 codes (32 bytes) per MMA
+                            tc_mma_f8(d, ad + (uint64_t)(k * 2), bd + (uint64_t)(k * 2), idesc_e4m3(128, C::BN), k > 0);
+                        tc_commit(&done[s]);
+                    }
+                    __syncwarp();
+                    bph ^= 1u << buf;
+                    if (++s == C::STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (elect_one_sync()) tc_commit(drain);
+            __syncwarp();
+            if (lane == 0) drain_ring(drain, 1, 1, p.err);
+            __syncwarp();
+        } else {
+            // ------------------------------------------------------------ scales
+            const int l = threadIdx.x - 64;
+            int slot = 0;
+            uint32_t sph = 0;
+            bool ok = true;
+            const int nblk = (p.N + 127) / 128;   // weight blocks of an expert (gated: of each half)
+            ExpertTile ti{};
+            if ((int)blockIdx.x < tiles) ti = expert_tile<C>(p, blockIdx.x);
+            for (int t = blockIdx.x; t < tiles && ok; t += step) {
+                const ExpertTile now = ti;
+                if (t + step < tiles) ti = expert_tile<C>(p, t + step);
+                // (a second block past the expert's last is not used: its columns are past N)
+                const int c0 = now.n0 / 128, c1 = C::GATED ? nblk + c0 : min(c0 + 1, nblk - 1);
+                const long b0 = (long)now.e * nblk * (C::GATED ? 2 : 1);
+                for (int kb = 0; kb < kbs; kb += C::SC_KB) {
+                    if (!mbar_wait(&sc_empty[slot], sph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_CONV_EMPTY)) {
+                        ok = false;
+                        break;
+                    }
+                    float* dst = sc + slot * C::SC_KB * C::SC_PITCH;
+#pragma unroll
+                    for (int i = 0; i < 2 * C::SC_KB; ++i) {
+                        const int k = i >> 1, r = (i & 1) * 64 + l;
+                        const bool in = kb + k < kbs && r < now.rows;
+                        cp_async4(dst + k * C::SC_PITCH + r, in ? p.Xs + ((long)now.m0 + r) * kbs + kb + k : p.Xs, in);
+                    }
+                    if (l < 2 * C::SC_KB) {
+                        const int k = l >> 1;
+                        const bool in = kb + k < kbs;
+                        cp_async4(dst + k * C::SC_PITCH + 128 + (l & 1), in ? p.S + (b0 + ((l & 1) ? c1 : c0)) * kbs + kb + k : p.S, in);
+                    }
+                    cp_async_arrive(&sc_full[slot]);
+                    if (++slot == C::SC_SLOTS) {
+                        slot = 0;
+                        sph ^= 1u;
+                    }
+                }
+            }
+            cp_async_wait_all();
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, 512);
+    }
+}
+
+template <class C>
+cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, int sms, int dev, cudaStream_t s) {
+    static PerDevice ready;
+    if (!ready.get(dev)) {
+        cudaError_t e = cudaFuncSetAttribute(fp8a8_experts_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return e;
+        // the warpgroups' register shares add up to the launch's: launch only if the kernel
+        // is allocated exactly that many (a setmaxnreg.inc past the pool waits)
+        cudaFuncAttributes fa{};
+        e = cudaFuncGetAttributes(&fa, fp8a8_experts_kernel<C>);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs != C::REGS) return cudaErrorInvalidConfiguration;
+        ready.set(dev, 1);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1] = {overlap_attribute()};
+    const long tiles = (long)p.max_tiles * p.n_tiles;
+    cfg.gridDim = dim3((unsigned)(tiles < sms ? tiles : sms), 1, 1);
+    cfg.blockDim = dim3(C::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fp8a8_experts_kernel<C>, tx, tw, p);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8a8_experts(const CUtensorMap& tx, const CUtensorMap& tw, Fp8a8Params p, bool gated, int sms, int dev,
+                                 cudaStream_t s) {
+    p.n_tiles = gated ? p.N / 128 : (p.N + 255) / 256;
+    if (gated) return launch<ExpertsCfg<true>>(tx, tw, p, sms, dev, s);
+    if (p.y_unit) return launch<ExpertsCfg<false, true>>(tx, tw, p, sms, dev, s);
+    return launch<ExpertsCfg<false, false>>(tx, tw, p, sms, dev, s);
+}
+
+}  // namespace qmm

@@ -140,11 +140,11 @@ cudaError_t moe_plan(int T, int D, int F, int E, int k, int dev, MoePlan* plan) 
     }
     const double experts = E * (1.0 - std::pow(1.0 - (k < E ? (double)k / E : 1.0), T)), rows = (double)T * k / experts;
     double least = 1e300;
-    MoePlan best{128, 1, 1};
+    MoePlan best{false, 128, 1, 1};
     for (int i = 0; i < 4; ++i) {
         if ((long)T * k / kTn[i] + E > 65535) continue;   // (the tiles are a dimension of the grid)
         const double fill = rows / kTn[i], entries = experts * (fill < 0.5 ? 1.0 : fill + 0.5);
-        MoePlan pl{kTn[i], 1, 1};
+        MoePlan pl{false, kTn[i], 1, 1};
         double total = 0.0;
         for (int gated = 0; gated < 2; ++gated) {
             const int kbs = gated ? (D + 127) / 128 : F / 128, columns = gated ? F / 128 : (D + 127) / 128;
@@ -168,6 +168,7 @@ cudaError_t moe_plan(int T, int D, int F, int E, int k, int dev, MoePlan* plan) 
             best = pl;
         }
     }
+    if (rows > 40) best = MoePlan{true, 128, 1, 1};
     slot = Known{T, D, F, E, k, dev, best};
     *plan = best;
     return cudaSuccess;

@@ -9,6 +9,8 @@
 #include "qmm_internal.h"
 #include "quant8.cuh"
 
+#include <type_traits>
+
 namespace qmm {
 namespace {
 
@@ -158,10 +160,11 @@ __global__ void __launch_bounds__(256) moe_gather_kernel(const uint4* Xq, const 
     }
 }
 
-// Y[t] = R[t] + sum_j w[t][j] Yslot[row[t][j]], j ascending, in fp32; four columns a thread.
-template <int K>
-__global__ void __launch_bounds__(256) moe_combine_kernel(const float4* Yslot, const int32_t* row, const float* w, int k, int vecs,
-                                                          const void* R, int r_bf16, long ldr, void* Y, int y_bf16) {
+// Y[t] = R[t] + sum_j w[t][j] y[row[t][j]], j ascending, in fp32; four columns a thread.
+// HALF: y is fp16 in units of y_unit, one per 64 columns.
+template <int K, bool HALF>
+__global__ void __launch_bounds__(256) moe_combine_kernel(const void* y, const float* y_unit, const int32_t* row, const float* w, int k,
+                                                          int vecs, const void* R, int r_bf16, long ldr, void* Y, int y_bf16) {
     launch_dependents();
     wait_prerequisites();
     const long t = blockIdx.x;
@@ -173,18 +176,32 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const float4* Yslot, c
         ww[j] = j < k ? __ldg(w + t * k + j) : 0.0f;
     }
     for (int i = threadIdx.x; i < vecs; i += 256) {
-        float4 v[K];
+        using V = std::conditional_t<HALF, uint2, float4>;
+        V v[K];
+        float u[K];
 #pragma unroll
-        for (int j = 0; j < K; ++j)
-            if (rr[j] >= 0) v[j] = __ldcs(Yslot + (long)rr[j] * vecs + i);
+        for (int j = 0; j < K; ++j) {
+            if (rr[j] >= 0) {
+                v[j] = __ldcs(static_cast<const V*>(y) + (long)rr[j] * vecs + i);
+                if constexpr (HALF) u[j] = __ldg(y_unit + (long)rr[j] * ((vecs + 15) / 16) + i / 16);
+            }
+        }
         float4 a = R ? load4(R, r_bf16, t * ldr + i * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < K; ++j) {
             if (rr[j] >= 0) {
-                a.x = fmaf(ww[j], v[j].x, a.x);
-                a.y = fmaf(ww[j], v[j].y, a.y);
-                a.z = fmaf(ww[j], v[j].z, a.z);
-                a.w = fmaf(ww[j], v[j].w, a.w);
+                float4 f;
+                float wj = ww[j];
+                if constexpr (HALF) {
+                    const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&v[j].x)), hi = __half22float2(*reinterpret_cast<const __half2*>(&v[j].y));
+                    f = make_float4(lo.x * u[j], lo.y * u[j], hi.x * u[j], hi.y * u[j]);   // (exact)
+                } else {
+                    f = v[j];
+                }
+                a.x = fmaf(wj, f.x, a.x);
+                a.y = fmaf(wj, f.y, a.y);
+                a.z = fmaf(wj, f.z, a.z);
+                a.w = fmaf(wj, f.w, a.w);
             }
         }
         store4(Y, y_bf16, (t * vecs + i) * 4, a);
@@ -234,10 +251,20 @@ cudaError_t launch_moe_gather(const uint8_t* Xq, const float* Xs, int P, int D, 
                   g.offsets + E, D / 16, (D + 127) / 128, reinterpret_cast<uint4*>(Xp), Xps);
 }
 
-cudaError_t launch_moe_combine(const float* Yslot, const int32_t* row, const float* w, int T, int k, int D, const void* R, int r_bf16,
-                               long ldr, void* Y, int y_bf16, cudaStream_t s) {
-    const auto kernel = k <= 2 ? moe_combine_kernel<2> : k <= 4 ? moe_combine_kernel<4> : k <= 8 ? moe_combine_kernel<8> : moe_combine_kernel<16>;
-    return launch(kernel, T, 256, 0, s, reinterpret_cast<const float4*>(Yslot), row, w, k, D / 4, R, r_bf16, ldr, Y, y_bf16);
+template <bool HALF>
+static cudaError_t combine(const void* y, const float* y_unit, const int32_t* row, const float* w, int T, int k, int D, const void* R,
+                           int r_bf16, long ldr, void* Y, int y_bf16, cudaStream_t s) {
+    const auto kernel = k <= 2   ? moe_combine_kernel<2, HALF>
+                        : k <= 4 ? moe_combine_kernel<4, HALF>
+                        : k <= 8 ? moe_combine_kernel<8, HALF>
+                                 : moe_combine_kernel<16, HALF>;
+    return launch(kernel, T, 256, 0, s, y, y_unit, row, w, k, D / 4, R, r_bf16, ldr, Y, y_bf16);
+}
+
+cudaError_t launch_moe_combine(const void* y, const float* y_unit, const int32_t* row, const float* w, int T, int k, int D, const void* R,
+                               int r_bf16, long ldr, void* Y, int y_bf16, cudaStream_t s) {
+    return y_unit ? combine<true>(y, y_unit, row, w, T, k, D, R, r_bf16, ldr, Y, y_bf16, s)
+                  : combine<false>(y, nullptr, row, w, T, k, D, R, r_bf16, ldr, Y, y_bf16, s);
 }
 
 }  // namespace qmm

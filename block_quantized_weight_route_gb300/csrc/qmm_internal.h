@@ -163,6 +163,7 @@ struct Fp8a8Params {
     const int4* tiles;   // {expert, first row, rows, 0}; null: not grouped
     const int* num_tiles;   // on the device
     int max_tiles;       // room in `tiles`
+    float* y_unit;       // [M][ceil(N/64)]: Y is fp16 in these units (null: fp32)
 };
 // Which kernel takes a product: the pair kernel (many tokens) with its tile's columns,
 // or the narrow kernel (few) with its tile's tokens and the CTAs that share its K blocks.
@@ -180,6 +181,7 @@ cudaError_t fp8a8_plan(int M, int K, int N, bool gated, int sms, int dev, Fp8a8P
 // The expert stage's tiles: tokens of a tile, and the CTAs that share the K blocks of one in
 // the gate/up and in the down product.
 struct MoePlan {
+    bool many;           // the kernel for many rows an expert (tiles of 128), else the narrow one
     int tn, cs_gate_up, cs_down;
 };
 cudaError_t moe_plan(int T, int D, int F, int E, int k, int dev, MoePlan* plan);
@@ -188,6 +190,8 @@ bool fp8a8_plans_fit(const Fp8a8Plans& r, int M, int K, int N, bool gated);   //
 cudaError_t fp8a8_narrow_at_once(bool gated, int tn, int cs, int dev, int* clusters);
 cudaError_t launch_fp8a8_narrow(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, bool gated, int tn,
                                 int cs, int dev, cudaStream_t s);
+cudaError_t launch_fp8a8_experts(const CUtensorMap& tx, const CUtensorMap& tw, Fp8a8Params p, bool gated, int sms, int dev,
+                                 cudaStream_t s);
 cudaError_t launch_fp8a8_pair(const CUtensorMap& tx, const CUtensorMap& tw, Fp8a8Params p, bool gated, int bn, int sms,
                               int dev, cudaStream_t s);
 
@@ -206,7 +210,8 @@ struct MoeGroups {
 cudaError_t launch_moe_group(const int32_t* ids, int P, int E, int k, const MoeGroups& g, int dev, cudaStream_t s);
 cudaError_t launch_moe_gather(const uint8_t* Xq, const float* Xs, int P, int D, const MoeGroups& g, int E, uint8_t* Xp, float* Xps,
                               int sms, cudaStream_t s);
-cudaError_t launch_moe_combine(const float* Yslot, const int32_t* row, const float* w, int T, int k, int D, const void* R, int r_bf16,
+// (y_unit: y is fp16 in units of it, as launch_fp8a8_experts writes it; else fp32)
+cudaError_t launch_moe_combine(const void* y, const float* y_unit, const int32_t* row, const float* w, int T, int k, int D, const void* R, int r_bf16,
                                long ldr, void* Y, int y_bf16, cudaStream_t s);
 
 // Routing by scores (route_scored.cu).

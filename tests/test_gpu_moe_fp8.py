@@ -2,7 +2,11 @@
 has to be equal; H within the tolerance of test_gpu_fp8a8's SwiGLU; Y from the H that was stored.
 
 Tolerance of Y: that of each expert's down product (test_gpu_fp8a8) times its weight, and the sum of
-k + 1 terms in fp32, each addition within 2^-24 of the sum of magnitudes; bf16 output half a bf16 step.
+k + 1 terms in fp32, each addition within 2^-24 of the sum of magnitudes; bf16 output half a bf16 step,
+and each expert's row then perhaps held as fp16 in units that bring the largest of 64 columns to
+2^14 .. 2^15.  fp16 has 11 significant bits: the step in [2^e, 2^(e+1)) is 2^(e-10), half of it at most
+2^-11 of the value; below 2^-14 the step is 2^-24, half of it 2^-25 of a unit, a unit at most 2^-14 of
+the largest: 2^-39 of that.
 """
 import numpy as np
 import pytest
@@ -104,6 +108,8 @@ def check(q, seed, T, D, F, E, k, how="even", dt=F32, res=None, weights=None):
         p = np.array(order[a:b])
         np.add.at(y, p // k, wf[p][:, None] * v)
         np.add.at(size, p // k, np.abs(wf[p][:, None] * v))
+        if dt == BF16:
+            d = d + 2.0 ** -11 * (np.abs(v) + d) + 2.0 ** -39 * np.abs(v).max(1, keepdims=True)
         np.add.at(tol, p // k, np.abs(wf[p])[:, None] * d)
     tol += (k + 1) * 2.0 ** -24 * (size + tol)
     if dt == BF16:

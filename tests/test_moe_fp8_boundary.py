@@ -87,12 +87,12 @@ def test_stage(L, kw, st):
 def test_workspace(L):
     f = L.moe_expert_stage_fp8_workspace_size
     assert f(4, 200, 128, 8, 2) == 0 and f(-1, 256, 128, 8, 2) == 0 and f(4, 256, 128, 8, 17) == 0
-    off = (sz * 13)()
+    off = (sz * 14)()
     for T, D, F, E, k in [(0, 256, 128, 8, 2), (1, 16, 128, 1, 1), (300, 2048, 768, 128, 8), (2 ** 18, 256, 128, 512, 16)]:
         assert L.moe_expert_stage_fp8_workspace_layout(T, D, F, E, k, ctypes.cast(off, P)) == 0
         offs, pairs = list(off), T * k
         sizes = [E * 4, E * 4 + 4, pairs * 4, pairs * 4, -(-pairs // 2048) * E * 4, None, 4, pairs * D, pairs * -(-D // 128) * 4, pairs * F,
-                 pairs * (F // 128) * 4, pairs * D * 4]
+                 pairs * (F // 128) * 4, pairs * D * 4, pairs * -(-D // 64) * 4]
         assert offs == sorted(offs) and all(o % 256 == 0 for o in offs) and offs[-1] == f(T, D, F, E, k)
         for i, n in enumerate(sizes):
             assert n is None or offs[i + 1] - offs[i] >= n
