@@ -1259,12 +1259,16 @@ qmm_status moe_expert_stage_fp8(const uint8_t* Xq, const float* Xs, const int32_
         p.tiles = g.tiles;
         p.num_tiles = g.num_tiles;
         p.max_tiles = g.max_tiles;
-        CUtensorMap tx, tw;
-        if ((st = make_tmap(&tx, p.Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, P, p.K, 128, plan.tn, CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK ||
-            (st = make_tmap(&tw, p.W, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, (uint64_t)E * p.N * (gated ? 2 : 1), p.K, 128, 128,
-                            CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK)
+        CUtensorMap tx, tw, ty;
+        memset(&ty, 0, sizeof ty);
+        if (!gated && y_unit &&
+            (st = make_tmap(&ty, y, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, D, P, (uint64_t)D * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK)
             return st;
-        e = plan.many ? launch_fp8a8_experts(tx, tw, p, gated, d->sms, d->index, stream)
+        if ((st = make_tmap(&tx, p.Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, P, p.K, 128, plan.tn, CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK ||
+            (st = make_tmap(&tw, p.W, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, (uint64_t)E * p.N * (gated ? 2 : 1), p.K, 128,
+                            plan.many && gated ? 64 : 128, CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK)
+            return st;
+        e = plan.many ? launch_fp8a8_experts(tx, tw, ty, p, gated, d->sms, d->index, stream)
                       : launch_fp8a8_narrow(tx, tw, p, gated, plan.tn, gated ? plan.cs_gate_up : plan.cs_down, d->index, stream);
         if (e != cudaSuccess) return cuda_fail(e, gated ? "moe_expert_stage_fp8: gate/up" : "moe_expert_stage_fp8: down");
     }

@@ -94,6 +94,17 @@ __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, i
                  : "memory");
 }
 
+// A box of shared memory to global memory, in this thread's bulk group; and the wait until its
+// groups have been read from shared memory, or are complete.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* smem_src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(smem_src)), "r"(x), "r"(y)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // Wait (bounded) for the completion of the `issued` most recent fills of a ring.
 __device__ __forceinline__ void drain_ring(uint64_t* full, long issued, int stages, uint32_t* err) {
     const long pending = issued < stages ? issued : stages;
@@ -118,6 +129,18 @@ __device__ __forceinline__ void drain_ring(uint64_t* full, long issued, int stag
 __device__ __forceinline__ float swiglu(float g, float u) {
     const float t = __expf(-fabsf(g));
     return __fdividef(g < 0.0f ? g * t : g, 1.0f + t) * u;
+}
+
+// Two at once: the two quotients share one reciprocal, 1 / (d0 d1) with d = 1 + t in [1, 2] (the
+// reciprocals and exponentials are what bounds a tile's SwiGLU: 8 cycles each a warp).
+__device__ __forceinline__ uint64_t swiglu2(uint64_t g2, uint64_t u2) {
+    const float2 g = unpack2(g2);
+    const float t0 = __expf(-fabsf(g.x)), t1 = __expf(-fabsf(g.y));
+    const float d0 = 1.0f + t0, d1 = 1.0f + t1;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d0 * d1));
+    const uint64_t n = mul2(mul2(g2, pack2(g.x < 0.0f ? t0 : 1.0f, g.y < 0.0f ? t1 : 1.0f)), u2);
+    return mul2(n, mul2(pack2(r, r), pack2(d1, d0)));
 }
 
 // The activations of the product's epilogue (qmm_act's order).  With t = exp(-|z|) <= 1, v times the logistic

@@ -190,8 +190,9 @@ bool fp8a8_plans_fit(const Fp8a8Plans& r, int M, int K, int N, bool gated);   //
 cudaError_t fp8a8_narrow_at_once(bool gated, int tn, int cs, int dev, int* clusters);
 cudaError_t launch_fp8a8_narrow(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, bool gated, int tn,
                                 int cs, int dev, cudaStream_t s);
-cudaError_t launch_fp8a8_experts(const CUtensorMap& tx, const CUtensorMap& tw, Fp8a8Params p, bool gated, int sms, int dev,
-                                 cudaStream_t s);
+// (ty: the fp16 rows, boxes of 32 rows x 64 columns; not read where they are fp32)
+cudaError_t launch_fp8a8_experts(const CUtensorMap& tx, const CUtensorMap& tw, const CUtensorMap& ty, Fp8a8Params p, bool gated, int sms,
+                                 int dev, cudaStream_t s);
 cudaError_t launch_fp8a8_pair(const CUtensorMap& tx, const CUtensorMap& tw, Fp8a8Params p, bool gated, int bn, int sms,
                               int dev, cudaStream_t s);
 

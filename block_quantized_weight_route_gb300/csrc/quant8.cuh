@@ -108,6 +108,9 @@ struct GroupScale {
     float s, inv, up;
     __device__ __forceinline__ bool tiny() const { return up != 1.0f; }
     __device__ __forceinline__ float operator()(float y) const { return y * up * inv; }
+    __device__ __forceinline__ uint64_t two(uint64_t y) const {   // (the same quotients)
+        return tiny() ? mul2(mul2(y, pack2(up, up)), pack2(inv, inv)) : mul2(y, pack2(inv, inv));
+    }
 };
 template <int LEVELS>
 __device__ __forceinline__ GroupScale group_scale(float top) {
