@@ -143,16 +143,63 @@ __device__ __forceinline__ uint64_t swiglu2(uint64_t g2, uint64_t u2) {
     return mul2(n, mul2(pack2(r, r), pack2(d1, d0)));
 }
 
-// The activations of the product's epilogue (qmm_act's order).  With t = exp(-|z|) <= 1, v times the logistic
-// function of z is v / (1 + t), or v t / (1 + t) for negative z: nothing overflows, and the fast
-// exponential's error falls with t.  The normal distribution's tail comes from erfc, where 1 + erf would cancel.
-__device__ __forceinline__ float activate(float v, int act) {
+// The activations of the product's epilogue (qmm_act's order).  silu and tanh's gelu are v times
+// the logistic function of z: with t = exp(-|z|) <= 1, v / (1 + t), or v t / (1 + t) for negative
+// z: nothing overflows, and the fast exponential's error falls with t.  erf's gelu is v times the
+// normal distribution, whose tail is half of erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + p x)
+// (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26: within 1.5e-7): as exact as fp32
+// in the sum, a third of the instructions of erfcf, and no cancellation in the tail.
+// Columns n and n + 1 (n even) share a reciprocal, that of both denominators' product.
+// v or v t, and the denominator (finite also for a NaN or an infinity, which stay in their column)
+__device__ __forceinline__ float act_parts(float v, int act, float* d) {
+    if (act == 3) {
+        *d = fminf(fmaf(0.23164190f, fabsf(v), 1.0f), 1e18f);   // 0.3275911 / sqrt 2
+        return v;
+    }
+    const float z = act == 2 ? v : 1.5957691216f * v * fmaf(0.044715f * v, v, 1.0f);   // 2 sqrt(2 / pi) (v + 0.044715 v^3)
+    const float t = fminf(__expf(-fabsf(z)), 1.0f);
+    *d = 1.0f + t;
+    return z < 0.0f ? v * t : v;
+}
+// The activation from these and the denominator's reciprocal.
+__device__ __forceinline__ float act_finish(float x, float r, int act) {
+    if (act != 3) return x * r;
+    const float q = r * fmaf(r, fmaf(r, fmaf(r, fmaf(r, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
+    const float h = 0.5f * fminf(x, 1e18f) * (q * __expf(-0.5f * x * x));   // x Phi(-|x|)
+    return x < 0.0f ? h : x - h;
+}
+__device__ __forceinline__ float reciprocal(float d) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    return r;
+}
+template <int ACT>
+__device__ __forceinline__ float4 activate4(float4 v) {
+    float d[4];
+    const float4 x = make_float4(act_parts(v.x, ACT, d), act_parts(v.y, ACT, d + 1), act_parts(v.z, ACT, d + 2), act_parts(v.w, ACT, d + 3));
+    const float r = reciprocal(d[0] * d[1]), s = reciprocal(d[2] * d[3]);
+    return make_float4(act_finish(x.x, r * d[1], ACT), act_finish(x.y, r * d[0], ACT), act_finish(x.z, s * d[3], ACT),
+                       act_finish(x.w, s * d[2], ACT));
+}
+__device__ __forceinline__ float4 relu4(float4 v) {
+    return make_float4(max_nan(v.x, 0.0f), max_nan(v.y, 0.0f), max_nan(v.z, 0.0f), max_nan(v.w, 0.0f));
+}
+__device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+// f(a function of four values) for the activation `act`, not QMM_ACT_NONE
+template <class F>
+__device__ __forceinline__ void with_activation(int act, F f) {
+    if (act == 1) f([](float4 v) { return relu4(v); });
+    else if (act == 2) f([](float4 v) { return activate4<2>(v); });
+    else if (act == 3) f([](float4 v) { return activate4<3>(v); });
+    else f([](float4 v) { return activate4<4>(v); });
+}
+// The same with a column a lane.
+__device__ __forceinline__ float activate_lanes(float v, int act) {
     if (act == 0) return v;
     if (act == 1) return max_nan(v, 0.0f);
-    if (act == 3) return 0.5f * v * erfcf(-0.70710678f * v);
-    const float z = act == 2 ? v : 1.5957691216f * v * fmaf(0.044715f * v, v, 1.0f);   // 2 sqrt(2 / pi) (v + 0.044715 v^3)
-    const float t = __expf(-fabsf(z));
-    return __fdividef(z < 0.0f ? v * t : v, 1.0f + t);
+    float d;
+    const float x = act_parts(v, act, &d), d2 = __shfl_xor_sync(0xffffffffu, d, 1);
+    return act_finish(x, reciprocal(d * d2) * d2, act);
 }
 
 // act(y + bias) + R of row m, columns n .. n + 3 (what is past the end stays as it is).
@@ -162,19 +209,19 @@ __device__ __forceinline__ float4 epilogue4(const Fp8a8Params& p, long m, int n,
         if (n >= p.N) return y;
         if (p.bias) b = load4(p.bias, p.bias_bf16, n);
         if (p.R) r = load4(p.R, p.r_bf16, m * p.ldr + n);
-        return make_float4(activate(y.x + b.x, p.act) + r.x, activate(y.y + b.y, p.act) + r.y, activate(y.z + b.z, p.act) + r.z,
-                           activate(y.w + b.w, p.act) + r.w);
-    }
-    float v[4] = {y.x, y.y, y.z, y.w};
+    } else {
+        float bb[4] = {}, rr[4] = {};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (n + j < p.N) {
-            if (p.bias) v[j] += load1(p.bias, p.bias_bf16, n + j);
-            v[j] = activate(v[j], p.act);
-            if (p.R) v[j] += load1(p.R, p.r_bf16, m * p.ldr + n + j);
+        for (int j = 0; j < 4; ++j) {
+            if (p.bias && n + j < p.N) bb[j] = load1(p.bias, p.bias_bf16, n + j);
+            if (p.R && n + j < p.N) rr[j] = load1(p.R, p.r_bf16, m * p.ldr + n + j);
         }
+        b = make_float4(bb[0], bb[1], bb[2], bb[3]);
+        r = make_float4(rr[0], rr[1], rr[2], rr[3]);
     }
-    return make_float4(v[0], v[1], v[2], v[3]);
+    y = add4(y, b);
+    if (p.act) with_activation(p.act, [&](auto act) { y = act(y); });
+    return add4(y, r);
 }
 
 // The column, inside the tile, of a fold thread's column i, for column group cq:
@@ -289,66 +336,107 @@ __device__ __forceinline__ void store_columns(const Fp8a8Params& p, uint8_t* stg
     }
 }
 
-// store_columns with the epilogue: 32 columns at a time as fp32 through the staging (32 rows x 128 bytes),
-// then, coalesced, the bias, the activation and the residual's rows, and the rounding.
-// VEC: eight lanes a row, four columns each, a row's eight residual loads in flight before
-// the first store (R may be Y, so the compiler would not move them past it).  Else a column a lane, a
-// row at a time.
-template <bool BF16, bool VEC>
-__device__ __forceinline__ void store_epilogue(const Fp8a8Params& p, uint8_t* stg, int lane, long row0, int col0,
+// The epilogue's bias for a fold warp's COLS columns, on its way to shared memory (COLS floats) while
+// the tile's K blocks are folded; past the end zeros.  And the residual's rows on theirs to L2.
+template <int COLS>
+__device__ __forceinline__ void prefetch_epilogue(const Fp8a8Params& p, float* bias, int lane, long row0, int col0) {
+    if (p.bias) {
+        const int esz = p.bias_bf16 ? 2 : 4, n = col0 + lane * (16 / esz);
+        if (lane * 16 < COLS * esz) {
+            const int left = (p.N - n) * esz, bytes = left < 0 ? 0 : left < 16 ? left : 16;
+            const uint8_t* src = static_cast<const uint8_t*>(p.bias) + (bytes ? (long)n * esz : 0);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(reinterpret_cast<uint8_t*>(bias) + lane * 16)), "l"(src),
+                         "r"(bytes)
+                         : "memory");
+        }
+    }
+    if (p.R && row0 + lane < p.M) {
+        const int esz = p.r_bf16 ? 2 : 4, cols = p.N - col0 < COLS ? p.N - col0 : COLS;
+        const uint8_t* a = static_cast<const uint8_t*>(p.R) + ((row0 + lane) * p.ldr + col0) * esz;
+        for (int x = 0; x < cols * esz; x += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(a + x) : "memory");
+    }
+}
+
+// store_columns with the epilogue: CH columns at a time as fp32 through the staging (CH / 32 parts of 32 rows x
+// 128 bytes), then, coalesced, the bias, the activation and the residual's rows, and the rounding.
+// VEC: eight lanes a row, four columns each.  A row's eight residual loads and its sums are in registers before the
+// first store (R may be Y, and a store through a plain pointer could be to shared memory: the compiler
+// would not move them past it).  Else a column a lane.
+// The loops over the parts and in the activation are not unrolled: the code, many times over, does not
+// fit the instruction cache.
+template <bool BF16, bool VEC, int COLS, int CH>
+__device__ __forceinline__ void store_epilogue(const Fp8a8Params& p, uint8_t* stg, const float* bias, int lane, long row0, int col0,
                                                const uint64_t* v) {
+    cp_async_wait_all();
 #pragma unroll
-    for (int c0 = 0; c0 < 64; c0 += 32) {
+    for (int c0 = 0; c0 < COLS; c0 += CH) {
         __syncwarp();
-        stage16<false>(stg, lane, 0, v + c0 / 2);
-        stage16<false>(stg, lane, 4, v + c0 / 2 + 8);
+#pragma unroll
+        for (int h = 0; h < CH / 32; ++h) {
+            stage16<false>(stg + h * 4096, lane, 0, v + (c0 + h * 32) / 2);
+            stage16<false>(stg + h * 4096, lane, 4, v + (c0 + h * 32) / 2 + 8);
+        }
         __syncwarp();
-        const int col = col0 + c0;
-        if constexpr (VEC) {
-            const int c = lane % 8, n = col + 4 * c;
-            if (n < p.N) {
-                float4 b = make_float4(0.f, 0.f, 0.f, 0.f), r[8];
-                if (p.bias) b = load4(p.bias, p.bias_bf16, n);
+#pragma unroll 1
+        for (int h = 0; h < CH / 32; ++h) {
+            uint8_t* part = stg + h * 4096;
+            if constexpr (VEC) {
+                const int c = lane % 8, n = col0 + c0 + 32 * h + 4 * c;
+                const bool in = n < p.N;
+                float4 r[8], b = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const long m = row0 + i * 4 + lane / 8;
                     r[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (p.R && m < p.M) r[i] = load4(p.R, p.r_bf16, m * p.ldr + n);
+                    if (p.R && in && m < p.M) r[i] = load4(p.R, p.r_bf16, m * p.ldr + n);
+                }
+                if (p.bias) b = load4(bias, p.bias_bf16, c0 + 32 * h + 4 * c);
+                auto at = [&](int i) {   // (this lane's alone)
+                    const int q = i * 4 + lane / 8;
+                    return reinterpret_cast<float4*>(part + (q * 8 + (c ^ (q & 7))) * 16);
+                };
+                if (p.act) {
+                    with_activation(p.act, [&](auto act) {
+#pragma unroll 1
+                        for (int i = 0; i < 8; ++i) *at(i) = act(add4(*at(i), b));
+                    });
+                    b = make_float4(0.f, 0.f, 0.f, 0.f);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int q = i * 4 + lane / 8;
-                    const long m = row0 + q;
-                    if (m < p.M) {
-                        const float4 y = *reinterpret_cast<const float4*>(stg + (q * 8 + (c ^ (q & 7))) * 16);
-                        const float o[4] = {activate(y.x + b.x, p.act) + r[i].x, activate(y.y + b.y, p.act) + r[i].y,
-                                            activate(y.z + b.z, p.act) + r[i].z, activate(y.w + b.w, p.act) + r[i].w};
-                        if constexpr (BF16) {
-                            const __nv_bfloat162 lo = __floats2bfloat162_rn(o[0], o[1]), hi = __floats2bfloat162_rn(o[2], o[3]);
-                            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.Y) + m * p.N + n) =
-                                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-                        } else {
-                            *reinterpret_cast<float4*>(static_cast<float*>(p.Y) + m * p.N + n) = make_float4(o[0], o[1], o[2], o[3]);
-                        }
+                for (int i = 0; i < 8; ++i) r[i] = add4(add4(*at(i), b), r[i]);
+                if (in) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const long m = row0 + i * 4 + lane / 8;
+                        if (m < p.M) store4(p.Y, BF16, m * p.N + n, r[i]);
                     }
                 }
-            }
-        } else {
-            const int n = col + lane, rows = p.M - row0 < 32 ? (int)(p.M - row0) : 32;
-            if (n < p.N) {
-                const float b = p.bias ? load1(p.bias, p.bias_bf16, n) : 0.0f;
+            } else {
+                const int n = col0 + c0 + 32 * h + lane, rows = p.M - row0 < 32 ? (int)(p.M - row0) : 32;
+                const bool in = n < p.N;
+                const float b = p.bias ? load1(bias, p.bias_bf16, c0 + 32 * h + lane) : 0.0f;
+#pragma unroll 1
                 for (int q0 = 0; q0 < rows; q0 += 8) {
                     float r[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) r[i] = p.R && q0 + i < rows ? load1(p.R, p.r_bf16, (row0 + q0 + i) * p.ldr + n) : 0.0f;
+                    for (int i = 0; i < 8; ++i) r[i] = p.R && in && q0 + i < rows ? load1(p.R, p.r_bf16, (row0 + q0 + i) * p.ldr + n) : 0.0f;
+#pragma unroll 1
+                    for (int i = 0; p.act && i < 8; ++i) {   // (of 32 rows staged)
+                        const int q = q0 + i;
+                        float* at = reinterpret_cast<float*>(part + (q * 8 + ((lane / 4) ^ (q & 7))) * 16) + lane % 4;
+                        *at = activate_lanes(*at + b, p.act);
+                    }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int q = q0 + i;
-                        if (q < rows) {
-                            const float y = reinterpret_cast<const float*>(stg + (q * 8 + ((lane / 4) ^ (q & 7))) * 16)[lane % 4];
-                            const float o = activate(y + b, p.act) + r[i];
-                            if constexpr (BF16) static_cast<__nv_bfloat16*>(p.Y)[(row0 + q) * p.N + n] = __float2bfloat16_rn(o);
-                            else static_cast<float*>(p.Y)[(row0 + q) * p.N + n] = o;
+                        r[i] += reinterpret_cast<const float*>(part + (q * 8 + ((lane / 4) ^ (q & 7))) * 16)[lane % 4] + (p.act ? 0.0f : b);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const long at = (row0 + q0 + i) * p.N + n;
+                        if (in && q0 + i < rows) {
+                            if constexpr (BF16) static_cast<__nv_bfloat16*>(p.Y)[at] = __float2bfloat16_rn(r[i]);
+                            else static_cast<float*>(p.Y)[at] = r[i];
                         }
                     }
                 }

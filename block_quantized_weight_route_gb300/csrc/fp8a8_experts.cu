@@ -22,20 +22,16 @@ template <bool GATED_, bool HALF_ = false>
 struct ExpertsCfg {
     static constexpr bool GATED = GATED_, HALF = HALF_;
     static constexpr int BN = 256, A_BYTES = 128 * 128, B_BYTES = BN * 128, STAGE_BYTES = A_BYTES + B_BYTES;
-#ifndef EX_CW
-#define EX_CW 128
-#define EX_LW 64
-#define EX_RF 216
-#define EX_RO 72
-#endif
-    static constexpr int CW = EX_CW, GROUPS = BN / CW, FOLD_WARPS = 4 * GROUPS, LW = EX_LW;
+    // Fold threads: a row and 128 columns, 64 of them a TMEM load.  (16 warps of 64 columns, whose
+    // registers hold loads of 8 or 16: 4 and 3% slower at 5268 tokens of 2048 columns.)
+    static constexpr int CW = 128, GROUPS = BN / CW, FOLD_WARPS = 4 * GROUPS, LW = 64;
     static constexpr int STAGING = CW * 64;   // of a fold warp, for its outputs
     static constexpr int OUT_BYTES = GATED ? 2 * GROUPS * 128 * 4 : FOLD_WARPS * STAGING;   // row maxima, or output staging
     static constexpr int STAGES = GATED ? 4 : 3, NBUF = 2, BUF_COLS = 256;   // a buffer holds both halves
     // Ring of scales: slots of SC_KB K blocks, which is also how many the fold loop unrolls
     // (gate/up unrolled by eight spills); a slot holds the tile's first row and its rows too.
     static constexpr int SC_KB = GATED ? 4 : 8, SC_SLOTS = 16 / SC_KB, SC_PITCH = 128 + 4, SC_FLOATS = SC_SLOTS * SC_KB * SC_PITCH;
-    static constexpr int THREADS = 128 + 32 * FOLD_WARPS, REGS = 65536 / THREADS / 8 * 8, REGS_FOLD = EX_RF, REGS_OTHER = EX_RO;
+    static constexpr int THREADS = 128 + 32 * FOLD_WARPS, REGS = 65536 / THREADS / 8 * 8, REGS_FOLD = 216, REGS_OTHER = 72;
     static_assert(REGS_FOLD * 32 * FOLD_WARPS + REGS_OTHER * 128 == REGS * THREADS, "register shares = launch registers");
     static_assert(GROUPS == 2, "a fold group for each half of the columns");
     static constexpr int W_ROWS = GATED ? 64 : 128, COPIES = 1 + BN / W_ROWS;   // rows of a weight copy; copies of a stage

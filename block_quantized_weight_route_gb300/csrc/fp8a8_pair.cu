@@ -44,9 +44,9 @@ struct PairCfg {
     static constexpr int BN = BN_;
     static constexpr bool GATED = GATED_, RAGGED = RAGGED_, BF16 = BF16_, EPI = EPI_;
     static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / 2 * 128, STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGING = 4096;   // of a fold warp, for its outputs
+    static constexpr int STAGING = EPI ? 8192 : 4096;   // of a fold warp, for its outputs
     // 160 KB of operands (256 columns to a product: 128 KB beside the 64 KB of staging, as fast)
-    static constexpr int STAGES = (!GATED && BN == 256 ? 131072 : 163840) / STAGE_BYTES;
+    static constexpr int STAGES = (!GATED && (BN == 256 || EPI) ? 131072 : 163840) / STAGE_BYTES;
     static constexpr int NBUF = BN <= 128 ? 4 : 2, BUF_COLS = 512 / NBUF;
     // Ring of scales: slots of SC_KB K blocks, which is also how many the fold loop unrolls: the
     // loop's end moves sums between registers (131 instructions a K block unrolled by four,
@@ -59,13 +59,17 @@ struct PairCfg {
     // with loads of 32 at 256 x 17408 x 5120; 12 warps: 32); 16 warps need more than an even
     // share of the registers for their sums (a register split) and loads of 8 (gate/up with
     // loads of 16: 15% slower at 2048 x 5120 x 2 x 17408).
-    static constexpr int CW = 64, GROUPS = BN / CW, FOLD_WARPS = 4 * GROUPS, LW = BN == 256 ? 8 : BN == 192 ? 32 : 64;
+    // With the epilogue: 8 warps of 128 columns at BN = 256, which leaves registers for it (16 warps
+    // spill in the K loop: 292 us in place of XXX at 2048 x 5120 x 17408 with bias and GELU).
+    static constexpr bool WIDE = EPI && BN == 256;
+    static constexpr int CW = WIDE ? 128 : 64, GROUPS = BN / CW, FOLD_WARPS = 4 * GROUPS, LW = WIDE ? 64 : BN == 256 ? 8 : BN == 192 ? (EPI ? 16 : 32) : 64;
     static constexpr int OUT_BYTES = GATED ? 2 * GROUPS * 128 * 4 : FOLD_WARPS * STAGING;   // row maxima, or output staging
     static constexpr bool REG_SPLIT = BN == 256;
-    static constexpr int THREADS = 128 + 32 * FOLD_WARPS, REGS = 65536 / THREADS / 8 * 8, REGS_FOLD = 104, REGS_OTHER = 64;
+    static constexpr int THREADS = 128 + 32 * FOLD_WARPS, REGS = 65536 / THREADS / 8 * 8, REGS_FOLD = WIDE ? 216 : 104, REGS_OTHER = WIDE ? 72 : 64;
     static_assert(!REG_SPLIT || REGS_FOLD * 32 * FOLD_WARPS + REGS_OTHER * 128 == REGS * THREADS, "register shares = launch registers");
     static constexpr int BARS = 2 * STAGES + NBUF + 2 * SC_SLOTS + 3;
-    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + OUT_BYTES + SC_FLOATS * 4 + BARS * 8 + 64;
+    static constexpr int BIAS_FLOATS = EPI ? FOLD_WARPS * CW : 0;   // the fold warps' columns of the bias
+    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + OUT_BYTES + (SC_FLOATS + BIAS_FLOATS) * 4 + BARS * 8 + 64;
     static_assert(SMEM <= 232448, "shared memory");
     static_assert(!GATED || BN == 256, "gate/up: 128 + 128 columns");
     static_assert(NBUF <= STAGES, "a stage's MMA barrier completes again only after its accumulator was read");
@@ -98,7 +102,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
     uint8_t* outs = stage + C::STAGES * C::STAGE_BYTES;         // output staging of the fold warps
     float* rowmax = reinterpret_cast<float*>(outs);              // gated: [tile parity][quarter][128]
     float* sc = reinterpret_cast<float*>(outs + C::OUT_BYTES);   // [slot][kb][128 rows, 2 weight blocks]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sc + C::SC_FLOATS);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sc + C::SC_FLOATS + C::BIAS_FLOATS);
     uint64_t* full = bars;                    // even CTA's: both CTAs' operands of a stage have landed
     uint64_t* done = full + C::STAGES;        // a stage's MMAs are complete: its operands are free, its P is in TMEM
     uint64_t* acc_empty = done + C::STAGES;   // even CTA's: both CTAs' fold warps have read the buffer
@@ -156,6 +160,12 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
             // which of the tile's two weight blocks the thread's 64 columns are in (gated: the
             // first half in one, the second in the other)
             const int blk = !C::GATED && cq * C::CW >= 128 - (pair_tile<C>(p, t, crank).n0 & 127);
+            float* bias = sc + C::SC_FLOATS + (warp - 4) * C::CW;
+            if constexpr (C::EPI) {
+                const PairTile ti = pair_tile<C>(p, t, crank);
+                __syncwarp();   // (the bias of the tile before has been read)
+                prefetch_epilogue<C::CW>(p, bias, lane, (long)ti.m0 + q * 32, ti.n0 + fold_col<C>(cq, 0));
+            }
             uint64_t acc[C::CW / 2];
 #pragma unroll
             for (int j = 0; j < C::CW / 2; ++j) acc[j] = 0;
@@ -209,7 +219,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
             const PairTile ti = pair_tile<C>(p, te, crank);
             if constexpr (!C::GATED) {
                 uint8_t* stg = outs + (warp - 4) * C::STAGING;
-                if constexpr (C::EPI) store_epilogue<C::BF16, !C::RAGGED>(p, stg, lane, (long)ti.m0 + q * 32, ti.n0 + fold_col<C>(cq, 0), acc);
+                if constexpr (C::EPI) store_epilogue<C::BF16, !C::RAGGED, C::CW, C::STAGING / 128>(p, stg, bias, lane, (long)ti.m0 + q * 32, ti.n0 + fold_col<C>(cq, 0), acc);
                 else store_columns<C::BF16, C::RAGGED, C::BN == 256 ? 4 : 8>(p, stg, lane, (long)ti.m0 + q * 32, ti.n0 + fold_col<C>(cq, 0), acc);
             } else {
                 // the first half of acc: gate columns; the second half: the same columns of up

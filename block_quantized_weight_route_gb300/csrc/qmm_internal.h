@@ -226,6 +226,7 @@ struct ScoredParams {
     int groups, groups_kept, group_top;
     int group_size;      // E / groups, and 2^20 / group_size rounded up (set by the launcher)
     unsigned group_inv;
+    int per_shift;       // lanes that share a group, as a power of two (set by the launcher)
     int renorm;
     float scale;
     int32_t* ids;        // [T][k]

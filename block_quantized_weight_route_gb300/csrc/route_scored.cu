@@ -10,7 +10,8 @@
 // and the logits themselves are compared; else c is computed in 32 bits with a bound on its
 // error, and a token with two neighbours in the order closer than that is done again in 64
 // bits (one in some hundred tokens of random logits).  Each of the k rounds is two warp
-// reductions (redux): the largest key, then the lowest index that has it.
+// reductions (redux): the largest key, then the lowest index that has it; a lane keeps its
+// keys sorted, so that the next one is in hand.
 #include <cfloat>
 
 #include "qmm_internal.h"
@@ -41,42 +42,58 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
     const uint32_t lo = __reduce_max_sync(kAll, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
     return (uint64_t)hi << 32 | lo;
 }
+template <int LANES = 32>   // (of the first LANES, and the rest among themselves)
 __device__ __forceinline__ float warp_max_f(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    for (int o = LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
     return v;
 }
-template <class F>
+template <int LANES = 32, class F>
 __device__ __forceinline__ F warp_sum(F v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
     return v;
 }
 
+__device__ __forceinline__ float live_logit(float v) { return v == v ? v : -INFINITY; }   // (NaN: off, as -inf)
 __device__ __forceinline__ float logit(const ScoredParams& p, long t, int e) {
     const long i = t * p.ldl + e;
-    const float v = p.l_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.logits)[i]) : static_cast<const float*>(p.logits)[i];
-    return v == v ? v : -INFINITY;   // (NaN: off, as -inf)
+    return live_logit(p.l_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.logits)[i]) : static_cast<const float*>(p.logits)[i]);
 }
 
 // exp(l) / (1 + exp(l)) from the side where nothing overflows, times exp(-shift) for l <= 0.
 __device__ __forceinline__ float sigmoid(float l, float shift) {
     const float t = expf(-fabsf(l));
-    return (l > 0.0f ? 1.0f : shift == 0.0f ? t : expf(l - shift)) / (1.0f + t);
+    return __fdividef(l > 0.0f ? 1.0f : shift == 0.0f ? t : expf(l - shift), 1.0f + t);
 }
+// The same for the choice.  2^(-|l| log2 e) by the exponential instruction is within 2 ulp and, for its
+// rounded argument, 1.2 |l| ulp more, which exp(-|l|) / (1 + exp(-|l|))^2, the slope, brings below 7e-8
+// for any l; the sum's rounding and the approximate reciprocal add 1.8e-7: within 2.5e-7 of the sigmoid.
+__device__ __forceinline__ float fast_sigmoid(float l) {
+    float t, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fabsf(l) * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
+    return l > 0.0f ? r : t * r;
+}
+constexpr float kSigmoidTol = 5e-7f;      // of the difference of two
+constexpr float kSoftmaxTol = 3.9e-6f;    // the same, of the largest score: an exponential and a sum of 16 and then 32 terms
+constexpr float kSumTol = 2.4e-7f;        // of a sum's size: the bias' addition, twice
 
-// The groups that stay, as a mask; `c` holds the row's values (-inf: off).  Lanes share the groups
-// evenly; `tol` (32 bits): *close is set where a group that stays and one that goes are no
-// further apart than their error.
+// Where a row's expert e is kept in shared memory: groups of 32 start in different banks.
+__device__ __forceinline__ int place(int e) { return e + (e >> 5) * 4; }
+
+// The groups that stay, as the ballot of their lanes: the lanes share the groups, 2^p.per_shift
+// each.  `c` holds the row's values (-inf: off); `tol` (32 bits): *close is set where the last
+// group that stays and the first that goes are no further apart than their error.
 template <class F>
 __device__ __forceinline__ uint32_t groups_kept(const ScoredParams& p, const F* c, int lane, float tol, bool* close) {
-    const int p2 = p.groups <= 1 ? 1 : 1 << (32 - __clz(p.groups - 1)), per = 32 / p2;   // lanes a group
-    const int g = lane / per, sub = lane % per;
+    const int per = 1 << p.per_shift, g = lane >> p.per_shift, sub = lane & (per - 1);
+    const bool live = g < p.groups;
     F a = -INFINITY, b = -INFINITY;   // the two largest
-    if (g < p.groups) {
-        const F* row = c + g * p.group_size;
-        for (int i = sub; i < p.group_size; i += per) {
-            const F v = row[i];
+    if (live) {
+        const int end = (g + 1) * p.group_size;
+        for (int e = g * p.group_size + sub; e < end; e += per) {
+            const F v = c[place(e)];
             b = fmax(b, fmin(a, v));
             a = fmax(a, v);
         }
@@ -87,32 +104,37 @@ __device__ __forceinline__ uint32_t groups_kept(const ScoredParams& p, const F* 
         a = fmax(a, a2);
     }
     const F score = p.group_top == 1 ? a : b > -INFINITY ? a + b : (F)-INFINITY;
-    int before = 0;
-    for (int h = 0; h < p.groups; ++h) {
-        const F s = __shfl_sync(kAll, score, h * per);
-        before += s > score || (s == score && h < g);
+    auto key = live && sub == 0 ? key_of(score) : 0;   // (a live group's is not 0)
+    uint32_t kept = 0;
+    F last = INFINITY;
+    for (int i = 0; i < p.groups_kept; ++i) {
+        const auto top = warp_max(key);
+        const uint32_t who = __ballot_sync(kAll, key == top);
+        const uint32_t first = who & -who;   // (the lowest group of equal ones)
+        kept |= first;
+        if (first >> lane & 1u) key = 0;
+        if constexpr (sizeof(F) == 4) last = value_of(top);
     }
-    const bool live = g < p.groups, keep = live && before < p.groups_kept;
     if constexpr (sizeof(F) == 4) {
-        const float low = -warp_max_f(keep ? -(float)score : -INFINITY);            // the worst that stays
-        const float high = warp_max_f(live && !keep ? (float)score : -INFINITY);    // the best that goes
-        const float size = warp_max_f(score > -INFINITY && score < INFINITY ? fabsf(a) + fabsf(b > -INFINITY ? b : a) : 0.0f);
-        *close = high > -INFINITY && low - high <= 2.0f * (tol + 2.4e-7f * size);
+        const uint32_t next = warp_max(key);
+        const float parts = fabsf(a) + fabsf(b);
+        const float size = __uint_as_float(__reduce_max_sync(kAll, live && parts < INFINITY ? __float_as_uint(parts) : 0u));
+        *close = next > key_of(-INFINITY) && last - value_of(next) <= 2.0f * (tol + kSumTol * size);
     }
-    const uint32_t lanes = __ballot_sync(kAll, keep && sub == 0);
-    uint32_t mask = 0;
-    for (int h = 0; h < p.groups; ++h) mask |= (lanes >> (h * per) & 1u) << h;
-    return mask;
+    return kept;
 }
 
-__device__ __forceinline__ bool in_groups(const ScoredParams& p, uint32_t mask, int e) {
-    return p.groups == 1 || (mask >> ((unsigned)e * p.group_inv >> 20) & 1u);
+// Whether e's group stays (p.group_inv: 2^20 / group_size, rounded up).
+__device__ __forceinline__ bool in_groups(const ScoredParams& p, uint32_t kept, int e) {
+    return kept >> (((unsigned)e * p.group_inv >> 20) << p.per_shift & 31u) & 1u;
 }
 
-// The choice in 64 bits, from shared memory: lane j returns the j-th id.
-__device__ __noinline__ int choose64(const ScoredParams& p, long t, int lane, double* c) {
+// The choice in 64 bits, from shared memory: lane j returns the j-th id.  `kept`: the groups that
+// stay, or (again) not known yet; experts whose 32-bit value is below `least` are not among the k.
+template <bool SCORED, bool GROUPS>
+__device__ __noinline__ int choose64(const ScoredParams& p, long t, int lane, double* c, bool again, uint32_t kept, float least) {
     double m = 0.0, z = 1.0;
-    if (!p.sigmoid) {
+    if (SCORED && !p.sigmoid) {
         float top = -INFINITY;
         for (int e = lane; e < p.E; e += 32) top = fmaxf(top, logit(p, t, e));
         m = warp_max_f(top);
@@ -125,28 +147,32 @@ __device__ __noinline__ int choose64(const ScoredParams& p, long t, int lane, do
     }
 #pragma unroll 1
     for (int e = lane; e < p.E; e += 32) {
-        const float l = logit(p, t, e);
-        double v = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - m) / z;
-        if (p.bias) v += (double)p.bias[e];
-        c[e] = l > -INFINITY && v == v ? v : -INFINITY;
+        const float l = logit(p, t, e), b = p.bias ? p.bias[e] : 0.0f;
+        double v = -INFINITY;
+        if (!SCORED) {
+            v = l;
+        } else if (l > -INFINITY && (again || !p.sigmoid || ((!GROUPS || in_groups(p, kept, e)) && fast_sigmoid(l) + b >= least))) {
+            v = (p.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - m) / z) + (double)b;
+            if (v != v) v = -INFINITY;
+        }
+        c[place(e)] = v;
     }
     __syncwarp();
-    uint32_t mask = ~0u;
     bool unused;
-    if (p.groups > 1) mask = groups_kept<double>(p, c, lane, 0.0f, &unused);
+    if (GROUPS && again) kept = groups_kept<double>(p, c, lane, 0.0f, &unused);
     __syncwarp();
     uint64_t* keys = reinterpret_cast<uint64_t*>(c);
     for (int e = lane; e < p.E; e += 32) {
-        const double v = c[e];
-        keys[e] = v > -INFINITY && in_groups(p, mask, e) ? key_of(v) : 0ull;
+        const double v = c[place(e)];
+        keys[place(e)] = v > -INFINITY && (!GROUPS || in_groups(p, kept, e)) ? key_of(v) : 0ull;
     }
     int mine = -1;
     for (int j = 0; j < p.k; ++j) {
         uint64_t best = 0;
         int at = kMaxE;
         for (int e = lane; e < p.E; e += 32) {
-            if (keys[e] > best) {
-                best = keys[e];
+            if (keys[place(e)] > best) {
+                best = keys[place(e)];
                 at = e;
             }
         }
@@ -154,14 +180,36 @@ __device__ __noinline__ int choose64(const ScoredParams& p, long t, int lane, do
         if (top == 0) break;
         const int e = (int)__reduce_min_sync(kAll, (unsigned)(best == top ? at : kMaxE));
         if (lane == j) mine = e;
-        if ((e & 31) == lane) keys[e] = 0;
+        if ((e & 31) == lane) keys[place(e)] = 0;
     }
     return mine;
 }
 
-template <int EPL>
-__global__ void __launch_bounds__(32 * kWarps) route_scored_kernel(ScoredParams p) {
-    extern __shared__ double smem[];   // [warps][E], where scores are needed
+// Largest first (a bitonic network: two operations a comparator).
+template <int N>
+__device__ __forceinline__ void sort_down(uint32_t (&k)[N]) {
+#pragma unroll
+    for (int size = 2; size <= N; size *= 2) {
+#pragma unroll
+        for (int step = size / 2; step > 0; step /= 2) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int o = i ^ step;
+                if (o > i) {
+                    const bool down = (i & size) == 0;
+                    const uint32_t hi = max(k[i], k[o]), lo = min(k[i], k[o]);
+                    k[i] = down ? hi : lo;
+                    k[o] = down ? lo : hi;
+                }
+            }
+        }
+    }
+}
+
+// SCORED: the choice needs the scores (a bias, or sums of a group); else the logits decide.
+template <int EPL, bool SCORED, bool GROUPS>
+__global__ void __launch_bounds__(32 * kWarps) route_scored_kernel(const __grid_constant__ ScoredParams p) {
+    extern __shared__ double smem[];   // a row of place(E) a warp
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     launch_dependents();
     wait_prerequisites();
@@ -174,85 +222,102 @@ __global__ void __launch_bounds__(32 * kWarps) route_scored_kernel(ScoredParams 
         }
         return;
     }
-    float l[EPL], m = -INFINITY, z = 0.0f;
+    float c[EPL], bias[EPL], m = -INFINITY, z = 0.0f;
+    if (p.l_bf16) {
+        const __nv_bfloat16* a = static_cast<const __nv_bfloat16*>(p.logits) + t * p.ldl + lane;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        const int e = lane + 32 * i;
-        l[i] = e < p.E ? logit(p, t, e) : -INFINITY;
-        m = fmaxf(m, l[i]);
+        for (int i = 0; i < EPL; ++i) c[i] = lane + 32 * i < p.E ? __bfloat162float(a[32 * i]) : -INFINITY;
+    } else {
+        const float* a = static_cast<const float*>(p.logits) + t * p.ldl + lane;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) c[i] = lane + 32 * i < p.E ? a[32 * i] : -INFINITY;
     }
-    const bool by_logit = !p.bias && (p.groups == 1 || p.group_top == 1);
-    float x[EPL];   // softmax: exp(l - max)
-    const bool need_z = !p.sigmoid && (!p.renorm || !by_logit);
+    if (SCORED) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) bias[i] = p.bias && lane + 32 * i < p.E ? __ldg(p.bias + lane + 32 * i) : 0.0f;
+    }
+    // (a NaN is not greater than -inf: off too)
+    const bool need_z = !p.sigmoid && (SCORED || !p.renorm);
+    float tol = 0.0f;   // bound on the difference of the errors of two scores
     if (need_z) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) m = fmaxf(m, c[i]);
         m = warp_max_f(m);
+        float x[EPL];
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            x[i] = l[i] > -INFINITY ? expf(l[i] - m) : 0.0f;
+            x[i] = c[i] > -INFINITY ? expf(c[i] - m) : 0.0f;
             z += x[i];
         }
         z = warp_sum(z);
-    }
-    float c[EPL];
-    float tol = 0.0f;   // bound on the difference of the errors of two scores
-    if (by_logit) {
+        if (SCORED) {
+            const float rz = 1.0f / z;
+            tol = kSoftmaxTol * rz;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) c[i] = l[i];
-    } else {
-        // A sigmoid is off by at most 7 roundings' halves (expf 2 ulp, sum, quotient), a softmax
-        // by those of its exponential and of a sum of 16 and then 32 terms; both at most
-        // their largest score.
-        const float rz = 1.0f / z;
-        tol = p.sigmoid ? 9.6e-7f : 3.9e-6f * rz;
+            for (int i = 0; i < EPL; ++i) {
+                const float v = x[i] * rz + bias[i];
+                c[i] = c[i] > -INFINITY && v > -INFINITY ? v : -INFINITY;
+            }
+        }
+    } else if (SCORED) {
+        tol = kSigmoidTol;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            const int e = lane + 32 * i;
-            float s = p.sigmoid ? sigmoid(l[i], 0.0f) : x[i] * rz;
-            if (p.bias && e < p.E) s += __ldg(p.bias + e);
-            c[i] = l[i] > -INFINITY && s == s ? s : -INFINITY;
+            const float v = fast_sigmoid(c[i]) + bias[i];
+            c[i] = c[i] > -INFINITY && v > -INFINITY ? v : -INFINITY;
         }
     }
-    uint32_t mask = ~0u;
-    bool close = false;
-    double* row = smem + warp * p.E;
-    if (p.groups > 1) {
+    uint32_t kept = ~0u;
+    bool again = false;   // groups too close to tell
+    double* row = smem + warp * place(p.E + 31);
+    if constexpr (GROUPS) {
         float* cf = reinterpret_cast<float*>(row);
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (lane + 32 * i < p.E) cf[lane + 32 * i] = c[i];
+            if (lane + 32 * i < p.E) cf[place(lane + 32 * i)] = c[i] > -INFINITY ? c[i] : -INFINITY;
         __syncwarp();
-        mask = groups_kept<float>(p, cf, lane, tol, &close);
-        close &= !by_logit;
+        kept = groups_kept<float>(p, cf, lane, tol, &again);
+        again &= SCORED;
         __syncwarp();
     }
+    // A lane's keys, sorted, largest first.  A key's low bits give way to the place i in the lane, from
+    // which a lower index is larger; keys whose other bits differ order as the values do, and where two
+    // neighbours' are equal the values may differ in what was cut off (bf16 logits lose nothing).
+    constexpr uint32_t kPlace = EPL - 1;
     uint32_t key[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) key[i] = c[i] > -INFINITY && in_groups(p, mask, lane + 32 * i) ? key_of(c[i]) : 0u;
-    int mine = -1;
-    float last = INFINITY;
-    const int rounds = p.k + !by_logit;   // (one more: the first that is not chosen must not be close either)
-    for (int j = 0; j < rounds; ++j) {
-        uint32_t best = 0;
-        int at = kMaxE;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            if (key[i] > best) {
-                best = key[i];
-                at = lane + 32 * i;
-            }
+    for (int i = 0; i < EPL; ++i)
+        key[i] = c[i] > -INFINITY && (!GROUPS || in_groups(p, kept, lane + 32 * i)) ? (key_of(c[i]) & ~kPlace) | (kPlace - i) : 0u;
+    sort_down(key);
+    // k rounds, and one more: the first that is not chosen must not be close to the last that is either.
+    // Lane j keeps the key and the lane of the j-th (key 0: there is none).
+    uint32_t my_key = 0, my_lane = 0;
+    for (int j = 0; j <= p.k; ++j) {
+        const uint32_t top = warp_max(key[0]);
+        const uint32_t from = __ffs(__ballot_sync(kAll, key[0] == top)) - 1;   // (equal keys: of one place, the lowest lane first)
+        if (lane == j) {
+            my_key = top;
+            my_lane = from;
         }
-        const uint32_t top = warp_max(best);
-        if (top == 0) break;
-        const int e = (int)__reduce_min_sync(kAll, (unsigned)(best == top ? at : kMaxE));
-        if (lane == j && j < p.k) mine = e;
-        const float v = value_of(top);
-        close |= !by_logit && last - v <= tol + 2.4e-7f * fabsf(v);
-        last = v;
+        if (lane == from) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (e == lane + 32 * i) key[i] = 0;
+            for (int i = 0; i + 1 < EPL; ++i) key[i] = key[i + 1];
+            key[EPL - 1] = 0;
+        }
     }
-    if (close) mine = choose64(p, t, lane, row);   // (the same in the whole warp)
+    const bool got = my_key != 0 && lane <= p.k;
+    int mine = got && lane < p.k ? (int)(my_lane + 32 * (kPlace - (my_key & kPlace))) : -1;
+    // Lane j looks at the j-th and the next.
+    const float cut = kPlace * 1.2e-7f + kSumTol;   // of a value's size: what was cut off, and kSumTol
+    const uint32_t next_key = __shfl_down_sync(kAll, my_key, 1);
+    const float v = value_of(my_key & ~kPlace), next = value_of(next_key & ~kPlace);
+    bool close = lane < p.k && next_key != 0;
+    close = close && (SCORED ? v - next <= tol + cut * fabsf(next) : !p.l_bf16 && v == next);
+    if (again || __any_sync(kAll, close)) {
+        const float last = __shfl_sync(kAll, v, p.k), size = __shfl_sync(kAll, fabsf(v), p.k);
+        const bool all = __shfl_sync(kAll, my_key, p.k) == 0;   // (no more than k to choose from)
+        mine = choose64<SCORED, GROUPS>(p, t, lane, row, again, kept, all ? -INFINITY : last - 2.0f * (tol + cut * size));
+    }
 
     // The weights: lane j has id j.  Renormalised ones are ratios, from exponentials relative to the largest
     // chosen logit, so that scores which all underflow keep their ratio.
@@ -260,10 +325,10 @@ __global__ void __launch_bounds__(32 * kWarps) route_scored_kernel(ScoredParams 
     const float lj = on ? logit(p, t, mine) : -INFINITY;
     float s = 0.0f;
     if (p.renorm) {
-        const float top = warp_max_f(lj);
+        const float top = warp_max_f<16>(lj);   // (k <= 16)
         if (on) s = p.sigmoid ? sigmoid(lj, fminf(top, 0.0f)) : expf(lj - top);
-        const float sum = warp_sum(s);
-        s = sum == 0.0f ? 0.0f : s / sum;
+        const float sum = warp_sum<16>(s);
+        s = sum == 0.0f ? 0.0f : __fdividef(s, sum);
     } else if (on) {
         s = p.sigmoid ? sigmoid(lj, 0.0f) : expf(lj - m) / z;
     }
@@ -273,17 +338,24 @@ __global__ void __launch_bounds__(32 * kWarps) route_scored_kernel(ScoredParams 
     }
 }
 
-template <int EPL>
+template <int EPL, bool SCORED, bool GROUPS>
 cudaError_t launch(const ScoredParams& p, int warps, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1] = {overlap_attribute()};
     cfg.gridDim = dim3((unsigned)((p.T + warps - 1) / warps), 1, 1);
     cfg.blockDim = dim3(32 * warps, 1, 1);
-    cfg.dynamicSmemBytes = p.bias || p.groups > 1 ? (size_t)warps * p.E * 8 : 0;
+    cfg.dynamicSmemBytes = (size_t)warps * (p.E + 31 + ((p.E + 31) >> 5) * 4) * 8;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, route_scored_kernel<EPL>, p);
+    return cudaLaunchKernelEx(&cfg, route_scored_kernel<EPL, SCORED, GROUPS>, p);
+}
+
+template <int EPL>
+cudaError_t launch_mode(const ScoredParams& p, int warps, cudaStream_t s) {
+    const bool groups = p.groups > 1, scored = p.bias || (groups && p.group_top > 1);
+    if (groups) return scored ? launch<EPL, true, true>(p, warps, s) : launch<EPL, false, true>(p, warps, s);
+    return scored ? launch<EPL, true, false>(p, warps, s) : launch<EPL, false, false>(p, warps, s);
 }
 
 }  // namespace
@@ -291,13 +363,15 @@ cudaError_t launch(const ScoredParams& p, int warps, cudaStream_t s) {
 cudaError_t launch_route_scored(ScoredParams p, int sms, cudaStream_t s) {
     p.group_size = p.E / p.groups;
     p.group_inv = ((1u << 20) + p.group_size - 1) / p.group_size;   // e / group_size = e * inv >> 20 for e < 512
+    p.per_shift = 5;
+    while ((32 >> p.per_shift) < p.groups) --p.per_shift;
     const int warps = p.T > sms ? kWarps : 1;   // (few tokens: each on an SM of its own)
     const int epl = (p.E + 31) / 32;
-    if (epl <= 1) return launch<1>(p, warps, s);
-    if (epl <= 2) return launch<2>(p, warps, s);
-    if (epl <= 4) return launch<4>(p, warps, s);
-    if (epl <= 8) return launch<8>(p, warps, s);
-    return launch<16>(p, warps, s);
+    if (epl <= 1) return launch_mode<1>(p, warps, s);
+    if (epl <= 2) return launch_mode<2>(p, warps, s);
+    if (epl <= 4) return launch_mode<4>(p, warps, s);
+    if (epl <= 8) return launch_mode<8>(p, warps, s);
+    return launch_mode<16>(p, warps, s);
 }
 
 }  // namespace qmm
