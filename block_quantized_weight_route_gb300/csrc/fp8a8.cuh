@@ -185,10 +185,11 @@ __device__ __forceinline__ float4 relu4(float4 v) {
     return make_float4(max_nan(v.x, 0.0f), max_nan(v.y, 0.0f), max_nan(v.z, 0.0f), max_nan(v.w, 0.0f));
 }
 __device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
-// f(a function of four values) for the activation `act`, not QMM_ACT_NONE
+// f(a function of four values) for the activation `act`
 template <class F>
 __device__ __forceinline__ void with_activation(int act, F f) {
-    if (act == 1) f([](float4 v) { return relu4(v); });
+    if (act == 0) f([](float4 v) { return v; });
+    else if (act == 1) f([](float4 v) { return relu4(v); });
     else if (act == 2) f([](float4 v) { return activate4<2>(v); });
     else if (act == 3) f([](float4 v) { return activate4<3>(v); });
     else f([](float4 v) { return activate4<4>(v); });
@@ -336,38 +337,74 @@ __device__ __forceinline__ void store_columns(const Fp8a8Params& p, uint8_t* stg
     }
 }
 
-// The epilogue's bias for a fold warp's COLS columns, on its way to shared memory (COLS floats) while
-// the tile's K blocks are folded; past the end zeros.  And the residual's rows on theirs to L2.
-template <int COLS>
-__device__ __forceinline__ void prefetch_epilogue(const Fp8a8Params& p, float* bias, int lane, long row0, int col0) {
+// The epilogue's bias for a tile's BN columns, on its way to shared memory (in its type, past the end
+// zeros), and the residual's rows of the tile on theirs to L2: by threads 0 .. THREADS - 1, while the tile's
+// K blocks are folded.
+template <int BN, int ROWS, int THREADS>
+__device__ __forceinline__ void prefetch_epilogue(const Fp8a8Params& p, float* bias, int thread, long row0, int col0) {
     if (p.bias) {
-        const int esz = p.bias_bf16 ? 2 : 4, n = col0 + lane * (16 / esz);
-        if (lane * 16 < COLS * esz) {
-            const int left = (p.N - n) * esz, bytes = left < 0 ? 0 : left < 16 ? left : 16;
+        const int esz = p.bias_bf16 ? 2 : 4;
+        for (int x = thread * 16; x < BN * esz; x += THREADS * 16) {
+            const int n = col0 + x / esz, left = (p.N - n) * esz, bytes = left < 0 ? 0 : left < 16 ? left : 16;
             const uint8_t* src = static_cast<const uint8_t*>(p.bias) + (bytes ? (long)n * esz : 0);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(reinterpret_cast<uint8_t*>(bias) + lane * 16)), "l"(src),
-                         "r"(bytes)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(reinterpret_cast<uint8_t*>(bias) + x)), "l"(src), "r"(bytes)
                          : "memory");
         }
     }
-    if (p.R && row0 + lane < p.M) {
-        const int esz = p.r_bf16 ? 2 : 4, cols = p.N - col0 < COLS ? p.N - col0 : COLS;
-        const uint8_t* a = static_cast<const uint8_t*>(p.R) + ((row0 + lane) * p.ldr + col0) * esz;
-        for (int x = 0; x < cols * esz; x += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(a + x) : "memory");
+    if (p.R) {
+        const int esz = p.r_bf16 ? 2 : 4, cols = p.N - col0 < BN ? p.N - col0 : BN;
+        for (int r = thread; r < ROWS && row0 + r < p.M; r += THREADS) {
+            const uint8_t* a = static_cast<const uint8_t*>(p.R) + ((row0 + r) * p.ldr + col0) * esz;
+#pragma unroll 1
+            for (int x = 0; x < cols * esz; x += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(a + x) : "memory");
+        }
+    }
+}
+
+// A lane's share of a part of 32 rows x 32 columns: four columns of eight rows, through `at(i)`, plus the bias
+// and the residual, to Y.  RT: the residual's raw four elements (float4: fp32, uint2: bf16), or void.
+// All eight residual loads and sums are in registers before the first store: R may be Y, and a store
+// through a plain pointer could be to shared memory, so the compiler would not move them past it.
+__device__ __forceinline__ float4 widen4(float4 v) { return v; }
+__device__ __forceinline__ float4 widen4(uint2 w) {
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                       __uint_as_float(w.y & 0xffff0000u));
+}
+template <bool BF16, class RT, class AT>
+__device__ __forceinline__ void finish_part(const Fp8a8Params& p, int lane, long row0, int n, float4 b, AT at) {
+    const bool in = n < p.N;
+    RT r[8];
+    const int nn = in ? n : 0;   // (what is past the end reads an element that exists)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const long m = row0 + i * 4 + lane / 8;
+        r[i] = *reinterpret_cast<const RT*>(static_cast<const uint8_t*>(p.R) + ((m < p.M ? m : p.M - 1) * p.ldr + nn) * (sizeof(RT) / 4));
+    }
+    if (p.act) {
+        with_activation(p.act, [&](auto act) {
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) *at(i) = act(add4(*at(i), b));
+        });
+        b = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float4 y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = add4(add4(*at(i), b), widen4(r[i]));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const long m = row0 + i * 4 + lane / 8;
+        if (in && m < p.M) store4(p.Y, BF16, m * p.N + n, y[i]);
     }
 }
 
 // store_columns with the epilogue: CH columns at a time as fp32 through the staging (CH / 32 parts of 32 rows x
-// 128 bytes), then, coalesced, the bias, the activation and the residual's rows, and the rounding.
-// VEC: eight lanes a row, four columns each.  A row's eight residual loads and its sums are in registers before the
-// first store (R may be Y, and a store through a plain pointer could be to shared memory: the compiler
-// would not move them past it).  Else a column a lane.
-// The loops over the parts and in the activation are not unrolled: the code, many times over, does not
-// fit the instruction cache.
+// 128 bytes), then, coalesced, the bias (`bias`, bias0 the warp's first column of it), the activation and the
+// residual's rows, and the rounding.  VEC: eight lanes a row, four columns each; else a column a lane.
+// The loops over the parts are not unrolled, nor the activation's (but for two at once with nothing behind it):
+// the code, many times over, does not fit the instruction cache.
 template <bool BF16, bool VEC, int COLS, int CH>
-__device__ __forceinline__ void store_epilogue(const Fp8a8Params& p, uint8_t* stg, const float* bias, int lane, long row0, int col0,
+__device__ __forceinline__ void store_epilogue(const Fp8a8Params& p, uint8_t* stg, const float* bias, int bias0, int lane, long row0, int col0,
                                                const uint64_t* v) {
-    cp_async_wait_all();
 #pragma unroll
     for (int c0 = 0; c0 < COLS; c0 += CH) {
         __syncwarp();
@@ -382,45 +419,35 @@ __device__ __forceinline__ void store_epilogue(const Fp8a8Params& p, uint8_t* st
             uint8_t* part = stg + h * 4096;
             if constexpr (VEC) {
                 const int c = lane % 8, n = col0 + c0 + 32 * h + 4 * c;
-                const bool in = n < p.N;
-                float4 r[8], b = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const long m = row0 + i * 4 + lane / 8;
-                    r[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (p.R && in && m < p.M) r[i] = load4(p.R, p.r_bf16, m * p.ldr + n);
-                }
-                if (p.bias) b = load4(bias, p.bias_bf16, c0 + 32 * h + 4 * c);
+                const float4 b = p.bias ? load4(bias, p.bias_bf16, bias0 + c0 + 32 * h + 4 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
                 auto at = [&](int i) {   // (this lane's alone)
                     const int q = i * 4 + lane / 8;
                     return reinterpret_cast<float4*>(part + (q * 8 + (c ^ (q & 7))) * 16);
                 };
-                if (p.act) {
+                if (!p.R) {
                     with_activation(p.act, [&](auto act) {
-#pragma unroll 1
-                        for (int i = 0; i < 8; ++i) *at(i) = act(add4(*at(i), b));
+#pragma unroll 2
+                        for (int i = 0; i < 8; ++i) {
+                            const long m = row0 + i * 4 + lane / 8;
+                            const float4 y = act(add4(*at(i), b));
+                            if (n < p.N && m < p.M) store4(p.Y, BF16, m * p.N + n, y);
+                        }
                     });
-                    b = make_float4(0.f, 0.f, 0.f, 0.f);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) r[i] = add4(add4(*at(i), b), r[i]);
-                if (in) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const long m = row0 + i * 4 + lane / 8;
-                        if (m < p.M) store4(p.Y, BF16, m * p.N + n, r[i]);
-                    }
+                } else if (p.r_bf16) {
+                    finish_part<BF16, uint2>(p, lane, row0, n, b, at);
+                } else {
+                    finish_part<BF16, float4>(p, lane, row0, n, b, at);
                 }
             } else {
                 const int n = col0 + c0 + 32 * h + lane, rows = p.M - row0 < 32 ? (int)(p.M - row0) : 32;
                 const bool in = n < p.N;
-                const float b = p.bias ? load1(bias, p.bias_bf16, c0 + 32 * h + lane) : 0.0f;
+                const float b = p.bias ? load1(bias, p.bias_bf16, bias0 + c0 + 32 * h + lane) : 0.0f;
 #pragma unroll 1
                 for (int q0 = 0; q0 < rows; q0 += 8) {
                     float r[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) r[i] = p.R && in && q0 + i < rows ? load1(p.R, p.r_bf16, (row0 + q0 + i) * p.ldr + n) : 0.0f;
-#pragma unroll 1
+#pragma unroll 4
                     for (int i = 0; p.act && i < 8; ++i) {   // (of 32 rows staged)
                         const int q = q0 + i;
                         float* at = reinterpret_cast<float*>(part + (q * 8 + ((lane / 4) ^ (q & 7))) * 16) + lane % 4;

@@ -60,15 +60,18 @@ struct PairCfg {
     // share of the registers for their sums (a register split) and loads of 8 (gate/up with
     // loads of 16: 15% slower at 2048 x 5120 x 2 x 17408).
     // With the epilogue: 8 warps of 128 columns at BN = 256, which leaves registers for it (16 warps
-    // spill in the K loop: 292 us in place of XXX at 2048 x 5120 x 17408 with bias and GELU).
+    // spill in the K loop: 292 us in place of 188 at 2048 x 5120 x 17408 with bias and GELU).
     static constexpr bool WIDE = EPI && BN == 256;
-    static constexpr int CW = WIDE ? 128 : 64, GROUPS = BN / CW, FOLD_WARPS = 4 * GROUPS, LW = WIDE ? 64 : BN == 256 ? 8 : BN == 192 ? (EPI ? 16 : 32) : 64;
+    static constexpr int CW = WIDE ? 128 : 64, GROUPS = BN / CW, FOLD_WARPS = 4 * GROUPS, LW = WIDE ? 64 : BN == 256 ? 8 : BN == 192 ? (EPI ? 8 : 32) : 64;
     static constexpr int OUT_BYTES = GATED ? 2 * GROUPS * 128 * 4 : FOLD_WARPS * STAGING;   // row maxima, or output staging
     static constexpr bool REG_SPLIT = BN == 256;
-    static constexpr int THREADS = 128 + 32 * FOLD_WARPS, REGS = 65536 / THREADS / 8 * 8, REGS_FOLD = WIDE ? 216 : 104, REGS_OTHER = WIDE ? 72 : 64;
+    static constexpr int THREADS = 128 + 32 * FOLD_WARPS, REGS = 65536 / THREADS / 8 * 8, REGS_FOLD = WIDE ? 224 : 104, REGS_OTHER = WIDE ? 56 : 64;
     static_assert(!REG_SPLIT || REGS_FOLD * 32 * FOLD_WARPS + REGS_OTHER * 128 == REGS * THREADS, "register shares = launch registers");
     static constexpr int BARS = 2 * STAGES + NBUF + 2 * SC_SLOTS + 3;
-    static constexpr int BIAS_FLOATS = EPI ? FOLD_WARPS * CW : 0;   // the fold warps' columns of the bias
+    // The bias of four tiles: the scales' warps, which copy it, are at most SC_SLOTS = 2 tiles ahead of the tile
+    // whose K blocks are folded, and the epilogue of the tile before that one may still be reading its own.
+    static constexpr int BIAS_FLOATS = EPI ? 4 * BN : 0;
+    static_assert(!EPI || SC_SLOTS <= 2, "the scales' warps are too far ahead");
     static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + OUT_BYTES + (SC_FLOATS + BIAS_FLOATS) * 4 + BARS * 8 + 64;
     static_assert(SMEM <= 232448, "shared memory");
     static_assert(!GATED || BN == 256, "gate/up: 128 + 128 columns");
@@ -153,19 +156,13 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
         // ------------------------------------------------------------ fold
         const int q = warp & 3, cq = (warp - 4) >> 2, row = q * 32 + lane;
         const uint32_t lane_addr = tmem_base + ((uint32_t)(q * 32) << 16);
-        int st = 0, slot = 0, parity = 0;
+        int st = 0, slot = 0, round = 0;
         uint32_t ph = 0, sph = 0, rph = 0;
         bool ok = true;
-        for (int t = cid; t < tiles && ok; t += ncl, parity ^= 1) {
+        for (int t = cid; t < tiles && ok; t += ncl, ++round) {
             // which of the tile's two weight blocks the thread's 64 columns are in (gated: the
             // first half in one, the second in the other)
             const int blk = !C::GATED && cq * C::CW >= 128 - (pair_tile<C>(p, t, crank).n0 & 127);
-            float* bias = sc + C::SC_FLOATS + (warp - 4) * C::CW;
-            if constexpr (C::EPI) {
-                const PairTile ti = pair_tile<C>(p, t, crank);
-                __syncwarp();   // (the bias of the tile before has been read)
-                prefetch_epilogue<C::CW>(p, bias, lane, (long)ti.m0 + q * 32, ti.n0 + fold_col<C>(cq, 0));
-            }
             uint64_t acc[C::CW / 2];
 #pragma unroll
             for (int j = 0; j < C::CW / 2; ++j) acc[j] = 0;
@@ -219,7 +216,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
             const PairTile ti = pair_tile<C>(p, te, crank);
             if constexpr (!C::GATED) {
                 uint8_t* stg = outs + (warp - 4) * C::STAGING;
-                if constexpr (C::EPI) store_epilogue<C::BF16, !C::RAGGED, C::CW, C::STAGING / 128>(p, stg, bias, lane, (long)ti.m0 + q * 32, ti.n0 + fold_col<C>(cq, 0), acc);
+                if constexpr (C::EPI) store_epilogue<C::BF16, !C::RAGGED, C::CW, C::STAGING / 128>(p, stg, sc + C::SC_FLOATS + (round & 3) * C::BN, fold_col<C>(cq, 0), lane, (long)ti.m0 + q * 32, ti.n0 + fold_col<C>(cq, 0), acc);
                 else store_columns<C::BF16, C::RAGGED, C::BN == 256 ? 4 : 8>(p, stg, lane, (long)ti.m0 + q * 32, ti.n0 + fold_col<C>(cq, 0), acc);
             } else {
                 // the first half of acc: gate columns; the second half: the same columns of up
@@ -233,6 +230,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
                     a = max_nan_abs(a, h0, h1);
                     acc[j] = pack2(h0, h1);
                 }
+                const int parity = round & 1;
                 float* rm = rowmax + parity * 512 + row;
                 rm[cq * 128] = a;
                 __syncwarp();
@@ -347,10 +345,10 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
             // blocks past the end are filled with zeros); a slot's barrier counts the
             // copies of all 64 lanes.
             const int l = threadIdx.x - 64;
-            int slot = 0;
+            int slot = 0, round = 0;
             uint32_t sph = 0;
             bool ok = true;
-            for (int t = cid; t < tiles && ok; t += ncl) {
+            for (int t = cid; t < tiles && ok; t += ncl, ++round) {
                 const PairTile ti = pair_tile<C>(p, t, crank);
                 const long b0 = ti.n0 / 128, b1 = C::GATED ? (p.N + ti.n0) / 128 : b0 + 1;
                 const long nblk = C::GATED ? p.N / 64 : (p.N + 127) / 128;
@@ -359,6 +357,8 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
                         ok = false;
                         break;
                     }
+                    // (the slot's barrier completes with the bias too)
+                    if (C::EPI && kb == 0) prefetch_epilogue<C::BN, 128, 64>(p, sc + C::SC_FLOATS + (round & 3) * C::BN, l, ti.m0, ti.n0);
                     float* dst = sc + slot * C::SC_KB * C::SC_PITCH;
 #pragma unroll
                     for (int i = 0; i < 2 * C::SC_KB; ++i) {
