@@ -1214,7 +1214,7 @@ qmm_status moe_expert_stage_fp8(const uint8_t* Xq, const float* Xs, const int32_
     if (st != QMM_OK || T == 0) return st;
 
     MoePlan plan;
-    cudaError_t e = moe_plan(T, D, F, E, k, d->index, &plan);
+    cudaError_t e = moe_plan(T, D, F, E, k, d->sms, d->index, &plan);
     if (e != cudaSuccess) return cuda_fail(e, who);
     const int P = T * k;
     uint8_t* base = static_cast<uint8_t*>(ws);
@@ -1238,13 +1238,23 @@ qmm_status moe_expert_stage_fp8(const uint8_t* Xq, const float* Xs, const int32_
     // the output's own 2^-8 of the sum), and are half the bytes: 173 MB in place of 345 written and read again for
     // 5268 tokens of 2048 columns and 8 experts.
     float* y_unit = plan.many && ydt == QMM_BF16 ? static_cast<float*>(at(12)) : nullptr;
-    if ((e = launch_moe_group(ids, P, E, k, g, d->index, stream)) != cudaSuccess) return cuda_fail(e, "moe_expert_stage_fp8: grouping");
-    if ((e = launch_moe_gather(Xq, Xs, P, D, g, E, Xp, Xps, d->sms, stream)) != cudaSuccess)
+    const bool small = P <= kMoeSmall && !plan.many;   // gate/up groups by itself
+    if (!small && (e = launch_moe_group(ids, P, E, k, g, d->index, stream)) != cudaSuccess)
+        return cuda_fail(e, "moe_expert_stage_fp8: grouping");
+    if (plan.many && (e = launch_moe_gather(Xq, Xs, P, D, g, E, Xp, Xps, d->sms, stream)) != cudaSuccess)
         return cuda_fail(e, "moe_expert_stage_fp8: gather");
     for (int gated = 1; gated >= 0; --gated) {
         Fp8a8Params p{};
-        p.Xq = gated ? Xp : Hq;
-        p.Xs = gated ? Xps : Hs;
+        const bool gather = gated && !plan.many;   // (the narrow kernel gathers the tokens itself)
+        p.Xq = !gated ? Hq : gather ? Xq : Xp;
+        p.Xs = !gated ? Hs : gather ? Xs : Xps;
+        p.src = g.src;
+        if (small && gated) {
+            p.ids = ids;
+            p.E = E;
+            p.k = k;
+            p.groups = g;
+        }
         p.W = gated ? Wgu : Wd;
         p.S = gated ? Sgu : Sd;
         p.M = P;
@@ -1264,7 +1274,8 @@ qmm_status moe_expert_stage_fp8(const uint8_t* Xq, const float* Xs, const int32_
         if (!gated && y_unit &&
             (st = make_tmap(&ty, y, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, D, P, (uint64_t)D * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK)
             return st;
-        if ((st = make_tmap(&tx, p.Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, P, p.K, 128, plan.tn, CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK ||
+        if ((st = make_tmap(&tx, p.Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, gather ? T : P, p.K, 128, gather ? 1 : plan.tn,
+                            CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK ||
             (st = make_tmap(&tw, p.W, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, (uint64_t)E * p.N * (gated ? 2 : 1), p.K, 128,
                             plan.many && gated ? 64 : 128, CU_TENSOR_MAP_SWIZZLE_128B)) != QMM_OK)
             return st;

@@ -49,7 +49,7 @@ struct ExpertTile {
 template <class C>
 __device__ __forceinline__ ExpertTile expert_tile(const Fp8a8Params& p, int t) {
     const int entry = t / p.n_tiles;
-    const int4 v = __ldg(p.tiles + entry);
+    const int4 v = p.tiles[entry];
     return ExpertTile{v.x, v.y, v.z, (t - entry * p.n_tiles) * (C::GATED ? 128 : C::BN)};
 }
 

@@ -4,7 +4,7 @@
 //   GATED: h = silu(y gate) * y up, rounded to E4M3 per 128 columns of a token
 //   EPI: y = act(y + bias[n]) + R[m][n], in the cluster's sum
 //   GROUPED: rows grouped by expert (a list of tiles {expert, first row, rows} on the device),
-//            each tile against its expert's weights
+//            each tile against its expert's weights; gate/up gathers the rows' tokens itself
 //
 // With few tokens the weights' bytes are the work, so the operands are swapped: a CTA
 // streams 128 weight rows (GATED: 128 gate and 128 up rows) through the M side of
@@ -31,7 +31,7 @@ namespace {
 template <int TN_, bool GATED_, bool EPI_ = false, bool GROUPED_ = false>
 struct NarrowCfg {
     static constexpr int TN = TN_, MATS = GATED_ ? 2 : 1;
-    static constexpr bool GATED = GATED_, EPI = EPI_, GROUPED = GROUPED_, TOKENS_M = TN == 128;
+    static constexpr bool GATED = GATED_, EPI = EPI_, GROUPED = GROUPED_, GATHER = GROUPED_ && GATED_, TOKENS_M = TN == 128;
     static constexpr int W_BYTES = MATS * 128 * 128, X_BYTES = TN * 128, STAGE_BYTES = W_BYTES + X_BYTES;
     // Two CTAs on an SM where a stage (and a fold thread) is small: one's start and end run beside the other's
     // stream, and a product of few tiles is split over more CTAs (one token, 5120 x 5120:
@@ -53,7 +53,7 @@ struct NarrowCfg {
     static constexpr int COPIES = MATS + 1;
     static_assert(COPIES * STAGES <= 32, "a lane per copy");
     static constexpr int BARS = 2 * STAGES + NBUF + 2 * SC_SLOTS + 1;
-    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + SC_FLOATS * 4 + BARS * 8 + 64;
+    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + SC_FLOATS * 4 + BARS * 8 + 64 + (GATHER ? 16 + 4 * TN : 0);
     static_assert(PER_SM * (SMEM + 1024) <= 233472 && PER_SM * TMEM_COLS <= 512, "shared memory and TMEM");
     static_assert(TN * 128 * 4 * MATS <= STAGES * STAGE_BYTES, "the sums fit the stages");
     static_assert(!TOKENS_M || SC_KB % NBUF == 0, "buffer = K block's place in its slot");
@@ -224,6 +224,51 @@ __device__ __forceinline__ void fold_tokens_m(const Fp8a8Params& p, int warp, in
     }
 }
 
+// A lane's pair among at most 32, grouped by expert as launch_moe_group does it.
+struct SmallGroup {
+    bool valid;
+    int e, rank, count, row;   // the expert, the pair's place among its pairs and how many there are, its row
+};
+__device__ __forceinline__ SmallGroup small_group(const Fp8a8Params& p, int lane) {
+    SmallGroup g;
+    g.e = lane < p.M ? p.ids[lane] : -1;
+    g.valid = (unsigned)g.e < (unsigned)p.E;
+    const int key = g.valid ? g.e : 0x7fffffff;
+    const unsigned same = __match_any_sync(0xffffffffu, key);
+    g.rank = __popc(same & ((1u << lane) - 1u));
+    g.count = __popc(same);
+    g.row = g.rank;
+    for (int i = 0; i < 32; ++i) g.row += __shfl_sync(0xffffffffu, key, i) < key;
+    return g;
+}
+// The same as the grouping kernels leave in the workspace (a warp; the tiles in the order of their first pairs).
+__device__ __noinline__ void write_small_group(const Fp8a8Params& p, int lane, int tile_rows) {
+    const SmallGroup g = small_group(p, lane);
+    const int key = g.valid ? g.e : 0x7fffffff;
+    for (int e0 = 0; e0 <= p.E; e0 += 32) {
+        const int e = e0 + lane;
+        int before = 0, own = 0;
+        for (int i = 0; i < 32; ++i) {
+            const int o = __shfl_sync(0xffffffffu, key, i);
+            before += o < e;
+            own += o == e;
+        }
+        if (e < p.E) p.groups.counts[e] = own;
+        if (e <= p.E) p.groups.offsets[e] = before;   // (pairs without an expert have the largest key: none is before e = E)
+    }
+    const unsigned first = __ballot_sync(0xffffffffu, g.valid && g.rank % tile_rows == 0);
+    if (first >> lane & 1u)
+        p.groups.tiles[__popc(first & ((1u << lane) - 1u))] = make_int4(g.e, g.row, min(tile_rows, g.count - g.rank), 0);
+    if (lane == 0) *p.groups.num_tiles = __popc(first);
+    if (lane < p.M) p.groups.row[lane] = g.valid ? g.row : -1;
+    if (g.valid) p.groups.src[g.row] = lane / p.k;
+}
+// The token of row r.
+template <class C>
+__device__ __forceinline__ int token_of(const Fp8a8Params& p, const int* own_tile, int m0, int r) {
+    return p.ids ? own_tile[4 + r - m0] : p.src[r];
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
     fp8a8_narrow_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, Fp8a8Params p) {
@@ -240,6 +285,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
     uint64_t* drain = sc_empty + C::SC_SLOTS;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* own_tile = reinterpret_cast<int*>(tmem_slot + 2);   // grouped here: {expert, first row, rows}, then the rows' tokens
 
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     launch_dependents();
@@ -279,12 +325,34 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
     wait_prerequisites();
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     if constexpr (C::GROUPED) {
-        if ((int)blockIdx.z >= *p.num_tiles) {   // (the grid covers the most tiles that there can be; the same in the whole cluster)
+        const bool here = C::GATHER && p.ids;   // no more pairs than one warp groups: no launch for it
+        if (here && warp == 0) {
+            const SmallGroup g = small_group(p, lane);
+            const unsigned first = __ballot_sync(0xffffffffu, g.valid && g.rank % C::TN == 0);   // a tile each
+            const bool mine = (first >> lane & 1u) && __popc(first & ((1u << lane) - 1u)) == (int)blockIdx.z;
+            const unsigned who = __ballot_sync(0xffffffffu, mine);
+            if (who == 0) {
+                if (lane == 0) own_tile[2] = 0;
+            } else {
+                const int from = __ffs(who) - 1;
+                const int e = __shfl_sync(0xffffffffu, g.e, from), r0 = __shfl_sync(0xffffffffu, g.rank, from);
+                if (lane == from) {
+                    own_tile[0] = e;
+                    own_tile[1] = g.row;
+                    own_tile[2] = min(C::TN, g.count - r0);
+                }
+                if (g.valid && g.e == e && g.rank >= r0 && g.rank < r0 + C::TN) own_tile[4 + g.rank - r0] = lane / p.k;
+            }
+        }
+        if (here && warp == 3 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) write_small_group(p, lane, C::TN);
+        if (here) __syncthreads();
+        // (the grid covers the most tiles that there can be; the same in the whole cluster)
+        if (here ? own_tile[2] == 0 : (int)blockIdx.z >= *p.num_tiles) {
             __syncthreads();
             if (warp == 1) tmem_dealloc(tmem_base, C::TMEM_COLS);
             return;
         }
-        const int4 tile = p.tiles[blockIdx.z];
+        const int4 tile = here ? make_int4(own_tile[0], own_tile[1], own_tile[2], 0) : p.tiles[blockIdx.z];
         m0 = tile.y;
         m_end = tile.y + tile.z;
         w0 += tile.x * p.N * C::MATS;
@@ -302,6 +370,11 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
             int s = 0;
             uint32_t ph = 0;
             long issued = 0;
+            int tokens[4] = {};   // of this lane's four rows (behind the last one its token again)
+            if constexpr (C::GATHER) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tokens[i] = token_of<C>(p, own_tile, m0, min(m0 + lane * 4 + i, m_end - 1));
+            }
             for (int kb = kb0; kb < kb1; ++kb) {
                 const bool got = mbar_wait(&done[s], ph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_TMA_EMPTY);
                 if (__any_sync(0xffffffffu, !got)) break;
@@ -311,7 +384,8 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
                 __syncwarp();
                 uint8_t* dst = stage + s * C::STAGE_BYTES + c * 128 * 128;
                 if (c >= 0 && c < C::MATS) tma_load_2d(dst, &tmW, &full[s], kb * 128, c * p.N + w0);
-                else if (c == C::MATS) tma_load_2d(dst, &tmX, &full[s], kb * 128, m0);
+                else if (!C::GATHER && c == C::MATS) tma_load_2d(dst, &tmX, &full[s], kb * 128, m0);
+                if (C::GATHER && lane < C::TN / 4) tma_gather4(stage + s * C::STAGE_BYTES + C::W_BYTES + lane * 512, &tmX, &full[s], kb * 128, tokens);
                 __syncwarp();
                 ++issued;
                 if (++s == C::STAGES) {
@@ -371,13 +445,22 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
             int slot = 0;
             uint32_t sph = 0;
             const long b0 = blk0, b1 = blk0 + p.N / 128;   // weight blocks (gated: gate, up)
+            // the tile's rows that this lane copies scales of: r = (lane + 32 u) % TN
+            constexpr int ROWS = C::TN < 32 ? 1 : C::TN / 32;
+            int rows[ROWS];
+#pragma unroll
+            for (int u = 0; u < ROWS; ++u) {
+                const int r = m0 + (lane + 32 * u) % C::TN;
+                rows[u] = C::GATHER ? token_of<C>(p, own_tile, m0, min(r, m_end - 1)) : r;
+            }
             for (int kb = kb0; kb < kb1; kb += C::SC_KB) {
                 if (!mbar_wait(&sc_empty[slot], sph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_CONV_EMPTY)) break;
                 float* dst = sc + slot * C::SC_KB * C::SC_PITCH;
-                for (int i = lane; i < C::SC_KB * C::TN; i += 32) {
-                    const int k = i / C::TN, r = i % C::TN;
+#pragma unroll
+                for (int u = 0; u < C::SC_KB * C::TN / 32; ++u) {
+                    const int i = lane + 32 * u, k = i / C::TN, r = i % C::TN;
                     const bool in = kb + k < kb1 && m0 + r < m_end;
-                    cp_async4(dst + k * C::SC_PITCH + r, in ? p.Xs + (long)(m0 + r) * kbs + kb + k : p.Xs, in);
+                    cp_async4(dst + k * C::SC_PITCH + r, in ? p.Xs + (long)rows[u % ROWS] * kbs + kb + k : p.Xs, in);
                 }
                 if (lane < C::MATS * C::SC_KB) {
                     const int k = lane / C::MATS, m = lane % C::MATS;

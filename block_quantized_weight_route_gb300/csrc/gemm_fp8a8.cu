@@ -1,4 +1,5 @@
 // FP8 x FP8 products with block scales: which kernel takes which shape.
+#include <algorithm>
 #include <cmath>
 
 #include "qmm_internal.h"
@@ -127,7 +128,7 @@ cudaError_t fp8a8_plan(int M, int K, int N, bool gated, int sms, int dev, Fp8a8P
 // The expert stage: the tile's tokens with the least estimated time of both products (the narrow
 // kernel's constants above), for tokens that choose their experts evenly: the host does not
 // know the rows of an expert.
-cudaError_t moe_plan(int T, int D, int F, int E, int k, int dev, MoePlan* plan) {
+cudaError_t moe_plan(int T, int D, int F, int E, int k, int sms, int dev, MoePlan* plan) {
     struct Known {
         int T, D, F, E, k, dev;
         MoePlan plan;
@@ -139,8 +140,17 @@ cudaError_t moe_plan(int T, int D, int F, int E, int k, int dev, MoePlan* plan) 
         return cudaSuccess;
     }
     const double experts = E * (1.0 - std::pow(1.0 - (k < E ? (double)k / E : 1.0), T)), rows = (double)T * k / experts;
-    double least = 1e300;
-    MoePlan best{false, 128, 1, 1};
+    // Many rows an expert: tiles of 128 x 256 (of H: 128) on persistent CTAs, a gather before them.  Few: the narrow
+    // kernel; where its CTAs come in more than one wave each pays its start anew.  Neither is faster than the
+    // weights' bytes come.  Measured with D = 2048, F = 768, k = 8, narrow / many, us: 128 experts, 32 tokens 110 / 110,
+    // 301 167 / 135, 512 213 / 138; 64 experts, 64 tokens 74 / 77; 16 experts, 64 tokens 34 / 40; 8 experts, F = 2048, 200 tokens 84 / 51.
+    const double weights_us = experts * D * (double)F / 5.9e6;   // of the down product; gate/up: twice
+    auto many_time = [&](int kbs, int columns, double bytes_us) {
+        const double tiles = experts * (rows / 128.0 < 0.5 ? 1.0 : rows / 128.0 + 0.5) * columns;
+        return std::max(std::ceil(tiles / sms) * (2.5 + 0.42 * kbs), bytes_us);
+    };
+    double least = 6.0 + many_time((D + 127) / 128, F / 128, 2 * weights_us) + many_time(F / 128, (D + 255) / 256, weights_us);
+    MoePlan best{true, 128, 1, 1};
     for (int i = 0; i < 4; ++i) {
         if ((long)T * k / kTn[i] + E > 65535) continue;   // (the tiles are a dimension of the grid)
         const double fill = rows / kTn[i], entries = experts * (fill < 0.5 ? 1.0 : fill + 0.5);
@@ -155,20 +165,20 @@ cudaError_t moe_plan(int T, int D, int F, int E, int k, int dev, MoePlan* plan) 
                 if (e != cudaSuccess) return e;
                 if (at_once < 1) continue;
                 const double tiles = entries * columns, waves = tiles < at_once ? 1.0 : tiles / at_once;
-                const double t = waves * (2.0 + 0.1 * cs + 0.011 * kTn[i] * (gated ? 2 : 1) + (kbs + cs - 1) / cs * kNarrowKb[gated][i]);
+                const double t = waves * ((waves > 1.0 ? 6.0 : 2.0) + 0.1 * cs + 0.011 * kTn[i] * (gated ? 2 : 1) +
+                                          (kbs + cs - 1) / cs * kNarrowKb[gated][i]);
                 if (t < t_best) {
                     t_best = t;
                     (gated ? pl.cs_gate_up : pl.cs_down) = cs;
                 }
             }
-            total += t_best;
+            total += std::max(t_best, (gated ? 2 : 1) * weights_us);
         }
         if (total < least) {
             least = total;
             best = pl;
         }
     }
-    if (rows > 40) best = MoePlan{true, 128, 1, 1};
     slot = Known{T, D, F, E, k, dev, best};
     *plan = best;
     return cudaSuccess;

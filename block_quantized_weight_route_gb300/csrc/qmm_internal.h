@@ -137,6 +137,20 @@ struct NormParams {
 int rmsnorm8_max_width();
 cudaError_t launch_rmsnorm8(const NormParams& p, bool q81, cudaStream_t s);
 
+// Grouping of the FP8 expert stage (moe_fp8.cu).
+constexpr int kMoeChunk = 2048, kMoeMaxExperts = 512;   // pairs of a grouping chunk
+constexpr int kMoeSmall = 32;                           // pairs that one warp groups
+struct MoeGroups {
+    int32_t* counts;        // [E]
+    int32_t* offsets;       // [E + 1]
+    int32_t* src;           // [P] token of each row
+    int32_t* row;           // [P] row of each pair, -1 for one without an expert
+    int32_t* chunk_counts;  // [chunks][E] (scratch)
+    int4* tiles;            // {expert, first row, rows, 0}
+    int* num_tiles;
+    int tile_rows, max_tiles;
+};
+
 // FP8 x FP8 products with block scales (gemm_fp8a8.cu).
 struct Fp8a8Params {
     const uint8_t* Xq;   // [M][K] E4M3
@@ -163,6 +177,10 @@ struct Fp8a8Params {
     const int4* tiles;   // {expert, first row, rows, 0}; null: not grouped
     const int* num_tiles;   // on the device
     int max_tiles;       // room in `tiles`
+    const int32_t* src;  // narrow kernel, gated: a row's token (Xq and Xs are the tokens', gathered by the kernel)
+    const int32_t* ids;  // narrow kernel, gated: not null: it groups the pairs by itself (M <= kMoeSmall of them) and
+    int E, k;            // writes the grouping that the tiles come from
+    MoeGroups groups;
     float* y_unit;       // [M][ceil(N/64)]: Y is fp16 in these units (null: fp32)
 };
 // Which kernel takes a product: the pair kernel (many tokens) with its tile's columns,
@@ -184,7 +202,7 @@ struct MoePlan {
     bool many;           // the kernel for many rows an expert (tiles of 128), else the narrow one
     int tn, cs_gate_up, cs_down;
 };
-cudaError_t moe_plan(int T, int D, int F, int E, int k, int dev, MoePlan* plan);
+cudaError_t moe_plan(int T, int D, int F, int E, int k, int sms, int dev, MoePlan* plan);
 bool fp8a8_plans_fit(const Fp8a8Plans& r, int M, int K, int N, bool gated);   // whether the kernels can run a given tiling
 // clusters of cs CTAs that the device holds at once (0: none)
 cudaError_t fp8a8_narrow_at_once(bool gated, int tn, int cs, int dev, int* clusters);
@@ -196,18 +214,6 @@ cudaError_t launch_fp8a8_experts(const CUtensorMap& tx, const CUtensorMap& tw, c
 cudaError_t launch_fp8a8_pair(const CUtensorMap& tx, const CUtensorMap& tw, Fp8a8Params p, bool gated, int bn, int sms,
                               int dev, cudaStream_t s);
 
-// Grouping of the FP8 expert stage (moe_fp8.cu).
-constexpr int kMoeChunk = 2048, kMoeMaxExperts = 512;   // pairs of a grouping chunk
-struct MoeGroups {
-    int32_t* counts;        // [E]
-    int32_t* offsets;       // [E + 1]
-    int32_t* src;           // [P] token of each row
-    int32_t* row;           // [P] row of each pair, -1 for one without an expert
-    int32_t* chunk_counts;  // [chunks][E] (scratch)
-    int4* tiles;            // {expert, first row, rows, 0}
-    int* num_tiles;
-    int tile_rows, max_tiles;
-};
 cudaError_t launch_moe_group(const int32_t* ids, int P, int E, int k, const MoeGroups& g, int dev, cudaStream_t s);
 cudaError_t launch_moe_gather(const uint8_t* Xq, const float* Xs, int P, int D, const MoeGroups& g, int E, uint8_t* Xp, float* Xps,
                               int sms, cudaStream_t s);

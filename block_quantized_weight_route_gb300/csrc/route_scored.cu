@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_scored_kernel(const __grid_
     }
     if (SCORED) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) bias[i] = p.bias && lane + 32 * i < p.E ? __ldg(p.bias + lane + 32 * i) : 0.0f;
+        for (int i = 0; i < EPL; ++i) bias[i] = p.bias && lane + 32 * i < p.E ? p.bias[lane + 32 * i] : 0.0f;
     }
     // (a NaN is not greater than -inf: off too)
     const bool need_z = !p.sigmoid && (SCORED || !p.renorm);
