@@ -29,8 +29,8 @@ struct ExpertsCfg {
     static constexpr int OUT_BYTES = GATED ? 2 * GROUPS * 128 * 4 : FOLD_WARPS * STAGING;   // row maxima, or output staging
     static constexpr int STAGES = GATED ? 4 : 3, NBUF = 2, BUF_COLS = 256;   // a buffer holds both halves
     // Ring of scales: slots of SC_KB K blocks, which is also how many the fold loop unrolls
-    // (gate/up unrolled by eight spills); a slot holds the tile's first row and its rows too.
-    static constexpr int SC_KB = GATED ? 4 : 8, SC_SLOTS = 16 / SC_KB, SC_PITCH = 128 + 4, SC_FLOATS = SC_SLOTS * SC_KB * SC_PITCH;
+    // (eight: 1% slower); a slot holds the tile's first row and its rows too.
+    static constexpr int SC_KB = 4, SC_SLOTS = 16 / SC_KB, SC_PITCH = 128 + 4, SC_FLOATS = SC_SLOTS * SC_KB * SC_PITCH;
     static constexpr int THREADS = 128 + 32 * FOLD_WARPS, REGS = 65536 / THREADS / 8 * 8, REGS_FOLD = 216, REGS_OTHER = 72;
     static_assert(REGS_FOLD * 32 * FOLD_WARPS + REGS_OTHER * 128 == REGS * THREADS, "register shares = launch registers");
     static_assert(GROUPS == 2, "a fold group for each half of the columns");

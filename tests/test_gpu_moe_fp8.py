@@ -122,7 +122,8 @@ def check(q, seed, T, D, F, E, k, how="even", dt=F32, res=None, weights=None):
 HOWS = ["even", "skewed", "holes", "twice", "one"]
 SHAPES = [(1, 256, 128, 8, 2), (1, 2048, 768, 16, 8), (2, 16, 128, 3, 1), (3, 144, 256, 5, 5), (7, 400, 384, 1, 1), (16, 128, 128, 2, 2),
           (17, 272, 128, 4, 3), (33, 1000 // 16 * 16, 256, 6, 4), (64, 512, 128, 12, 6), (100, 2000, 256, 4, 4), (129, 640, 512, 3, 2),
-          (200, 256, 1024, 5, 2), (300, 384, 256, 2, 1), (513, 128, 128, 7, 3), (700, 272, 256, 2, 2), (1030, 256, 128, 4, 2)]
+          (200, 256, 1024, 5, 2), (300, 384, 256, 2, 1), (513, 128, 128, 7, 3), (700, 272, 256, 2, 2), (1030, 256, 128, 4, 2), (260, 144, 128, 2, 1), (513, 1024, 768, 3, 1),
+          (1500, 272, 384, 2, 1)]
 
 
 @pytest.mark.parametrize("how", HOWS)
