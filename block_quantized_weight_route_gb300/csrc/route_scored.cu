@@ -130,7 +130,7 @@ __device__ __forceinline__ bool in_groups(const ScoredParams& p, uint32_t kept, 
 }
 
 // The choice in 64 bits, from shared memory: lane j returns the j-th id.  `kept`: the groups that
-// stay, or (again) not known yet; experts whose 32-bit value is below `least` are not among the k.
+// stay, or (again) not known yet; experts whose 32-bit value is below `least` (sigmoid) are not among the k.
 template <bool SCORED, bool GROUPS>
 __device__ __noinline__ int choose64(const ScoredParams& p, long t, int lane, double* c, bool again, uint32_t kept, float least) {
     double m = 0.0, z = 1.0;
@@ -145,17 +145,47 @@ __device__ __noinline__ int choose64(const ScoredParams& p, long t, int lane, do
         }
         z = warp_sum(z);
     }
+    auto value = [&](float l, float b) {
+        if (!SCORED) return (double)l;
+        const double v = (p.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - m) / z) + (double)b;
+        return v == v ? v : -INFINITY;
+    };
+    if (SCORED && p.sigmoid && !again) {
+        // The few that can be among the k, one to a lane: one exponential in 64 bits (1 us, and 8 for a lane's
+        // eight one after the other: at the end of a launch nothing else runs beside it).  A value's
+        // place is the number of those before it.
+        int* list = reinterpret_cast<int*>(c);
+        int n = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int e = e0 + lane;
+            const float l = e < p.E ? logit(p, t, e) : -INFINITY, b = p.bias && e < p.E ? p.bias[e] : 0.0f;
+            const bool in = l > -INFINITY && (!GROUPS || in_groups(p, kept, e)) && fast_sigmoid(l) + b >= least;
+            const uint32_t who = __ballot_sync(kAll, in);
+            const int at = n + __popc(who & ((1u << lane) - 1u));
+            if (in && at < 32) list[at] = e;
+            n += __popc(who);
+        }
+        __syncwarp();
+        if (n <= 32) {
+            const int e = lane < n ? list[lane] : kMaxE;
+            const double v = lane < n ? value(logit(p, t, e), p.bias ? p.bias[e] : 0.0f) : -INFINITY;
+            int before = 0;
+            for (int i = 0; i < n; ++i) {
+                const double o = __shfl_sync(kAll, v, i);
+                before += o > v || (o == v && i < lane);   // (the list is in ascending order)
+            }
+            __syncwarp();
+            if (lane < n && v > -INFINITY) list[before] = e;
+            const int got = __popc(__ballot_sync(kAll, lane < n && v > -INFINITY));
+            __syncwarp();
+            return lane < p.k && lane < got ? list[lane] : -1;
+        }
+        __syncwarp();
+    }
 #pragma unroll 1
     for (int e = lane; e < p.E; e += 32) {
-        const float l = logit(p, t, e), b = p.bias ? p.bias[e] : 0.0f;
-        double v = -INFINITY;
-        if (!SCORED) {
-            v = l;
-        } else if (l > -INFINITY && (again || !p.sigmoid || ((!GROUPS || in_groups(p, kept, e)) && fast_sigmoid(l) + b >= least))) {
-            v = (p.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - m) / z) + (double)b;
-            if (v != v) v = -INFINITY;
-        }
-        c[place(e)] = v;
+        const float l = logit(p, t, e);
+        c[place(e)] = l > -INFINITY ? value(l, p.bias ? p.bias[e] : 0.0f) : -INFINITY;
     }
     __syncwarp();
     bool unused;
