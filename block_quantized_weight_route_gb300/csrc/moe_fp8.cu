@@ -66,6 +66,7 @@ __device__ int block_scan(int v, int* total) {
 __global__ void __launch_bounds__(kThreads) moe_rows_kernel(const int32_t* ids, int P, int E, int k, MoeGroups g) {
     extern __shared__ uint16_t piece[];   // [kPieces][E]: pairs of the expert in a piece, then in the pieces before it
     __shared__ int32_t first[kMoeMaxExperts];   // the chunk's first row of an expert
+    __shared__ int32_t all_pairs[kMoeMaxExperts], earlier_pairs[kMoeMaxExperts];
     launch_dependents();
     wait_prerequisites();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -73,6 +74,17 @@ __global__ void __launch_bounds__(kThreads) moe_rows_kernel(const int32_t* ids, 
     const int n = (int)(P - q0 < kMoeChunk ? P - q0 : kMoeChunk), pieces = (n + 31) / 32;
     for (int i = threadIdx.x; i < (pieces * E + 1) / 2; i += kThreads) reinterpret_cast<uint32_t*>(piece)[i] = 0;
     __syncthreads();
+    if (gridDim.x > 1 && !g.chunk_counts) {   // few chunks: each CTA counts them all
+        for (int e = threadIdx.x; e < E; e += kThreads) all_pairs[e] = earlier_pairs[e] = 0;
+        __syncthreads();
+        for (long q = threadIdx.x; q < P; q += kThreads) {
+            const int e = ids[q];
+            if ((unsigned)e < (unsigned)E) {
+                atomicAdd(&all_pairs[e], 1);
+                if (q < q0) atomicAdd(&earlier_pairs[e], 1);
+            }
+        }
+    }
     int mine[kMoeChunk / kThreads], rank[kMoeChunk / kThreads];
 #pragma unroll
     for (int r = 0; r < kMoeChunk / kThreads; ++r) {
@@ -95,7 +107,10 @@ __global__ void __launch_bounds__(kThreads) moe_rows_kernel(const int32_t* ids, 
             run += v;
         }
         total = run;
-        if (gridDim.x > 1) {
+        if (gridDim.x > 1 && !g.chunk_counts) {
+            total = all_pairs[e];
+            before = earlier_pairs[e];
+        } else if (gridDim.x > 1) {
             total = 0;
 #pragma unroll 8
             for (int c = 0; c < (int)gridDim.x; ++c) {
@@ -240,12 +255,15 @@ cudaError_t launch_moe_group(const int32_t* ids, int P, int E, int k, const MoeG
         ready.set(dev, 1);
     }
     const int chunks = (P + kMoeChunk - 1) / kMoeChunk;
-    if (chunks > 1) {
+    // (up to eight chunks a launch that counts them costs more than each CTA counting all)
+    MoeGroups groups = g;
+    if (chunks <= 8) groups.chunk_counts = nullptr;
+    if (chunks > 8) {
         const cudaError_t e = launch(moe_count_kernel, chunks, kThreads, 0, s, ids, P, E, g.chunk_counts);
         if (e != cudaSuccess) return e;
     }
     const int pieces = P < kMoeChunk ? (P + 31) / 32 : kPieces;
-    return launch(moe_rows_kernel, chunks, kThreads, ((size_t)pieces * E * 2 + 3) / 4 * 4, s, ids, P, E, k, g);
+    return launch(moe_rows_kernel, chunks, kThreads, ((size_t)pieces * E * 2 + 3) / 4 * 4, s, ids, P, E, k, groups);
 }
 
 cudaError_t launch_moe_gather(const uint8_t* Xq, const float* Xs, int P, int D, const MoeGroups& g, int E, uint8_t* Xp, float* Xps,
