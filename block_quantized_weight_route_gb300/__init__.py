@@ -113,6 +113,10 @@ def lib() -> ctypes.CDLL:
         L.moe_expert_stage_fp8_workspace_layout.argtypes = [i32, i32, i32, i32, i32, P]
         L.moe_expert_stage_fp8.restype = i32
         L.moe_expert_stage_fp8.argtypes = [P, P, P, P, i32, i32, i32, i32, i32, P, P, P, P, P, i64, i32, P, i32, P, sz, P]
+        L.qmm_dbg_moe_fp8_plan.restype = i32
+        L.qmm_dbg_moe_fp8_plan.argtypes = [i32, i32, i32, i32, i32, P]
+        L.qmm_dbg_moe_expert_stage_fp8.restype = i32
+        L.qmm_dbg_moe_expert_stage_fp8.argtypes = L.moe_expert_stage_fp8.argtypes[:-1] + [P, P]
         L.qmm_dbg_fp8a8_epilogue_blk128.restype = i32
         L.qmm_dbg_fp8a8_epilogue_blk128.argtypes = [P, P, i32, i32, i32, P, P, P, i32, i32, P, i64, i32, P, i32, P, P]
         L.qmm_dbg_fp8a8_plan.restype = i32
@@ -557,13 +561,8 @@ def moe_expert_stage_fp8_workspace_layout(T: int, D: int, F: int, E: int, k: int
     return dict(zip(MOE_FP8_WS_FIELDS, [int(v) for v in arr]))
 
 
-def moe_expert_stage_fp8(Xq, Xs, ids, w, Wgu, Sgu, Wd, Sd, R=None, out_dtype=torch.bfloat16, Y=None, ws=None):
-    """The routed expert stage over FP8 weights: Y[t] = R[t] + sum_j w[t,j] * Wd[e] . fp8(silu(g) * u),
-    e = ids[t, j] (outside [0, E): nothing), g and u the gate and up rows of Wgu[e] times X[t].
-    Xq [T, D] E4M3 and Xs [T, ceil(D/128)] fp32 (as qmm_add_rmsnorm_fp8 gives them), ids int32 and
-    w fp32 [T, k] (as moe_route_scored gives them), Wgu [E, 2F, D] (gate rows first) with Sgu [E, 2F/128,
-    ceil(D/128)], Wd [E, D, F] with Sd [E, ceil(D/128), F/128], R [T, D] fp32 or bf16 (a row slice,
-    or Y itself).  ws: a uint8 tensor of moe_expert_stage_fp8_workspace_size bytes (default: allocated)."""
+def _stage_fp8_args(Xq, Xs, ids, w, Wgu, Sgu, Wd, Sd, R, out_dtype, Y, ws):
+    """Checked arguments of the FP8 expert stage: (Y, what has to live until the call is made, its arguments up to the stream)."""
     dev = _device(Xq, "Xq")
     T, D = Xq.shape
     k = ids.shape[1]
@@ -594,9 +593,20 @@ def moe_expert_stage_fp8(Xq, Xs, ids, w, Wgu, Sgu, Wd, Sd, R=None, out_dtype=tor
     elif not _ok(ws, _U8, (ws.numel(),), dev):
         _need(ws, "ws", _U8, (ws.numel(),))
     Xs, Sgu, Sd, ids, w = _aligned(Xs), _aligned(Sgu), _aligned(Sd), _aligned(ids), _aligned(w)
-    st = lib().moe_expert_stage_fp8(Xq.data_ptr(), Xs.data_ptr(), ids.data_ptr(), w.data_ptr(), T, D, F, E, k, Wgu.data_ptr(),
-                                    Sgu.data_ptr(), Wd.data_ptr(), Sd.data_ptr(), r, ldr, rdt, Y.data_ptr(),
-                                    _DTYPE[out_dtype], ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    return Y, (Xs, Sgu, Sd, ids, w, R, ws), (Xq.data_ptr(), Xs.data_ptr(), ids.data_ptr(), w.data_ptr(), T, D, F, E, k,
+                                             Wgu.data_ptr(), Sgu.data_ptr(), Wd.data_ptr(), Sd.data_ptr(), r, ldr, rdt,
+                                             Y.data_ptr(), _DTYPE[out_dtype], ws.data_ptr(), ws.numel())
+
+
+def moe_expert_stage_fp8(Xq, Xs, ids, w, Wgu, Sgu, Wd, Sd, R=None, out_dtype=torch.bfloat16, Y=None, ws=None):
+    """The routed expert stage over FP8 weights: Y[t] = R[t] + sum_j w[t,j] * Wd[e] . fp8(silu(g) * u),
+    e = ids[t, j] (outside [0, E): nothing), g and u the gate and up rows of Wgu[e] times X[t].
+    Xq [T, D] E4M3 and Xs [T, ceil(D/128)] fp32 (as qmm_add_rmsnorm_fp8 gives them), ids int32 and
+    w fp32 [T, k] (as moe_route_scored gives them), Wgu [E, 2F, D] (gate rows first) with Sgu [E, 2F/128,
+    ceil(D/128)], Wd [E, D, F] with Sd [E, ceil(D/128), F/128], R [T, D] fp32 or bf16 (a row slice,
+    or Y itself).  ws: a uint8 tensor of moe_expert_stage_fp8_workspace_size bytes (default: allocated)."""
+    Y, keep, args = _stage_fp8_args(Xq, Xs, ids, w, Wgu, Sgu, Wd, Sd, R, out_dtype, Y, ws)
+    st = lib().moe_expert_stage_fp8(*args, _raw_stream(Xq.get_device()))
     if st:
         _check("moe_expert_stage_fp8", st)
     return Y
@@ -840,6 +850,25 @@ def qmm_dbg_fp8a8_swiglu_blk128(Xq, Xs, Wgu, Sgu, plan):
            lib().qmm_dbg_fp8a8_swiglu_blk128(_ptr(Xq), _ptr(Xs), M, K, F, _ptr(Wgu), _ptr(Sgu), _ptr(Hq), _ptr(Hs),
                                              ctypes.cast(_plan_array(plan), ctypes.c_void_p), _stream(Xq.device)))
     return Hq, Hs
+
+
+QMM_MOE_FP8_PLAN_FIELDS = 4
+
+
+def qmm_dbg_moe_fp8_plan(T: int, D: int, F: int, E: int, k: int) -> tuple:
+    """The tiling that the FP8 expert stage takes: (many, tn, cs of gate/up, cs of down)."""
+    arr = (ctypes.c_int * QMM_MOE_FP8_PLAN_FIELDS)()
+    _check("qmm_dbg_moe_fp8_plan", lib().qmm_dbg_moe_fp8_plan(T, D, F, E, k, ctypes.cast(arr, ctypes.c_void_p)))
+    return tuple(arr)
+
+
+def qmm_dbg_moe_expert_stage_fp8(Xq, Xs, ids, w, Wgu, Sgu, Wd, Sd, plan, R=None, out_dtype=torch.bfloat16, Y=None, ws=None):
+    """moe_expert_stage_fp8 by a given tiling."""
+    Y, keep, args = _stage_fp8_args(Xq, Xs, ids, w, Wgu, Sgu, Wd, Sd, R, out_dtype, Y, ws)
+    arr = (ctypes.c_int * QMM_MOE_FP8_PLAN_FIELDS)(*plan)
+    _check("qmm_dbg_moe_expert_stage_fp8",
+           lib().qmm_dbg_moe_expert_stage_fp8(*args, ctypes.cast(arr, ctypes.c_void_p), _stream(Xq.device)))
+    return Y
 
 
 def qmm_dbg_wait_timeout(timeout_us: int, device=None) -> None:

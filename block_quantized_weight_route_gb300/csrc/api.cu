@@ -1189,13 +1189,15 @@ qmm_status moe_expert_stage_fp8_workspace_layout(int T, int D, int F, int E, int
     return st;
 }
 
-qmm_status moe_expert_stage_fp8(const uint8_t* Xq, const float* Xs, const int32_t* ids, const float* w, int T, int D,
+// The stage, by the rule's kernels or (fields) given ones.
+static qmm_status moe_stage_fp8(const char* who, const uint8_t* Xq, const float* Xs, const int32_t* ids, const float* w, int T, int D,
                                 int F, int E, int k, const uint8_t* Wgu, const float* Sgu, const uint8_t* Wd,
                                 const float* Sd, const void* R, int64_t ldr, qmm_dtype rdt, void* Y, qmm_dtype ydt,
-                                void* ws, size_t ws_bytes, cudaStream_t stream) {
-    const char* who = "moe_expert_stage_fp8";
+                                void* ws, size_t ws_bytes, const int* fields, cudaStream_t stream) {
     qmm_status st = check_moe_fp8_shape(who, T, D, F, E, k);
     if (st != QMM_OK) return st;
+    const MoePlan given = fields ? MoePlan{fields[0] != 0, fields[1], fields[2], fields[3]} : MoePlan{};
+    if (fields && !moe_plan_fits(given, T, D, F, E, k)) return fail(QMM_ERR_INVALID_ARG, "%s: no such tiling of this shape", who);
     if (!is_dtype(ydt) || (R && !is_dtype(rdt))) return fail(QMM_ERR_INVALID_ARG, "%s: bad type", who);
     if (!Wgu || !Sgu || !Wd || !Sd || (T > 0 && (!Xq || !Xs || !ids || !w || !Y || !ws)))
         return fail(QMM_ERR_INVALID_ARG, "%s: null pointer", who);
@@ -1213,9 +1215,9 @@ qmm_status moe_expert_stage_fp8(const uint8_t* Xq, const float* Xs, const int32_
     st = device_state(&d);
     if (st != QMM_OK || T == 0) return st;
 
-    MoePlan plan;
-    cudaError_t e = moe_plan(T, D, F, E, k, d->sms, d->index, &plan);
-    if (e != cudaSuccess) return cuda_fail(e, who);
+    MoePlan plan = given;
+    cudaError_t e = cudaSuccess;
+    if (!fields && (e = moe_plan(T, D, F, E, k, d->sms, d->index, &plan)) != cudaSuccess) return cuda_fail(e, who);
     const int P = T * k;
     uint8_t* base = static_cast<uint8_t*>(ws);
     auto at = [&](int i) { return static_cast<void*>(base + off[i]); };
@@ -1285,6 +1287,39 @@ qmm_status moe_expert_stage_fp8(const uint8_t* Xq, const float* Xs, const int32_
     }
     e = launch_moe_combine(y, y_unit, g.row, w, T, k, D, R, rdt == QMM_BF16, (long)ldr, Y, ydt == QMM_BF16, stream);
     return e == cudaSuccess ? QMM_OK : cuda_fail(e, "moe_expert_stage_fp8: combine");
+}
+
+qmm_status moe_expert_stage_fp8(const uint8_t* Xq, const float* Xs, const int32_t* ids, const float* w, int T, int D,
+                                int F, int E, int k, const uint8_t* Wgu, const float* Sgu, const uint8_t* Wd,
+                                const float* Sd, const void* R, int64_t ldr, qmm_dtype rdt, void* Y, qmm_dtype ydt,
+                                void* ws, size_t ws_bytes, cudaStream_t stream) {
+    return moe_stage_fp8("moe_expert_stage_fp8", Xq, Xs, ids, w, T, D, F, E, k, Wgu, Sgu, Wd, Sd, R, ldr, rdt, Y, ydt, ws, ws_bytes,
+                         nullptr, stream);
+}
+
+qmm_status qmm_dbg_moe_fp8_plan(int T, int D, int F, int E, int k, int* plan) {
+    if (!plan) return fail(QMM_ERR_INVALID_ARG, "qmm_dbg_moe_fp8_plan: null pointer");
+    qmm_status st = check_moe_fp8_shape("qmm_dbg_moe_fp8_plan", T, D, F, E, k);
+    if (st != QMM_OK) return st;
+    if (T == 0) return fail(QMM_ERR_UNSUPPORTED_SHAPE, "qmm_dbg_moe_fp8_plan: no tokens");
+    DeviceState* d = nullptr;
+    if ((st = device_state(&d)) != QMM_OK) return st;
+    MoePlan r;
+    const cudaError_t e = moe_plan(T, D, F, E, k, d->sms, d->index, &r);
+    if (e != cudaSuccess) return cuda_fail(e, "qmm_dbg_moe_fp8_plan");
+    const int f[QMM_MOE_FP8_PLAN_FIELDS] = {r.many, r.tn, r.cs_gate_up, r.cs_down};
+    memcpy(plan, f, sizeof f);
+    return QMM_OK;
+}
+
+qmm_status qmm_dbg_moe_expert_stage_fp8(const uint8_t* Xq, const float* Xs, const int32_t* ids, const float* w, int T,
+                                        int D, int F, int E, int k, const uint8_t* Wgu, const float* Sgu,
+                                        const uint8_t* Wd, const float* Sd, const void* R, int64_t ldr, qmm_dtype rdt,
+                                        void* Y, qmm_dtype ydt, void* ws, size_t ws_bytes, const int* plan,
+                                        cudaStream_t stream) {
+    if (!plan) return fail(QMM_ERR_INVALID_ARG, "qmm_dbg_moe_expert_stage_fp8: null pointer");
+    return moe_stage_fp8("qmm_dbg_moe_expert_stage_fp8", Xq, Xs, ids, w, T, D, F, E, k, Wgu, Sgu, Wd, Sd, R, ldr, rdt, Y, ydt, ws, ws_bytes,
+                         plan, stream);
 }
 
 qmm_status qmm_profile_enable(int on) {

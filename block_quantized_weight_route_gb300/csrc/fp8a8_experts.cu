@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
                     const float2 h = unpack2(acc[j]);
                     a = max_nan_abs(a, h.x, h.y);
                 }
-                float* rm = rowmax + parity * 512 + row;
+                float* rm = rowmax + parity * (C::GROUPS * 128) + row;
                 rm[cq * 128] = a;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&rm_full[parity]);

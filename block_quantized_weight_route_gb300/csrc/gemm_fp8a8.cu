@@ -184,6 +184,14 @@ cudaError_t moe_plan(int T, int D, int F, int E, int k, int sms, int dev, MoePla
     return cudaSuccess;
 }
 
+bool moe_plan_fits(const MoePlan& pl, int T, int D, int F, int E, int k) {
+    if (pl.many) return pl.tn == 128;
+    bool tile = false;
+    for (int tn : kTn) tile |= pl.tn == tn;
+    return tile && pl.cs_gate_up >= 1 && pl.cs_gate_up <= 8 && pl.cs_gate_up <= (D + 127) / 128 && pl.cs_down >= 1 && pl.cs_down <= 8 &&
+           pl.cs_down <= F / 128 && (long)T * k / pl.tn + E <= 65535;
+}
+
 static bool plan_fits(const Fp8a8Plan& pl, int M, int kbs, int cols, bool gated) {
     if (pl.pair) {
         for (int i = 0; i < (gated ? 1 : 3); ++i)

@@ -202,6 +202,7 @@ struct MoePlan {
     bool many;           // the kernel for many rows an expert (tiles of 128), else the narrow one
     int tn, cs_gate_up, cs_down;
 };
+bool moe_plan_fits(const MoePlan& pl, int T, int D, int F, int E, int k);   // whether the kernels can run a given tiling
 cudaError_t moe_plan(int T, int D, int F, int E, int k, int sms, int dev, MoePlan* plan);
 bool fp8a8_plans_fit(const Fp8a8Plans& r, int M, int K, int N, bool gated);   // whether the kernels can run a given tiling
 // clusters of cs CTAs that the device holds at once (0: none)

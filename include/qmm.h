@@ -448,6 +448,22 @@ qmm_status qmm_dbg_fp8a8_epilogue_blk128(const uint8_t *Xq, const float *Xs, int
                                          cudaStream_t stream);
 
 /*
+ * qmm_dbg_moe_* -- the tilings of the FP8 expert stage, so that each can be checked by itself.
+ *   A tiling is QMM_MOE_FP8_PLAN_FIELDS ints: {many, tn, cs of gate/up, cs of down}.  many != 0: tiles of
+ *   tn = 128 rows x 256 columns on persistent CTAs; many == 0: tiles of tn rows (16, 32, 64 or 128) x 128
+ *   columns, K over clusters of cs CTAs (1 to 8, at most the K blocks).
+ * qmm_dbg_moe_fp8_plan -- the tiling that moe_expert_stage_fp8 takes on the current device.
+ * qmm_dbg_moe_expert_stage_fp8 -- the stage by a given tiling.
+ */
+#define QMM_MOE_FP8_PLAN_FIELDS 4
+qmm_status qmm_dbg_moe_fp8_plan(int T, int D, int F, int E, int k, int *plan);
+qmm_status qmm_dbg_moe_expert_stage_fp8(const uint8_t *Xq, const float *Xs, const int32_t *ids, const float *w, int T,
+                                        int D, int F, int E, int k, const uint8_t *Wgu, const float *Sgu,
+                                        const uint8_t *Wd, const float *Sd, const void *R, int64_t ldr, qmm_dtype rdt,
+                                        void *Y, qmm_dtype ydt, void *ws, size_t ws_bytes, const int *plan,
+                                        cudaStream_t stream);
+
+/*
  * qmm_dbg_wait_timeout -- test hook for failure detection (no counterpart on
  * the pages).  Launches one warp that waits, with the same bounded mbarrier
  * wait every kernel of the library uses, on a barrier that nothing arrives on;

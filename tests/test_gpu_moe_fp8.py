@@ -65,7 +65,7 @@ def choice(seed, T, E, k, how):
     return ids.to(torch.int32).cuda(), w.cuda()
 
 
-def check(q, seed, T, D, F, E, k, how="even", dt=F32, res=None, weights=None):
+def check(q, seed, T, D, F, E, k, how="even", dt=F32, res=None, weights=None, plan=None):
     Wgu, Sgu, Wd, Sd = weights or experts(seed, D, F, E)
     Xq, Xs = tokens(seed + 1, T, D)
     ids, w = choice(seed + 2, T, E, k, how)
@@ -73,7 +73,10 @@ def check(q, seed, T, D, F, E, k, how="even", dt=F32, res=None, weights=None):
     P, kb = T * k, -(-D // 128)
     ws = torch.empty(q.moe_expert_stage_fp8_workspace_size(T, D, F, E, k) + 256, dtype=torch.uint8, device="cuda")
     ws.fill_(0x7F)   # (NaN codes and large scales in what nothing writes)
-    Y = q.moe_expert_stage_fp8(Xq, Xs, ids, w, Wgu, Sgu, Wd, Sd, R=R, out_dtype=dt, ws=ws[:-256])
+    if plan is None:
+        Y = q.moe_expert_stage_fp8(Xq, Xs, ids, w, Wgu, Sgu, Wd, Sd, R=R, out_dtype=dt, ws=ws[:-256])
+    else:
+        Y = q.qmm_dbg_moe_expert_stage_fp8(Xq, Xs, ids, w, Wgu, Sgu, Wd, Sd, plan, R=R, out_dtype=dt, ws=ws[:-256])
     q.qmm_check_status()
     assert ws[-256:].eq(0x7F).all()
     lay = q.moe_expert_stage_fp8_workspace_layout(T, D, F, E, k)
@@ -124,12 +127,42 @@ SHAPES = [(1, 256, 128, 8, 2), (1, 2048, 768, 16, 8), (2, 16, 128, 3, 1), (3, 14
           (17, 272, 128, 4, 3), (33, 1000 // 16 * 16, 256, 6, 4), (64, 512, 128, 12, 6), (100, 2000, 256, 4, 4), (129, 640, 512, 3, 2),
           (200, 256, 1024, 5, 2), (300, 384, 256, 2, 1), (513, 128, 128, 7, 3), (700, 272, 256, 2, 2), (1030, 256, 128, 4, 2), (260, 144, 128, 2, 1), (513, 1024, 768, 3, 1),
           (1500, 272, 384, 2, 1)]
+MANY = (1, 128, 1, 1)
 
 
 @pytest.mark.parametrize("how", HOWS)
 @pytest.mark.parametrize("i", range(len(SHAPES)))
 def test_stage(q, i, how):
     check(q, 10 * i, *SHAPES[i], how=how, dt=[F32, BF16][i % 2], res=[None, F32, BF16][(i + len(how)) % 3])
+
+
+@pytest.mark.parametrize("how", HOWS)
+@pytest.mark.parametrize("i", range(len(SHAPES)))
+def test_tiles_of_128_rows(q, i, how):
+    """Every shape by the kernel for many rows an expert."""
+    check(q, 10 * i + 1, *SHAPES[i], how=how, dt=[BF16, F32][i % 2], res=[None, F32, BF16][(i + len(how)) % 3], plan=MANY)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("T,D,F,E,k", [(64, 2048, 768, 64, 4), (700, 400, 384, 96, 3), (300, 1008, 1024, 48, 4), (2500, 272, 256, 130, 2), (500, 2320, 128, 200, 4),
+                                       (40, 128, 1280, 100, 4), (3000, 640, 640, 3, 2)])
+def test_more_tiles_than_ctas(q, T, D, F, E, k, dt):
+    """Several tiles a persistent CTA, of one to twenty K blocks, odd and even."""
+    check(q, T, T, D, F, E, k, dt=dt, res=BF16, plan=MANY)
+    check(q, T, T, D, F, E, k, how="holes", dt=dt, plan=MANY)
+
+
+@pytest.mark.parametrize("tn", [16, 32, 64, 128])
+@pytest.mark.parametrize("cs", [(1, 1), (2, 2), (3, 1), (1, 2), (8, 2)])
+def test_tiles_of_few_rows(q, tn, cs):
+    for n, (shape, how) in enumerate([((3, 1040, 256, 5, 4), "even"), ((200, 1040, 256, 3, 2), "skewed"), ((90, 1024, 256, 40, 6), "holes"), ((40, 1040, 256, 2, 3), "twice")]):
+        check(q, tn + n, *shape, how=how, dt=[F32, BF16][n % 2], res=[BF16, None][n % 2], plan=(0, tn, *cs))
+
+
+def test_the_rule_reaches_both_kernels(q):
+    plans = {q.qmm_dbg_moe_fp8_plan(T, 2048, 768, 128, 8)[0] for T in (1, 8, 301, 5268)}
+    assert plans == {0, 1}
+    check(q, 77, 301, 512, 768, 128, 8, dt=BF16)
 
 
 @pytest.mark.parametrize("T,k,E", [(2048, 1, 512), (300, 16, 512), (1025, 2, 2), (2049, 3, 40), (5000, 2, 8)])
@@ -263,6 +296,9 @@ def test_refusals(q):
                              ("out_dtype", torch.float16, TypeError)]:
         with pytest.raises(error):
             q.moe_expert_stage_fp8(**{**good, name: bad})
+    for plan in ((1, 64, 1, 1), (0, 48, 1, 1), (0, 16, 3, 1), (0, 16, 1, 2), (0, 16, 0, 1), (0, 16, 1, 9)):   # (2 K blocks, 1)
+        with pytest.raises(q.QmmError):
+            q.qmm_dbg_moe_expert_stage_fp8(**good, plan=plan)
     x = torch.zeros(5, 256, device="cuda")
     with pytest.raises(q.QmmError):   # in place, of another type
         q.moe_expert_stage_fp8(**good, R=x, Y=x.view(-1)[:640].view(BF16).view(5, 256))
