@@ -84,18 +84,24 @@ __device__ __forceinline__ int place(int e) { return e + (e >> 5) * 4; }
 
 // The groups that stay, as the ballot of their lanes: the lanes share the groups, 2^p.per_shift
 // each.  `c` holds the row's values (-inf: off); `tol` (32 bits): *close is set where the last
-// group that stays and the first that goes are no further apart than their error.
+// group that stays and the first that goes are no further apart than their error.  *least: the smallest
+// value in the lane's group's score.
 template <class F>
-__device__ __forceinline__ uint32_t groups_kept(const ScoredParams& p, const F* c, int lane, float tol, bool* close) {
+__device__ __forceinline__ uint32_t groups_kept(const ScoredParams& p, const F* c, int lane, float tol, bool* close, F* least) {
     const int per = 1 << p.per_shift, g = lane >> p.per_shift, sub = lane & (per - 1);
     const bool live = g < p.groups;
     F a = -INFINITY, b = -INFINITY;   // the two largest
     if (live) {
         const int end = (g + 1) * p.group_size;
-        for (int e = g * p.group_size + sub; e < end; e += per) {
-            const F v = c[place(e)];
-            b = fmax(b, fmin(a, v));
-            a = fmax(a, v);
+        for (int e = g * p.group_size + sub; e < end; e += 4 * per) {   // (four loads in flight)
+            F v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = e + i * per < end ? c[place(e + i * per)] : (F)-INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                b = fmax(b, fmin(a, v[i]));
+                a = fmax(a, v[i]);
+            }
         }
     }
     for (int o = 1; o < per; o <<= 1) {
@@ -104,6 +110,7 @@ __device__ __forceinline__ uint32_t groups_kept(const ScoredParams& p, const F* 
         a = fmax(a, a2);
     }
     const F score = p.group_top == 1 ? a : b > -INFINITY ? a + b : (F)-INFINITY;
+    *least = p.group_top == 1 ? a : b;
     auto key = live && sub == 0 ? key_of(score) : 0;   // (a live group's is not 0)
     uint32_t kept = 0;
     F last = INFINITY;
@@ -127,6 +134,38 @@ __device__ __forceinline__ uint32_t groups_kept(const ScoredParams& p, const F* 
 // Whether e's group stays (p.group_inv: 2^20 / group_size, rounded up).
 __device__ __forceinline__ bool in_groups(const ScoredParams& p, uint32_t kept, int e) {
     return kept >> (((unsigned)e * p.group_inv >> 20) << p.per_shift & 31u) & 1u;
+}
+
+// A sigmoid's value for the choice in 64 bits (-inf for a bias that is NaN).
+__device__ __forceinline__ double sigmoid64(const ScoredParams& p, long t, int e) {
+    const double v = 1.0 / (1.0 + exp(-(double)logit(p, t, e))) + (p.bias ? (double)p.bias[e] : 0.0);
+    return v == v ? v : -INFINITY;
+}
+
+// The groups that stay, from the 64-bit values of the n <= 32 experts in `list` that can be among the largest of
+// their groups.
+__device__ __noinline__ uint32_t groups64(const ScoredParams& p, long t, int lane, const int* list, int n) {
+    const int e = lane < n ? list[lane] : 0;
+    const double v = lane < n ? sigmoid64(p, t, e) : -INFINITY;
+    const int of = (int)((unsigned)e * p.group_inv >> 20);
+    double a = -INFINITY, b = -INFINITY;   // lane g: the two largest of group g
+    for (int i = 0; i < n; ++i) {
+        const double o = __shfl_sync(kAll, v, i);
+        if (__shfl_sync(kAll, of, i) == lane) {
+            b = fmax(b, fmin(a, o));
+            a = fmax(a, o);
+        }
+    }
+    const double score = p.group_top == 1 ? a : b > -INFINITY ? a + b : -INFINITY;
+    int before = 0;
+    for (int h = 0; h < p.groups; ++h) {
+        const double o = __shfl_sync(kAll, score, h);
+        before += o > score || (o == score && h < lane);
+    }
+    const uint32_t keep = __ballot_sync(kAll, lane < p.groups && before < p.groups_kept);
+    uint32_t kept = 0;
+    for (int h = 0; h < p.groups; ++h) kept |= (keep >> h & 1u) << (h << p.per_shift);
+    return kept;
 }
 
 // The choice in 64 bits, from shared memory: lane j returns the j-th id.  `kept`: the groups that
@@ -168,7 +207,7 @@ __device__ __noinline__ int choose64(const ScoredParams& p, long t, int lane, do
         __syncwarp();
         if (n <= 32) {
             const int e = lane < n ? list[lane] : kMaxE;
-            const double v = lane < n ? value(logit(p, t, e), p.bias ? p.bias[e] : 0.0f) : -INFINITY;
+            const double v = lane < n ? sigmoid64(p, t, e) : -INFINITY;
             int before = 0;
             for (int i = 0; i < n; ++i) {
                 const double o = __shfl_sync(kAll, v, i);
@@ -189,7 +228,8 @@ __device__ __noinline__ int choose64(const ScoredParams& p, long t, int lane, do
     }
     __syncwarp();
     bool unused;
-    if (GROUPS && again) kept = groups_kept<double>(p, c, lane, 0.0f, &unused);
+    double unused_too;
+    if (GROUPS && again) kept = groups_kept<double>(p, c, lane, 0.0f, &unused, &unused_too);
     __syncwarp();
     uint64_t* keys = reinterpret_cast<uint64_t*>(c);
     for (int e = lane; e < p.E; e += 32) {
@@ -306,9 +346,30 @@ __global__ void __launch_bounds__(32 * kWarps) route_scored_kernel(const __grid_
         for (int i = 0; i < EPL; ++i)
             if (lane + 32 * i < p.E) cf[place(lane + 32 * i)] = c[i] > -INFINITY ? c[i] : -INFINITY;
         __syncwarp();
-        kept = groups_kept<float>(p, cf, lane, tol, &again);
+        float least;
+        kept = groups_kept<float>(p, cf, lane, tol, &again, &least);
         again &= SCORED;
         __syncwarp();
+        if (SCORED && again && p.sigmoid) {   // (the same in the whole warp)
+            int* list = reinterpret_cast<int*>(row);
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const unsigned group = (unsigned)(lane + 32 * i) * p.group_inv >> 20;
+                const float l = __shfl_sync(kAll, least, group << p.per_shift & 31u);
+                const bool in = c[i] > -INFINITY && c[i] >= l - 2.0f * (tol + kSumTol * fabsf(l));
+                const uint32_t who = __ballot_sync(kAll, in);
+                const int at = n + __popc(who & ((1u << lane) - 1u));
+                if (in && at < 32) list[at] = lane + 32 * i;
+                n += __popc(who);
+            }
+            __syncwarp();
+            if (n <= 32) {
+                kept = groups64(p, t, lane, list, n);
+                again = false;
+            }
+            __syncwarp();
+        }
     }
     // A lane's keys, sorted, largest first.  A key's low bits give way to the place i in the lane, from
     // which a lower index is larger; keys whose other bits differ order as the values do, and where two

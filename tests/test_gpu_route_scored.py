@@ -111,6 +111,20 @@ def test_scores_closer_than_32_bits_tell(q, E, groups, kept, score):
         check(q, l.cuda(), min(8, E // groups * kept), score=score, bias=bias.cuda(), groups=groups, groups_kept=kept)
 
 
+@pytest.mark.parametrize("top,use_bias", [(1, True), (2, False), (2, True)])
+@pytest.mark.parametrize("E,groups,kept", [(64, 8, 3), (256, 8, 4), (512, 16, 5), (90, 6, 1)])
+def test_groups_closer_than_32_bits_tell(q, E, groups, kept, top, use_bias):
+    """Every group's score is the same but for the rounding of its one or two largest logits; the rest are far below."""
+    g = torch.Generator().manual_seed(E + top)
+    T, size = 40, E // groups
+    l = -6 + 0.1 * torch.randn(T, groups, size, generator=g, dtype=torch.float64)
+    at = torch.rand(T, groups, size, generator=g).argsort(2)[:, :, :2]
+    d = 0.2 * torch.rand(T, groups, generator=g, dtype=torch.float64) if top == 2 else 1e-8 * torch.rand(T, groups, generator=g, dtype=torch.float64)
+    l.scatter_(2, at, torch.logit(torch.stack([0.7 + d, 0.6 - d], 2)))
+    bias = (torch.full((E,), 0.125) if use_bias else torch.zeros(E)).cuda() if use_bias or top == 1 else None
+    check(q, l.reshape(T, E).float().cuda(), min(2 * kept, 8), score="sigmoid", bias=bias, groups=groups, groups_kept=kept, group_top=top)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("use_bias", [False, True])
 def test_ties_go_to_the_lower_index(q, score, use_bias):
