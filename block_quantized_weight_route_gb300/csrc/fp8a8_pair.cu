@@ -38,7 +38,9 @@ namespace {
 
 // RAGGED: Y's row pitch is no multiple of 16 bytes.  BF16: Y is bf16, not fp32.  (One kernel with
 // all four ways to store makes the fold spill.)
-// EPI: y = act(y + bias) + R before the rounding; RAGGED is then Y's or R's pitch no multiple of 4 elements.
+// EPI: y = act(y + bias) + R before the rounding (2048 x 5120 x 17408 with bias and tanh's gelu 188 us, 5268 x 17408 x
+// 5120 onto an fp32 residual 405 us: the K loop as without it, and 4 to 6 us at a tile's end, when every CTA's
+// fold warps stop at about the same time); RAGGED is then Y's or R's pitch no multiple of 4 elements.
 template <int BN_, bool GATED_, bool BF16_ = true, bool RAGGED_ = false, bool EPI_ = false>
 struct PairCfg {
     static constexpr int BN = BN_;

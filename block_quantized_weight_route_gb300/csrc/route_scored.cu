@@ -9,9 +9,12 @@
 // rounded: without a bias (and with group scores of one expert) c grows with the logit
 // and the logits themselves are compared; else c is computed in 32 bits with a bound on its
 // error, and a token with two neighbours in the order closer than that is done again in 64
-// bits (one in some hundred tokens of random logits).  Each of the k rounds is two warp
-// reductions (redux): the largest key, then the lowest index that has it; a lane keeps its
-// keys sorted, so that the next one is in hand.
+// bits (one in a thousand tokens of random logits), for the few experts that it is between.  A round of the
+// choice is one warp reduction (redux) and a ballot: a lane keeps its keys sorted, so that the next one
+// is in hand, and a key carries its place in the lane.
+// Measured with 256 experts, 8 of them a token, sigmoid, bias, 4 of 8 groups: 1 token 3.1 us (in a graph), 5268
+// 12 us, 21504 28 us.  What bounds it is instructions (about 1000 a token, issue slots 80% busy;
+// the logits' 22 MB take 3.3 us): 19 us without groups, 15 without bias either.
 #include <cfloat>
 
 #include "qmm_internal.h"
