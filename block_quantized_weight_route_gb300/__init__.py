@@ -462,8 +462,10 @@ def _epilogue_args(Xq, Xs, W, S, bias, act, R, out_dtype, Y, dev):
     if bias is not None:
         if not _ok(bias, _DTYPE, (N,), dev):
             _need(bias, "bias", tuple(_DTYPE), (N,))
-        bias = _aligned(bias)
         b, bdt = bias.data_ptr(), _DTYPE[bias.dtype]
+        if b & 15:
+            bias = bias.clone()
+            b = bias.data_ptr()
     r, ldr, rdt = None, 0, 0
     if R is not None:
         ldr = _pitch(R, "R", (M, N), dev)
@@ -475,10 +477,13 @@ def _epilogue_args(Xq, Xs, W, S, bias, act, R, out_dtype, Y, dev):
         Y = torch.empty((M, N), dtype=out_dtype, device=Xq.device)
     elif not _ok(Y, (out_dtype,), (M, N), dev):
         _need(Y, "Y", (out_dtype,), (M, N))
-    Xs, S = _aligned(Xs), _aligned(S)
+    xs, s = Xs.data_ptr(), S.data_ptr()
+    if (xs | s) & 15:
+        Xs, S = _aligned(Xs), _aligned(S)
+        xs, s = Xs.data_ptr(), S.data_ptr()
     # (the tensors behind copies are kept until the call is made)
-    return Y, (bias, Xs, S, R), (Xq.data_ptr(), Xs.data_ptr(), M, K, N, W.data_ptr(), S.data_ptr(), b, bdt, QMM_ACTS[act], r, ldr,
-                              rdt, Y.data_ptr(), _DTYPE[out_dtype])
+    return Y, (bias, Xs, S, R), (Xq.data_ptr(), xs, M, K, N, W.data_ptr(), s, b, bdt, QMM_ACTS[act], r, ldr, rdt, Y.data_ptr(),
+                                 _DTYPE[out_dtype])
 
 
 def qmm_fp8a8_epilogue_blk128(Xq, Xs, W, S, bias=None, act: str = "none", R=None, out_dtype=torch.bfloat16, Y=None):

@@ -212,23 +212,25 @@ __device__ __forceinline__ float activate_lanes(float v, int act) {
     return act_finish(x, reciprocal(d * d2) * d2, act);
 }
 
-// act(y + bias) + R of row m, columns n .. n + 3 (what is past the end stays as it is).
-__device__ __forceinline__ float4 epilogue4(const Fp8a8Params& p, long m, int n, float4 y) {
-    float4 b = make_float4(0.f, 0.f, 0.f, 0.f), r = b;
-    if (p.vec4) {
-        if (n >= p.N) return y;
-        if (p.bias) b = load4(p.bias, p.bias_bf16, n);
-        if (p.R) r = load4(p.R, p.r_bf16, m * p.ldr + n);
-    } else {
-        float bb[4] = {}, rr[4] = {};
+// The bias of columns n .. n + 3 and the residual of row m there (past the end zeros), and
+// act(y + bias) + R.
+__device__ __forceinline__ float4 epilogue_bias(const Fp8a8Params& p, int n) {
+    float b[4] = {};
+    if (p.bias && p.vec4 && n < p.N) return load4(p.bias, p.bias_bf16, n);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (p.bias && n + j < p.N) bb[j] = load1(p.bias, p.bias_bf16, n + j);
-            if (p.R && n + j < p.N) rr[j] = load1(p.R, p.r_bf16, m * p.ldr + n + j);
-        }
-        b = make_float4(bb[0], bb[1], bb[2], bb[3]);
-        r = make_float4(rr[0], rr[1], rr[2], rr[3]);
-    }
+    for (int j = 0; j < 4; ++j)
+        if (p.bias && n + j < p.N) b[j] = load1(p.bias, p.bias_bf16, n + j);
+    return make_float4(b[0], b[1], b[2], b[3]);
+}
+__device__ __forceinline__ float4 epilogue_residual(const Fp8a8Params& p, long m, int n) {
+    float r[4] = {};
+    if (p.R && p.vec4 && n < p.N) return load4(p.R, p.r_bf16, m * p.ldr + n);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (p.R && n + j < p.N) r[j] = load1(p.R, p.r_bf16, m * p.ldr + n + j);
+    return make_float4(r[0], r[1], r[2], r[3]);
+}
+__device__ __forceinline__ float4 epilogue4(const Fp8a8Params& p, float4 y, float4 b, float4 r) {
     y = add4(y, b);
     if (p.act) with_activation(p.act, [&](auto act) { y = act(y); });
     return add4(y, r);

@@ -480,14 +480,23 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
         }
     }
 
+    const int n = n0 + lane * 4;
+    float4 bias, residual;   // of the warp's first token: on their way while the cluster meets
+    if constexpr (C::EPI) {
+        const int t = rank + cs * warp;
+        bias = epilogue_bias(p, n);
+        if (t < C::TN && m0 + t < m_end) residual = epilogue_residual(p, (long)m0 + t, n);
+    }
     __syncthreads();
     cluster_sync();   // every CTA's sums are in its shared memory
     for (int t = rank + cs * warp; t < C::TN && m0 + t < m_end; t += cs * (C::THREADS / 32)) {
         const long m = (long)m0 + t;
         const uint32_t a = smem_u32(sums + t * 128 + (C::TOKENS_M ? lane ^ (t & 31) : lane) * 4);
         float4 y = cluster_sum(a, cs);
-        const int n = n0 + lane * 4;
-        if constexpr (C::EPI) y = epilogue4(p, m, n, y);
+        if constexpr (C::EPI) {
+            if (t != rank + cs * warp) residual = epilogue_residual(p, m, n);
+            y = epilogue4(p, y, bias, residual);
+        }
         if constexpr (!C::GATED) {
             const float v[4] = {y.x, y.y, y.z, y.w};
             if (p.y_bf16) {

@@ -271,6 +271,7 @@ qmm_status moe_expert_stage_fp8(const uint8_t *Xq, const float *Xs, const int32_
  *   0 counts [E] i32 (pairs of an expert)   1 offsets [E+1] i32 (its first row)
  *   2 src [P] i32 (a row's token)   3 row [P] i32 (a pair's row, -1: no expert)
  *   4 chunk counts   5 tile list   6 its count   7 X rows [P][D] E4M3   8 their scales [P][ceil(D/128)]
+ *   (7 and 8 are written where there are many rows an expert; else the product gathers its tokens)
  *   9 Hq [P][F] E4M3   10 Hs [P][F/128] fp32   11 y [P][D] (fp32, or fp16 in units of 12)
  *  12 units [P][ceil(D/64)]   13 total size */
 #define QMM_MOE_FP8_WS_FIELDS 14

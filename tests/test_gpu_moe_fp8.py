@@ -184,6 +184,8 @@ def test_tokens_without_experts(q, T):
     ids, w = choice(0, T, 4, 3, "none")
     assert torch.equal(q.moe_expert_stage_fp8(Xq, Xs, ids, w, Wgu, Sgu, Wd, Sd, R=R, out_dtype=F32), R)
     assert q.moe_expert_stage_fp8(Xq, Xs, ids, w, Wgu, Sgu, Wd, Sd).eq(0).all()
+    for plan in (MANY, (0, 16, 1, 1), (0, 128, 2, 1)):
+        assert torch.equal(q.qmm_dbg_moe_expert_stage_fp8(Xq, Xs, ids, w, Wgu, Sgu, Wd, Sd, plan, R=R, out_dtype=F32), R)
     assert q.moe_expert_stage_fp8(Xq[:0], Xs[:0], ids[:0], w[:0], Wgu, Sgu, Wd, Sd).shape == (0, 256)
     q.qmm_check_status()
 
