@@ -241,7 +241,7 @@ __device__ __forceinline__ SmallGroup small_group(const Fp8a8Params& p, int lane
     g.rank = __popc(same & ((1u << lane) - 1u));
     g.count = __popc(same);
     g.row = g.rank;
-    for (int i = 0; i < 32; ++i) g.row += __shfl_sync(0xffffffffu, key, i) < key;
+    for (int i = 0; i < p.M; ++i) g.row += __shfl_sync(0xffffffffu, key, i) < key;   // (lanes past the pairs: the largest key)
     return g;
 }
 // The same as the grouping kernels leave in the workspace (a warp; the tiles in the order of their first pairs).
@@ -251,7 +251,7 @@ __device__ __noinline__ void write_small_group(const Fp8a8Params& p, int lane, i
     for (int e0 = 0; e0 <= p.E; e0 += 32) {
         const int e = e0 + lane;
         int before = 0, own = 0;
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < p.M; ++i) {
             const int o = __shfl_sync(0xffffffffu, key, i);
             before += o < e;
             own += o == e;

@@ -171,6 +171,14 @@ def test_grouping_over_several_chunks(q, T, k, E):
     check(q, T, T, 128, 128, E, k, how="holes")
 
 
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("T,D,k", [(1216, 1040, 2), (1217, 1040, 2), (1216, 2064, 6), (1217, 2064, 6), (1300, 1024, 16)])
+def test_rows_summed_in_one_block_or_several(q, T, D, k, dt):
+    """Both ways to give a token's columns to blocks, on both sides of the rule and with a part of a block left."""
+    check(q, T, T, D, 128, 4, k, how="holes", dt=dt, res=BF16, plan=(0, 64, 1, 1))
+    check(q, T, T, D, 128, 4, k, how="holes", dt=dt, plan=MANY)
+
+
 def test_more_experts_than_pairs_and_more_choices_than_experts(q):
     check(q, 1, 3, 256, 128, 512, 2)
     check(q, 2, 40, 256, 128, 2, 16)
