@@ -211,6 +211,25 @@ def test_nan_rows_stay_in_their_token(q):
     assert got[[0, 7, 39]].isnan().all() and torch.equal(got[rest], want[rest])
 
 
+@pytest.mark.parametrize("plan", [MANY, (0, 16, 1, 1), (0, 128, 2, 1)])
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_what_is_not_finite_stays_in_its_token(q, plan, dt):
+    """NaN codes, scales that are infinite, NaN or near the largest number: the other tokens' bits are as without them."""
+    T, D, F, E, k = 301, 272, 256, 3, 2
+    Wgu, Sgu, Wd, Sd = experts(4, D, F, E)
+    Xq, Xs = tokens(4, T, D)
+    ids, w = choice(4, T, E, k, "even")
+    want = q.qmm_dbg_moe_expert_stage_fp8(Xq, Xs, ids, w, Wgu, Sgu, Wd, Sd, plan, out_dtype=dt)
+    assert want.isfinite().all()
+    code, scale, weight = Xq.clone(), Xs.clone(), w.clone()
+    code.view(torch.uint8)[[0, 300], 5] = 0x7F
+    scale[7, 0], scale[31, 1], scale[32, 2], weight[140, 1] = float("nan"), float("inf"), 3e38, float("nan")
+    got = q.qmm_dbg_moe_expert_stage_fp8(code, scale, ids, weight, Wgu, Sgu, Wd, Sd, plan, out_dtype=dt)
+    rest = [t for t in range(T) if t not in (0, 7, 31, 32, 140, 300)]
+    assert got[[0, 7, 140, 300]].isnan().all() and torch.equal(got[rest], want[rest])
+    q.qmm_check_status()
+
+
 @pytest.mark.parametrize("T", [1, 5, 300])
 @pytest.mark.parametrize("dt", [F32, BF16])
 def test_residual_in_place_slices_and_repeats(q, T, dt):
