@@ -24,7 +24,7 @@
 // 3.6 TB/s; 6.0 where the weights are in L2); at 128 tokens a tile shared memory (32 KB
 // written and read a K block, 0.27 of the 0.30 us it takes; 300 x 5120 x 5120: 16.7 us).
 // GROUPED, the expert stage (D = 2048, F = 768, 128 experts, 8 a token): one token 18.4 us in all three
-// launches (38 MB of weights, floor 5.6), 4 tokens 36 us, 8 tokens 61 us; what bounds it is each launch's start, first
+// launches (38 MB of weights, floor 5.6), 4 tokens 38 us, 8 tokens 61 us; what bounds it is each launch's start, first
 // bytes and cluster sum, and from two waves of CTAs on a start for each.
 #include "fp8a8.cuh"
 
