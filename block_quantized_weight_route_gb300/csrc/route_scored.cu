@@ -127,9 +127,11 @@ __device__ __forceinline__ uint32_t groups_kept(const ScoredParams& p, const F* 
     }
     if constexpr (sizeof(F) == 4) {
         const uint32_t next = warp_max(key);
-        const float parts = fabsf(a) + fabsf(b);
-        const float size = __uint_as_float(__reduce_max_sync(kAll, live && parts < INFINITY ? __float_as_uint(parts) : 0u));
-        *close = next > key_of(-INFINITY) && last - value_of(next) <= 2.0f * (tol + kSumTol * size);
+        // (infinite biases add exactly; a finite sum past the largest number makes the size infinite: 64 bits decide)
+        const float x = fabsf(a), y = p.group_top == 1 ? 0.0f : fabsf(b);
+        const float parts = (x < INFINITY ? x : 0.0f) + (y < INFINITY ? y : 0.0f);
+        const float size = __uint_as_float(__reduce_max_sync(kAll, live ? __float_as_uint(parts) : 0u));
+        *close = size == INFINITY || (next > key_of(-INFINITY) && last - value_of(next) <= 2.0f * (tol + kSumTol * size));
     }
     return kept;
 }
@@ -360,7 +362,8 @@ __global__ void __launch_bounds__(32 * kWarps) route_scored_kernel(const __grid_
             for (int i = 0; i < EPL; ++i) {
                 const unsigned group = (unsigned)(lane + 32 * i) * p.group_inv >> 20;
                 const float l = __shfl_sync(kAll, least, group << p.per_shift & 31u);
-                const bool in = c[i] > -INFINITY && c[i] >= l - 2.0f * (tol + kSumTol * fabsf(l));
+                const float margin = fabsf(l) < INFINITY ? 2.0f * (tol + kSumTol * fabsf(l)) : 0.0f;
+                const bool in = c[i] > -INFINITY && c[i] >= l - margin;
                 const uint32_t who = __ballot_sync(kAll, in);
                 const int at = n + __popc(who & ((1u << lane) - 1u));
                 if (in && at < 32) list[at] = lane + 32 * i;

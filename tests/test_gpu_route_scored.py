@@ -177,6 +177,45 @@ def test_infinite_logits(q):
     assert ids[:2].eq(-1).all() and w[:2].eq(0).all() and ids[2].ge(0).all()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("kept,k", [(1, 2), (2, 6), (3, 16)])
+def test_infinite_biases_beside_groups_that_tie(q, score, kept, k):
+    g = torch.Generator().manual_seed(k)
+    logits = torch.randn(40, 64, generator=g)
+    logits[:, 16:32] = logits[:, :16]   # (groups 0 and 1 tie)
+    for off in [(33, 40), (33, 40, 50), (33, 40, 50, 51)]:
+        bias = torch.full((64,), 0.25)
+        bias[list(off)] = float("inf")
+        check(q, logits.cuda(), k, score=score, bias=bias.cuda(), groups=4, groups_kept=kept, group_top=2)
+        check(q, logits.cuda(), k, score=score, bias=bias.cuda(), groups=4, groups_kept=kept, group_top=1)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("kept,k", [(1, 2), (2, 6)])
+def test_sums_of_a_group_beyond_32_bits(q, score, sign, kept, k):
+    logits = torch.randn(40, 64, generator=torch.Generator().manual_seed(k))
+    bias = sign * torch.tensor([2.0e38, 2.5e38, 3.0e38, 2.2e38]).repeat_interleave(16)
+    check(q, logits.cuda(), k, score=score, bias=bias.cuda(), groups=4, groups_kept=kept, group_top=2)
+    bias[:48] = sign * 1.7014118e38   # (their sums are the largest number, or round to it or past it)
+    bias[16:32] = sign * 1.7014117e38
+    check(q, logits.cuda(), k, score=score, bias=bias.cuda(), groups=4, groups_kept=kept, group_top=2)
+
+
+@pytest.mark.parametrize("E,groups", [(32, 32), (64, 32), (24, 24), (33, 11)])
+@pytest.mark.parametrize("at", [100.0, -3000.0])
+def test_large_biases_of_single_experts(q, E, groups, at):
+    """Groups decided by one expert, whose sums differ by what a large bias rounds off."""
+    g = torch.Generator().manual_seed(E)
+    for _ in range(4):
+        logits = 2 * torch.randn(1, E, generator=g)
+        bias = (at - torch.sigmoid(logits.double()))[0].float()
+        logits = logits + 1e-6 * torch.randn(60, E, generator=g)
+        if groups < E:
+            logits[:, ::E // groups] = float("-inf")   # (a group with fewer)
+        check(q, logits.cuda(), 4, score="sigmoid", bias=bias.cuda(), groups=groups, groups_kept=4, group_top=1)
+
+
 @pytest.mark.parametrize("n", [-3, 0, 1, 77, 199, 200, 1000])
 def test_live_tokens(q, n):
     logits = torch.randn(200, 64, generator=torch.Generator().manual_seed(1)).cuda()
