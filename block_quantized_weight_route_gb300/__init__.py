@@ -570,8 +570,10 @@ def _stage_fp8_args(Xq, Xs, ids, w, Wgu, Sgu, Wd, Sd, R, out_dtype, Y, ws):
     """Checked arguments of the FP8 expert stage: (Y, what has to live until the call is made, its arguments up to the stream)."""
     dev = _device(Xq, "Xq")
     T, D = Xq.shape
+    if ids.dim() != 2 or Wgu.dim() != 3:
+        raise ValueError(f"ids must be [T, k] and Wgu [E, 2F, D], got {tuple(ids.shape)} and {tuple(Wgu.shape)}")
     k = ids.shape[1]
-    E, F2 = Wgu.shape[0], Wgu.shape[1]
+    E, F2 = Wgu.shape[:2]
     F = F2 // 2
     kb = (D + 127) // 128
     if out_dtype not in _DTYPE:

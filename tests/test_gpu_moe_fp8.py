@@ -325,6 +325,10 @@ def test_refusals(q):
                              ("out_dtype", torch.float16, TypeError)]:
         with pytest.raises(error):
             q.moe_expert_stage_fp8(**{**good, name: bad})
+    for name, bad in [("ids", ids[:, 0].contiguous()), ("ids", ids[0, 0]), ("Wgu", Wgu[0]), ("Wgu", Wgu[0, 0]), ("Wgu", Wgu[:, :255].contiguous()),
+                      ("Wd", Wd[0]), ("Xs", Xs[:, 0].contiguous())]:
+        with pytest.raises(ValueError):
+            q.moe_expert_stage_fp8(**{**good, name: bad})
     for plan in ((1, 64, 1, 1), (0, 48, 1, 1), (0, 16, 3, 1), (0, 16, 1, 2), (0, 16, 0, 1), (0, 16, 1, 9)):   # (2 K blocks, 1)
         with pytest.raises(q.QmmError):
             q.qmm_dbg_moe_expert_stage_fp8(**good, plan=plan)
