@@ -154,15 +154,21 @@ __device__ __forceinline__ uint64_t swiglu2(uint64_t g2, uint64_t u2) {
 
 // The activations of the product's epilogue (qmm_act's order).  silu and tanh's gelu are v times
 // the logistic function of z: with t = exp(-|z|) <= 1, v / (1 + t), or v t / (1 + t) for negative
-// z: nothing overflows, and the fast exponential's error falls with t.  erf's gelu is v times the
-// normal distribution, whose tail is half of erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + p x)
-// (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26: within 1.5e-7): as exact as fp32
-// in the sum, a third of the instructions of erfcf, and no cancellation in the tail.
+// z: nothing overflows or cancels.  erf's gelu is v times the normal distribution, whose tail is
+// Phi(-x) = q(r) exp(-x^2 / 2), r = 1 / (1 + 5/16 x): q is r times a polynomial of degree 7 fitted to
+// Phi(-x) exp(x^2 / 2) so that its largest relative error on 0 <= x <= 14.4 (where v Phi(v) leaves 32 bits) is
+// least, 2.3e-7 with the coefficients in fp32 (found by linear programming at 1200 Chebyshev points).  So
+// a small negative result keeps its bits too; a formula within an absolute bound on erf would not do (one
+// of degree 5 within 1.5e-7 was 1e-2 off at v = -8).
+// Errors relative to the result, in units of 2^-24, for exact v: silu 16 + 3 |v|, gelu_tanh 16 + 9 |z| with
+// z = 2 sqrt(2 / pi) (v + 0.044715 v^3), gelu 32 + 2 v^2.  The first part is the reciprocals and products, the other
+// the exponential's argument: __expf is within 2 + 1.173 |argument| units of 2^-23, its rounded argument adds
+// the rest.  (An error of half a unit in v itself changes the results by as much.)
 // Columns n and n + 1 (n even) share a reciprocal, that of both denominators' product.
 // v or v t, and the denominator (finite also for a NaN or an infinity, which stay in their column)
 __device__ __forceinline__ float act_parts(float v, int act, float* d) {
     if (act == 3) {
-        *d = fminf(fmaf(0.23164190f, fabsf(v), 1.0f), 1e18f);   // 0.3275911 / sqrt 2
+        *d = fminf(fmaf(0.3125f, fabsf(v), 1.0f), 1e18f);
         return v;
     }
     const float z = act == 2 ? v : 1.5957691216f * v * fmaf(0.044715f * v, v, 1.0f);   // 2 sqrt(2 / pi) (v + 0.044715 v^3)
@@ -173,8 +179,14 @@ __device__ __forceinline__ float act_parts(float v, int act, float* d) {
 // The activation from these and the denominator's reciprocal.
 __device__ __forceinline__ float act_finish(float x, float r, int act) {
     if (act != 3) return x * r;
-    const float q = r * fmaf(r, fmaf(r, fmaf(r, fmaf(r, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
-    const float h = 0.5f * fminf(x, 1e18f) * (q * __expf(-0.5f * x * x));   // x Phi(-|x|)
+    float q = fmaf(r, 0.0353278928f, -0.135801405f);
+    q = fmaf(r, q, 0.140355065f);
+    q = fmaf(r, q, -0.00452047074f);
+    q = fmaf(r, q, 0.10540054f);
+    q = fmaf(r, q, 0.109672867f);
+    q = fmaf(r, q, 0.124903277f);
+    q = r * fmaf(r, q, 0.124662347f);
+    const float h = fminf(x, 1e18f) * (q * __expf(-0.5f * x * x));   // x Phi(-|x|)
     return x < 0.0f ? h : x - h;
 }
 __device__ __forceinline__ float reciprocal(float d) {

@@ -195,7 +195,9 @@ qmm_status qmm_fp8a8_swiglu_blk128(const uint8_t *Xq, const float *Xs, int M, in
  *   bias [N] fp32 or bf16, or NULL (bdt is then ignored);
  *   R [M] rows of ldr elements, fp32 or bf16, or NULL (ldr and rdt are then ignored); R may be
  *   Y (same type, ldr = N): the residual stream in place.  Other overlaps of R and Y are not allowed.
- *   Y [M][N] fp32 or bf16 (RNE).  Everything between the product and Y is fp32.
+ *   Y [M][N] fp32 or bf16 (RNE).  Everything between the product and Y is fp32; the activations' errors are
+ *   relative to their results, small negative ones too, in units of 2^-24 within: silu 16 + 3 |v|,
+ *   gelu 32 + 2 v^2, gelu_tanh 16 + 9 |z| with z = 2 sqrt(2/pi) (v + 0.044715 v^3).
  * Shapes as qmm_fp8a8_blk128; ldr >= N.
  */
 typedef enum {
