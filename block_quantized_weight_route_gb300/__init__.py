@@ -611,7 +611,9 @@ def moe_expert_stage_fp8(Xq, Xs, ids, w, Wgu, Sgu, Wd, Sd, R=None, out_dtype=tor
     Xq [T, D] E4M3 and Xs [T, ceil(D/128)] fp32 (as qmm_add_rmsnorm_fp8 gives them), ids int32 and
     w fp32 [T, k] (as moe_route_scored gives them), Wgu [E, 2F, D] (gate rows first) with Sgu [E, 2F/128,
     ceil(D/128)], Wd [E, D, F] with Sd [E, ceil(D/128), F/128], R [T, D] fp32 or bf16 (a row slice,
-    or Y itself).  ws: a uint8 tensor of moe_expert_stage_fp8_workspace_size bytes (default: allocated)."""
+    or Y itself).  ws: a uint8 tensor of moe_expert_stage_fp8_workspace_size bytes (default: allocated).
+    out_dtype float32 adds the experts' rows as 32-bit sums; with bfloat16 and many rows an expert they are
+    rounded to 11 bits first (2^-11 of a term at most), which shows only where terms and R cancel."""
     Y, keep, args = _stage_fp8_args(Xq, Xs, ids, w, Wgu, Sgu, Wd, Sd, R, out_dtype, Y, ws)
     st = lib().moe_expert_stage_fp8(*args, _raw_stream(Xq.get_device()))
     if st:
