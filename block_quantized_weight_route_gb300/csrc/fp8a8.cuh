@@ -226,7 +226,7 @@ __device__ __forceinline__ float activate_lanes(float v, int act) {
 
 // The bias of columns n .. n + 3 and the residual of row m there (past the end zeros), and
 // act(y + bias) + R.
-__device__ __forceinline__ float4 epilogue_bias(const Fp8a8Params& p, int n) {
+__device__ __forceinline__ float4 epilogue_bias(const Fp8a8EpilogueParams& p, int n) {
     float b[4] = {};
     if (p.bias && p.vec4 && n < p.N) return load4(p.bias, p.bias_bf16, n);
 #pragma unroll
@@ -234,7 +234,7 @@ __device__ __forceinline__ float4 epilogue_bias(const Fp8a8Params& p, int n) {
         if (p.bias && n + j < p.N) b[j] = load1(p.bias, p.bias_bf16, n + j);
     return make_float4(b[0], b[1], b[2], b[3]);
 }
-__device__ __forceinline__ float4 epilogue_residual(const Fp8a8Params& p, long m, int n) {
+__device__ __forceinline__ float4 epilogue_residual(const Fp8a8EpilogueParams& p, long m, int n) {
     float r[4] = {};
     if (p.R && p.vec4 && n < p.N) return load4(p.R, p.r_bf16, m * p.ldr + n);
 #pragma unroll
@@ -242,7 +242,7 @@ __device__ __forceinline__ float4 epilogue_residual(const Fp8a8Params& p, long m
         if (p.R && n + j < p.N) r[j] = load1(p.R, p.r_bf16, m * p.ldr + n + j);
     return make_float4(r[0], r[1], r[2], r[3]);
 }
-__device__ __forceinline__ float4 epilogue4(const Fp8a8Params& p, float4 y, float4 b, float4 r) {
+__device__ __forceinline__ float4 epilogue4(const Fp8a8EpilogueParams& p, float4 y, float4 b, float4 r) {
     y = add4(y, b);
     if (p.act) with_activation(p.act, [&](auto act) { y = act(y); });
     return add4(y, r);
@@ -281,7 +281,7 @@ __device__ __forceinline__ uint4 bf16x8(const uint64_t* v) {
 
 // A warp's staging for outputs: 32 rows x 128 bytes, 16-byte chunk c of row r at c ^ (r % 8) (no bank
 // conflicts on either side).  Copied to Y at (row0, col): eight lanes to a row.
-__device__ __forceinline__ void flush_aligned(const Fp8a8Params& p, const uint8_t* stg, int lane, long row0, int col, int esz) {
+__device__ __forceinline__ void flush_aligned(const Fp8a8Base& p, const uint8_t* stg, int lane, long row0, int col, int esz) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int r = i * 4 + lane / 8, c = lane % 8;
@@ -313,7 +313,7 @@ __device__ __forceinline__ void stage16(uint8_t* stg, int lane, int c0, const ui
 // odd element (4-byte stores are aligned) is shifted by one; the first and the last
 // element of such rows follow, a row per lane.
 template <bool BF16, int UNROLL>
-__device__ __forceinline__ void flush_ragged(const Fp8a8Params& p, const uint8_t* stg, int lane, long row0, int col) {
+__device__ __forceinline__ void flush_ragged(const Fp8a8Base& p, const uint8_t* stg, int lane, long row0, int col) {
     const int rows = p.M - (int)row0 < 32 ? p.M - (int)row0 : 32, cols = p.N - col;
     auto word = [&](int r, int i) { return reinterpret_cast<const uint32_t*>(stg + (r * 8 + ((i / 4) ^ (r & 7))) * 16)[i % 4]; };
     if constexpr (!BF16) {
@@ -346,7 +346,7 @@ __device__ __forceinline__ void flush_ragged(const Fp8a8Params& p, const uint8_t
 // ends are sectors written in part).  Ragged rows are copied UNROLL at a time, what the
 // kernel's registers allow.
 template <bool BF16, bool RAGGED, int UNROLL>
-__device__ __forceinline__ void store_columns(const Fp8a8Params& p, uint8_t* stg, int lane, long row0, int col,
+__device__ __forceinline__ void store_columns(const Fp8a8Base& p, uint8_t* stg, int lane, long row0, int col,
                                               const uint64_t* v) {
     constexpr int STEP = BF16 ? 64 : 32;
 #pragma unroll
@@ -364,7 +364,7 @@ __device__ __forceinline__ void store_columns(const Fp8a8Params& p, uint8_t* stg
 // zeros), and the residual's rows of the tile on theirs to L2: by threads 0 .. THREADS - 1, while the tile's
 // K blocks are folded.
 template <int BN, int ROWS, int THREADS>
-__device__ __forceinline__ void prefetch_epilogue(const Fp8a8Params& p, float* bias, int thread, long row0, int col0) {
+__device__ __forceinline__ void prefetch_epilogue(const Fp8a8EpilogueParams& p, float* bias, int thread, long row0, int col0) {
     if (p.bias) {
         const int esz = p.bias_bf16 ? 2 : 4;
         for (int x = thread * 16; x < BN * esz; x += THREADS * 16) {
@@ -394,7 +394,7 @@ __device__ __forceinline__ float4 widen4(uint2 w) {
                        __uint_as_float(w.y & 0xffff0000u));
 }
 template <bool BF16, class RT, class AT>
-__device__ __forceinline__ void finish_part(const Fp8a8Params& p, int lane, long row0, int n, float4 b, AT at) {
+__device__ __forceinline__ void finish_part(const Fp8a8EpilogueParams& p, int lane, long row0, int n, float4 b, AT at) {
     const bool in = n < p.N;
     RT r[8];
     const int nn = in ? n : 0;   // (what is past the end reads an element that exists)
@@ -426,7 +426,7 @@ __device__ __forceinline__ void finish_part(const Fp8a8Params& p, int lane, long
 // The loops over the parts are not unrolled, nor the activation's (but for two at once with nothing behind it):
 // the code, many times over, does not fit the instruction cache.
 template <bool BF16, bool VEC, int COLS, int CH>
-__device__ __forceinline__ void store_epilogue(const Fp8a8Params& p, uint8_t* stg, const float* bias, int bias0, int lane, long row0, int col0,
+__device__ __forceinline__ void store_epilogue(const Fp8a8EpilogueParams& p, uint8_t* stg, const float* bias, int bias0, int lane, long row0, int col0,
                                                const uint64_t* v) {
 #pragma unroll
     for (int c0 = 0; c0 < COLS; c0 += CH) {

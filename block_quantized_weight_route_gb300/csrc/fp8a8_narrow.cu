@@ -28,6 +28,8 @@
 // bytes and cluster sum, and from two waves of CTAs on a start for each.
 #include "fp8a8.cuh"
 
+#include <type_traits>
+
 namespace qmm {
 namespace {
 
@@ -35,6 +37,7 @@ template <int TN_, bool GATED_, bool EPI_ = false, bool GROUPED_ = false>
 struct NarrowCfg {
     static constexpr int TN = TN_, MATS = GATED_ ? 2 : 1;
     static constexpr bool GATED = GATED_, EPI = EPI_, GROUPED = GROUPED_, GATHER = GROUPED_ && GATED_, TOKENS_M = TN == 128;
+    using Params = std::conditional_t<GROUPED, Fp8a8Params, std::conditional_t<EPI, Fp8a8EpilogueParams, Fp8a8Base>>;
     static constexpr int W_BYTES = MATS * 128 * 128, X_BYTES = TN * 128, STAGE_BYTES = W_BYTES + X_BYTES;
     // Two CTAs on an SM where a stage (and a fold thread) is small: one's start and end run beside the other's
     // stream, and a product of few tiles is split over more CTAs (one token, 5120 x 5120:
@@ -90,7 +93,7 @@ __device__ __forceinline__ float4 cluster_sum(uint32_t local, int cs) {
 
 // The fold of a warp, weights on the M side: lane = weight row, `acc` the tokens.
 template <class C>
-__device__ __forceinline__ void fold_weights_m(const Fp8a8Params& p, int warp, int lane, int kb0, int kb1, uint32_t tmem_base,
+__device__ __forceinline__ void fold_weights_m(const Fp8a8Base& p, int warp, int lane, int kb0, int kb1, uint32_t tmem_base,
                                                const float* sc, float* sums, uint64_t* done, uint64_t* acc_empty,
                                                uint64_t* sc_full, uint64_t* sc_empty, volatile int* abort_flag) {
     constexpr int LD = 16;   // columns of a TMEM load
@@ -165,7 +168,7 @@ __device__ __forceinline__ void fold_weights_m(const Fp8a8Params& p, int warp, i
 
 // Tokens on the M side: lane = token, `acc` 32 weight rows (GATED: 32 gate, then 32 up).
 template <class C>
-__device__ __forceinline__ void fold_tokens_m(const Fp8a8Params& p, int warp, int lane, int kb0, int kb1, uint32_t tmem_base,
+__device__ __forceinline__ void fold_tokens_m(const Fp8a8Base& p, int warp, int lane, int kb0, int kb1, uint32_t tmem_base,
                                               const float* sc, float* sums, uint64_t* done, uint64_t* acc_empty,
                                               uint64_t* sc_full, uint64_t* sc_empty, volatile int* abort_flag) {
     constexpr int COLS = 32 * C::MATS, LD = C::GATED ? 16 : 32;   // sums of a thread; columns of a TMEM load
@@ -274,7 +277,7 @@ __device__ __forceinline__ int token_of(const Fp8a8Params& p, const int* own_til
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
-    fp8a8_narrow_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, Fp8a8Params p) {
+    fp8a8_narrow_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, typename C::Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stage = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* sums = reinterpret_cast<float*>(stage);               // afterwards: [mat][token][128 rows]
@@ -454,7 +457,8 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
 #pragma unroll
             for (int u = 0; u < ROWS; ++u) {
                 const int r = m0 + (lane + 32 * u) % C::TN;
-                rows[u] = C::GATHER ? token_of<C>(p, own_tile, m0, min(r, m_end - 1)) : r;
+                if constexpr (C::GATHER) rows[u] = token_of<C>(p, own_tile, m0, min(r, m_end - 1));
+                else rows[u] = r;
             }
             for (int kb = kb0; kb < kb1; kb += C::SC_KB) {
                 if (!mbar_wait(&sc_empty[slot], sph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_CONV_EMPTY)) break;
@@ -577,7 +581,7 @@ cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Para
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, fp8a8_narrow_kernel<C>, tx, tw, p);
+    return cudaLaunchKernelEx(&cfg, fp8a8_narrow_kernel<C>, tx, tw, static_cast<const typename C::Params&>(p));
 }
 
 }  // namespace

@@ -33,6 +33,8 @@
 // is near: without any fold the same loop reaches 3.0 PFLOP/s at clocks down to 1.6 GHz.
 #include "fp8a8.cuh"
 
+#include <type_traits>
+
 namespace qmm {
 namespace {
 
@@ -45,6 +47,7 @@ template <int BN_, bool GATED_, bool BF16_ = true, bool RAGGED_ = false, bool EP
 struct PairCfg {
     static constexpr int BN = BN_;
     static constexpr bool GATED = GATED_, RAGGED = RAGGED_, BF16 = BF16_, EPI = EPI_;
+    using Params = std::conditional_t<EPI, Fp8a8EpilogueParams, Fp8a8Base>;
     static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / 2 * 128, STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGING = EPI ? 8192 : 4096;   // of a fold warp, for its outputs
     // 160 KB of operands (256 columns to a product: 128 KB beside the 64 KB of staging, as fast)
@@ -85,7 +88,7 @@ struct PairTile {
 };
 
 template <class C>
-__device__ __forceinline__ PairTile pair_tile(const Fp8a8Params& p, int t, int crank) {
+__device__ __forceinline__ PairTile pair_tile(const Fp8a8Base& p, int t, int crank) {
     const int mt = t % p.m_tiles, nt = t / p.m_tiles;
     PairTile r;
     r.m0 = mt * 256 + crank * 128;
@@ -101,7 +104,7 @@ __device__ __forceinline__ uint32_t codes4(const GroupScale& gs, uint64_t a, uin
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
-    fp8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, Fp8a8Params p) {
+    fp8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, typename C::Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stage = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* outs = stage + C::STAGES * C::STAGE_BYTES;         // output staging of the fold warps
@@ -360,7 +363,8 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
                         break;
                     }
                     // (the slot's barrier completes with the bias too)
-                    if (C::EPI && kb == 0) prefetch_epilogue<C::BN, 128, 64>(p, sc + C::SC_FLOATS + (round & 3) * C::BN, l, ti.m0, ti.n0);
+                    if constexpr (C::EPI)
+                        if (kb == 0) prefetch_epilogue<C::BN, 128, 64>(p, sc + C::SC_FLOATS + (round & 3) * C::BN, l, ti.m0, ti.n0);
                     float* dst = sc + slot * C::SC_KB * C::SC_PITCH;
 #pragma unroll
                     for (int i = 0; i < 2 * C::SC_KB; ++i) {
@@ -394,7 +398,7 @@ __global__ void __launch_bounds__(C::THREADS) __maxnreg__(C::REGS)
 }
 
 template <class C>
-cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const Fp8a8Params& p, int sms, int dev, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& tx, const CUtensorMap& tw, const typename C::Params& p, int sms, int dev, cudaStream_t s) {
     static PerDevice most;   // pairs that fit the device at once
     cudaError_t e;
     int at_once = most.get(dev);

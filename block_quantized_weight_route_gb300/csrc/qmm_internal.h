@@ -151,8 +151,11 @@ struct MoeGroups {
     int tile_rows, max_tiles;
 };
 
-// FP8 x FP8 products with block scales (gemm_fp8a8.cu).
-struct Fp8a8Params {
+// FP8 x FP8 products with block scales (gemm_fp8a8.cu).  A kernel takes the fields that its form has and no more:
+// with those of the other forms beside them, which none of its code reads, two of the plain products' 256-column pair
+// kernels spill in their K loops (44 and 96 bytes stored; 5268 x 17408 x 5120 with fp32 output 487 us in place of
+// 355, 2048 x 5120 x 17407 285 in place of 165), and the others are 5% slower (364 us in place of 348 with bf16 output).
+struct Fp8a8Base {
     const uint8_t* Xq;   // [M][K] E4M3
     const float* Xs;     // [M][ceil(K/128)]
     const uint8_t* W;    // [N][K] E4M3; gated: [2N][K], gate rows first
@@ -165,7 +168,9 @@ struct Fp8a8Params {
     uint32_t* err;       // device error word
     int n_first, n_end;  // the launch's columns (n_first a multiple of 128)
     int m_tiles, n_tiles;
-    // y = act(y + bias[n]) + R[m][n]
+};
+// y = act(y + bias[n]) + R[m][n]
+struct Fp8a8EpilogueParams : Fp8a8Base {
     bool epilogue;
     int act;             // a qmm_act
     const void* bias;    // [N], or null
@@ -173,7 +178,9 @@ struct Fp8a8Params {
     long ldr;
     int bias_bf16, r_bf16;
     bool vec4;           // N and ldr are multiples of 4
-    // rows grouped by expert: W [E][N or 2N][K], S alike, M all rows
+};
+// rows grouped by expert: W [E][N or 2N][K], S alike, M all rows
+struct Fp8a8Params : Fp8a8EpilogueParams {
     const int4* tiles;   // {expert, first row, rows, 0}; null: not grouped
     const int* num_tiles;   // on the device
     int max_tiles;       // room in `tiles`
