@@ -1285,7 +1285,7 @@ static qmm_status moe_stage_fp8(const char* who, const uint8_t* Xq, const float*
                       : launch_fp8a8_narrow(tx, tw, p, gated, plan.tn, gated ? plan.cs_gate_up : plan.cs_down, d->index, stream);
         if (e != cudaSuccess) return cuda_fail(e, gated ? "moe_expert_stage_fp8: gate/up" : "moe_expert_stage_fp8: down");
     }
-    e = launch_moe_combine(y, y_unit, g.row, w, T, k, D, R, rdt == QMM_BF16, (long)ldr, Y, ydt == QMM_BF16, stream);
+    e = launch_moe_combine(y, y_unit, g.row, w, T, k, D, R, rdt == QMM_BF16, (long)ldr, Y, ydt == QMM_BF16, d->sms, stream);
     return e == cudaSuccess ? QMM_OK : cuda_fail(e, "moe_expert_stage_fp8: combine");
 }
 

@@ -13,9 +13,10 @@
 //   warps 4..11: fold, four for each half; warp w reads TMEM lanes 32 (w % 4) .. +31 (a row per lane)
 // Tiles of 128 rows rather than a CTA pair's 256, because an expert's last tile is half empty in the
 // mean: 42144 rows of 128 experts fill 84% of such tiles and 64% of the pair's.
-// What bounds it: a K block takes about 900 cycles, where the MMAs take 656 (82 each at N = 128), shared memory
-// 875 (48 KB in, 64 KB to the MMAs at 128 bytes a cycle) and each fold warp about 700 (two TMEM loads
-// of 64 columns and their latency, 64 packed FMAs); a tile's end takes 2300 cycles (down) to 3500 (gate/up) more,
+// What bounds it: shared memory.  A K block takes about 900 cycles, of which its 48 KB in and 64 KB to the MMAs (each
+// issuer reads the 16 KB of rows) at 128 bytes a cycle are 896; the MMAs take 656 (82 each at N = 128) and each
+// fold warp about 700 (two TMEM loads of 64 columns and their latency, 64 packed FMAs), which one issuer's 768 cycles
+// of shared memory do not hide either (N = 256 MMAs, 1% slower); a tile's end takes 2300 cycles (down) to 3500 (gate/up) more,
 // hidden in part because the halves of the columns drift apart.  With few rows an expert the weights' bytes bound it.
 // Measured (5268 tokens, D = 2048, F = 768, 128 experts, 8 a token): gate/up 151 us (1.76 PFLOP/s, tensor pipe 48%
 // active), down 95 us (1.39 PFLOP/s); 64 tokens: gate/up 65 us (6.0 TB/s), down 39 us (5.0 TB/s).

@@ -287,12 +287,12 @@ static cudaError_t combine(const void* y, const float* y_unit, const int32_t* ro
 }
 
 cudaError_t launch_moe_combine(const void* y, const float* y_unit, const int32_t* row, const float* w, int T, int k, int D, const void* R,
-                               int r_bf16, long ldr, void* Y, int y_bf16, cudaStream_t s) {
+                               int r_bf16, long ldr, void* Y, int y_bf16, int sms, cudaStream_t s) {
     // Where a block to a token would not fill the device (eight to an SM), its columns go to more
     // blocks: one after another their loads would be waited for in turn (a stage of 32 tokens 107.2 ->
     // 104.5 us, 301 tokens 130.3 -> 127.6).  With more tokens a block reads its rows' numbers once
     // (21504 tokens 1671 us, 1684 split).
-    if (T <= 8 * 152)
+    if (moe_combine_splits(T, sms))
         return y_unit ? combine<true, true>(y, y_unit, row, w, T, k, D, R, r_bf16, ldr, Y, y_bf16, s)
                       : combine<false, true>(y, nullptr, row, w, T, k, D, R, r_bf16, ldr, Y, y_bf16, s);
     return y_unit ? combine<true, false>(y, y_unit, row, w, T, k, D, R, r_bf16, ldr, Y, y_bf16, s)

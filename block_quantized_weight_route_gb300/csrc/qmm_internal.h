@@ -225,9 +225,11 @@ cudaError_t launch_fp8a8_pair(const CUtensorMap& tx, const CUtensorMap& tw, Fp8a
 cudaError_t launch_moe_group(const int32_t* ids, int P, int E, int k, const MoeGroups& g, int dev, cudaStream_t s);
 cudaError_t launch_moe_gather(const uint8_t* Xq, const float* Xs, int P, int D, const MoeGroups& g, int E, uint8_t* Xp, float* Xps,
                               int sms, cudaStream_t s);
+// Whether the combine's tokens are too few to fill the device with a block each (eight to an SM).
+inline bool moe_combine_splits(int T, int sms) { return T <= 8 * sms; }
 // (y_unit: y is fp16 in units of it, as launch_fp8a8_experts writes it; else fp32)
 cudaError_t launch_moe_combine(const void* y, const float* y_unit, const int32_t* row, const float* w, int T, int k, int D, const void* R, int r_bf16,
-                               long ldr, void* Y, int y_bf16, cudaStream_t s);
+                               long ldr, void* Y, int y_bf16, int sms, cudaStream_t s);
 
 // Routing by scores (route_scored.cu).
 struct ScoredParams {

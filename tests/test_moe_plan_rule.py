@@ -81,3 +81,15 @@ def test_the_answer_does_not_hang_on_the_one_before(rule):
     shapes = [(T, D, 768, E, k) for T in (1, 7, 301, 5268) for D in (2048, 2064) for E in (8, 128) for k in (2, 8)]
     first = [plan(rule, *s) for s in shapes]
     assert [plan(rule, *s) for s in reversed(shapes)] == first[::-1]
+
+
+def test_the_combine_goes_by_the_devices_sms(tmp_path):
+    src, lib = tmp_path / "combine.cpp", tmp_path / "combine.so"
+    src.write_text('#include "qmm_internal.h"\nextern "C" int splits(int T, int sms) { return qmm::moe_combine_splits(T, sms); }\n')
+    cuda = os.path.join(os.path.dirname(os.path.dirname(qbuild.nvcc())), "include")
+    r = subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-I", qbuild.CSRC, "-I", cuda, str(src), "-o", str(lib)],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    rule = ctypes.CDLL(str(lib))
+    for sms in (1, 76, 152):
+        assert [rule.splits(T, sms) for T in (1, 8 * sms, 8 * sms + 1)] == [1, 1, 0]
