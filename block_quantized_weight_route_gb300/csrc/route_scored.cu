@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_scored_kernel(const __grid_
     }
     if (lane < p.k) {
         p.ids[t * p.k + lane] = mine;
-        p.w[t * p.k + lane] = s * p.scale;
+        p.w[t * p.k + lane] = on ? s * p.scale : 0.0f;   // (0 whatever the scale)
     }
 }
 
