@@ -148,8 +148,9 @@ __device__ __forceinline__ uint64_t swiglu2(uint64_t g2, uint64_t u2) {
     const float d0 = 1.0f + t0, d1 = 1.0f + t1;
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d0 * d1));
-    const uint64_t n = mul2(mul2(g2, pack2(g.x < 0.0f ? t0 : 1.0f, g.y < 0.0f ? t1 : 1.0f)), u2);
-    return mul2(n, mul2(pack2(r, r), pack2(d1, d0)));
+    // (u last: g u may be past the largest number where h is not)
+    const uint64_t n = mul2(g2, pack2(g.x < 0.0f ? t0 : 1.0f, g.y < 0.0f ? t1 : 1.0f));
+    return mul2(mul2(n, mul2(pack2(r, r), pack2(d1, d0))), u2);
 }
 
 // The activations of the product's epilogue (qmm_act's order).  silu and tanh's gelu are v times
