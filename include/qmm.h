@@ -252,8 +252,8 @@ qmm_status moe_route_scored(const void *logits, qmm_dtype ldt, int64_t ldl, cons
  *   With ydt QMM_F32 every y_tj is the product's fp32 sum.  With QMM_BF16 and many rows an expert (by estimated
  *   time, from the shape alone; qmm_dbg_moe_fp8_plan's `many`) y_tj is first rounded to 11 significant bits:
  *   off by at most 2^-11 of itself, or 2^-39 of the largest of its 64 columns (64 c .. 64 c + 63) where that
- *   is more.  So Y is then within sum_j |w y_tj| 2^-11 before its own rounding: more than that
- *   rounding (2^-8 of Y) where the terms and R cancel to less than an eighth of their size.
+ *   is more.  Before its own rounding Y is then off by at most sum_j |w[t][j]| times that: more than
+ *   that rounding (2^-8 of Y) only where terms and R cancel to less than an eighth of the terms' size.
  *   A pair whose id is outside [0, E) (a router's -1) adds nothing, whatever its weight; a
  *   token may name an expert more than once.
  *   Xq [T][D] E4M3, Xs [T][ceil(D/128)] fp32 (as qmm_add_rmsnorm_fp8 writes them);
